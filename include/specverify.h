@@ -279,6 +279,131 @@ int sv_residual_add(uint16_t* h, int ldh, const uint16_t* t, int ldt, int M, int
 int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int I, uint16_t* s, int lds,
               void* stream);
 
+/* ---------------------------------------------------- attention of a round ---
+ * The steps between a layer's q | k | v projection and its o projection, for
+ * targets that attend over a KV cache (wiki page, "Architecture": the target
+ * verifies the whole drafted block in one forward over its cache; the pages
+ * give no layer internals, so head norms, rotation and cache layout are the
+ * usual ones of the target family).  Order of use per layer and round:
+ *   sv_qmm_run (q|k|v) -> sv_qk_norm_rope -> sv_kv_append -> sv_tree_attention
+ *   -> sv_qmm_run (o, residual),
+ * then, once per round after the accept step, sv_kv_commit over all layers
+ * when the drafts were a tree (a chain's accepted rows are already in place),
+ * and kv_len[b] += accepted rows.
+ *
+ * B requests stack their rows: row_offsets is a HOST array int32 [B+1]
+ * starting at 0, request b owns rows row_offsets[b] .. row_offsets[b+1] - 1
+ * (none is allowed), 1 <= B <= 256.  Rows from row_offsets[B] on are neither
+ * read nor written.
+ *
+ * sv_qk_norm_rope: per row and head x (bf16 [head_dim], the heads of a row
+ * adjacent), with w = q_weight or k_weight (bf16 [head_dim], NULL = 1):
+ *   x <- x / sqrt(mean(x^2) + eps) * w                         (norm != 0)
+ *   (x_i, x_j) <- (x_i cos a - x_j sin a, x_j cos a + x_i sin a),
+ *   a = positions[row] * inv_freq[p],  p = 0 .. rotary_dim/2 - 1,
+ * with the pair (i, j) = (p, p + rotary_dim/2), or (2p, 2p + 1) when
+ * interleaved != 0; elements from rotary_dim on are not rotated.  The angle is
+ * formed in fp64 and reduced to one turn before its sine and cosine, the rest
+ * is fp32, and each output is rounded to bf16 once.  positions int32 [rows],
+ * inv_freq fp32 [rotary_dim/2] (both may be NULL when rotary_dim == 0).
+ * q_out may be q (same stride) and k_out may be k: each head is read whole
+ * before it is written; other overlap is not allowed.  n_kv_heads == 0 skips
+ * k.  head_dim a multiple of 8 up to 256, rotary_dim a multiple of 16 up to
+ * head_dim, rows <= 2^20.  Strides are in elements; 16-byte aligned buffers
+ * with strides that are multiples of 8 take wide accesses, others are
+ * accepted.
+ *
+ * sv_kv_cache: one layer's cache, paged.  Page p, head h, place i hold one
+ * token's key or value:
+ *   bits == 16: k, v are bf16 [n_pages, n_kv_heads, page_size, head_dim];
+ *   bits 8 or 4: k, v are uint32 words [n_pages, n_kv_heads, page_size,
+ *     head_dim*bits/32], the weight format's packing (least significant field
+ *     first), with fp16 scales and biases [n_pages, n_kv_heads, page_size,
+ *     head_dim/64] per group of 64; the value is scale*code + bias.
+ * All pointers 16-byte aligned; page_size a power of two, 16 .. 65536;
+ * head_dim a multiple of 64 up to 256; n_kv_heads 1 .. 256; bits 4, 8 or 16.
+ * Where a request's tokens are: position t of request b is place t % page_size
+ * of page block_table[b*table_pages + t/page_size].  block_table int32
+ * [B, table_pages] and kv_len int32 [B] are DEVICE arrays, read when the call
+ * runs; table_pages*page_size <= 2^30.  Entries past a request's last used
+ * page are not read.  A page outside [0, n_pages), a negative kv_len, or a
+ * position past the table sets the bad-input bit that sv_device_error()
+ * reports: sv_kv_append and sv_kv_commit then write nothing for the rows or
+ * the request concerned, sv_kv_read leaves their output rows as they were,
+ * and sv_tree_attention's output for that request is undefined (no access
+ * leaves the arrays).  Two requests may share pages that none of them writes.
+ *
+ * sv_kv_append writes row i of request b (k, v bf16 [rows, n_kv_heads*head_dim],
+ * strides ldk, ldv) at position kv_len[b] + i.  Quantization of a group
+ * (bits 8, 4): inputs clamped to +-65280 (so every value dequantizes inside
+ * fp16's range), lo and hi their extremes,
+ *   scale = fp16(fp32(hi - lo) / (2^bits - 1)),  bias = fp16(lo),
+ *   code = rint(fp32(x - bias) / scale) (ties to even), clamped to the codes,
+ * every step rounded to fp32; scale == 0 gives code 0.  A NaN makes its
+ * whole group read as NaN.  kv_len is not changed.
+ * sv_kv_read is the reverse: positions first[b] + i (first int32 [B], DEVICE)
+ * to row i of request b of k and v, bf16 (scale*code + bias in one fp32
+ * multiply-add, then rounded).
+ * In both, k and v rows need 2-byte alignment only; 16-byte aligned buffers
+ * with strides that are multiples of 8 take wide accesses.  Rows <= 2^22.
+ *
+ * sv_tree_attention: row i of request b (0 <= i < m_b <= 64) attends to the
+ * m_b drafted rows' keys and values at positions kv_len[b] .. kv_len[b]+m_b-1
+ * (written by sv_kv_append before) as its mask allows and to every position
+ * before them:
+ *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max),
+ * t visible iff t < kv_len[b] or bit t - kv_len[b] of tree_mask[row] is set
+ * (tree_mask uint64 [rows], DEVICE: a row's ancestors and normally itself;
+ * bits from m_b on are ignored; NULL = a chain, bits 0 .. i).  A row that sees
+ * nothing, or only scores of -inf, gets zeros.  What a row does not see does
+ * not reach it, infinities and NaN included; a visible value of +-inf gives
+ * +-inf or NaN.  q and out bf16 [rows, n_q_heads*head_dim] (strides ldq, ldo);
+ * query head h reads key head h / (n_q_heads / n_kv_heads).  One row (m = 1)
+ * is the plain decode step.  scale is finite.  head_dim 64 or 128
+ * (SV_EUNSUPPORTED otherwise), n_q_heads a multiple of n_kv_heads and at most
+ * 64 times as many.  q and out 16-byte aligned, strides multiples of 8.
+ * Softmax statistics and sums are fp32; the probabilities enter the second
+ * product in 16 bits.  The result does not depend on timing: it is bitwise
+ * reproducible for given inputs on one device.
+ * Workspace: sv_tree_attention_workspace_bytes (0 for a bad argument), 256-byte
+ * aligned, no zero fill, free for other use once the call has run.
+ *
+ * sv_kv_commit: after the accept step, request b keeps path_len[b] of its
+ * drafted rows, namely rows path[b*max_path + j], j = 0 .. path_len[b] - 1,
+ * strictly increasing in [0, 64) (a root-to-leaf path of the tree in
+ * topological order; the anchor is row 0).  Moves what position kv_len[b] +
+ * path[j] holds to position kv_len[b] + j, codes, scales and biases as they
+ * are, in each of n_layers caches (a HOST array; same sizes and bits, n_layers
+ * <= 1024) that share the block table.  path, path_len int32, DEVICE;
+ * 1 <= max_path <= 64.  A path that is not increasing or out of range is bad
+ * input (above). */
+typedef struct {
+  void* k;
+  void* v;
+  uint16_t* k_scales;
+  uint16_t* k_biases;
+  uint16_t* v_scales;
+  uint16_t* v_biases;
+  int n_pages, page_size, n_kv_heads, head_dim, bits;
+} sv_kv_cache;
+
+int sv_qk_norm_rope(const uint16_t* q, int ldq, const uint16_t* k, int ldk, int rows, int n_q_heads, int n_kv_heads,
+                    int head_dim, int norm, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                    const int32_t* positions, const float* inv_freq, int rotary_dim, int interleaved, uint16_t* q_out,
+                    int ldqo, uint16_t* k_out, int ldko, void* stream);
+int sv_kv_append(const sv_kv_cache* cache, int B, const int32_t* row_offsets, const int32_t* kv_len,
+                 const int32_t* block_table, int table_pages, const uint16_t* k, int ldk, const uint16_t* v, int ldv,
+                 void* stream);
+int sv_kv_read(const sv_kv_cache* cache, int B, const int32_t* row_offsets, const int32_t* first,
+               const int32_t* block_table, int table_pages, uint16_t* k, int ldk, uint16_t* v, int ldv, void* stream);
+size_t sv_tree_attention_workspace_bytes(const sv_kv_cache* cache, int B, const int32_t* row_offsets, int n_q_heads);
+int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offsets, const int32_t* kv_len,
+                      const int32_t* block_table, int table_pages, const uint16_t* q, int ldq, int n_q_heads, float scale,
+                      const uint64_t* tree_mask, uint16_t* out, int ldo, void* workspace, size_t workspace_bytes,
+                      void* stream);
+int sv_kv_commit(const sv_kv_cache* layers, int n_layers, int B, const int32_t* kv_len, const int32_t* block_table,
+                 int table_pages, const int32_t* path, int max_path, const int32_t* path_len, void* stream);
+
 /* --------------------------------------------------------- verify round ---
  * One whole verify round of a dense target whose every linear layer is
  * group-quantized (wiki page, "Architecture": the target runs [anchor] + m

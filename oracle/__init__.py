@@ -24,6 +24,8 @@ printed on the source pages):
 * ``philox`` - Philox-4x32-10 (Salmon et al., SC'11) for the uniforms that
   drive sampled acceptance.
 * ``glue``   - RMSNorm, residual add and SwiGLU between projections.
+* ``attention`` - head norms with rotary positions, the paged cache's quantizer,
+  tree-masked attention and the commit of an accepted path [reading].
 * ``chain``  - one verify round of a dense decoder stack built from the above.
 * ``cap``    - the draft-cap choice from measured verify costs and a live
   acceptance estimate (PyPI page, "The Apple-Silicon speedup ceiling";
@@ -34,4 +36,4 @@ where the pages are silent and a plain reading was taken is marked
 "[reading]".
 """
 
-from . import quant, qmm, accept, philox, glue, chain, cap  # noqa: F401
+from . import quant, qmm, accept, philox, glue, attention, chain, cap  # noqa: F401

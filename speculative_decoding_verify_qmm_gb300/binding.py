@@ -44,6 +44,38 @@ class Model(ctypes.Structure):
 
 _c_model_p = ctypes.POINTER(Model)
 
+
+class KVCacheView(ctypes.Structure):
+    """sv_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("k_biases", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("v_biases", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("bits", ctypes.c_int)]
+
+
+_c_kv_p = ctypes.POINTER(KVCacheView)
+
+
+class KVCache:
+    """One layer's paged cache: its tensors (kept alive here) and the sv_kv_cache over them."""
+
+    def __init__(self, view, tensors):
+        self.view, self.tensors, self.ref = view, tensors, ctypes.byref(view)
+        self.k, self.v = tensors[0], tensors[1]
+        self.device = self.k.device
+        self.width = view.n_kv_heads * view.head_dim
+
+
+class KVLayers:
+    """The caches of several layers as one host array of sv_kv_cache."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches or any(c.device != self.caches[0].device for c in self.caches):
+            raise SVError(SV_EINVAL, "the layers' caches must be on one device, and at least one")
+        self.array = (KVCacheView * len(self.caches))(*[c.view for c in self.caches])
+        self.device = self.caches[0].device
+
 SV_CAP_MAX = 31
 
 
@@ -114,6 +146,18 @@ _SIGNATURES = {
     "sv_gather_qmm": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p,
                                _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
                                _c_size_t, _c_void_p]),
+    "sv_qk_norm_rope": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                 _c_void_p, _c_void_p, _c_float, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p,
+                                 _c_int, _c_void_p, _c_int, _c_void_p]),
+    "sv_kv_append": (_c_int, [_c_kv_p, _c_int, _c_i32_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                              _c_int, _c_void_p]),
+    "sv_kv_read": (_c_int, [_c_kv_p, _c_int, _c_i32_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                            _c_int, _c_void_p]),
+    "sv_tree_attention_workspace_bytes": (_c_size_t, [_c_kv_p, _c_int, _c_i32_p, _c_int]),
+    "sv_tree_attention": (_c_int, [_c_kv_p, _c_int, _c_i32_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_int,
+                                   _c_float, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    "sv_kv_commit": (_c_int, [_c_kv_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                              _c_void_p]),
     "sv_expected_committed": (ctypes.c_double, [ctypes.c_double, _c_int]),
     "sv_best_cap": (_c_int, [ctypes.c_double, _c_int, _c_f64_p, _c_f64_p, ctypes.c_double, _c_int_p, _c_f64_p]),
     "sv_verify_knee": (_c_int, [_c_f64_p, _c_int, ctypes.c_double, _c_int_p]),
@@ -213,6 +257,30 @@ def _stream(stream):
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _tensors(device, dtype, *tensors):
+    """Refuse tensors that the C side would read as something else."""
+    for t in tensors:
+        if t.dtype != dtype or t.device != device:
+            raise SVError(SV_EINVAL, "expected a %s tensor on %s, got %s on %s" % (dtype, device, t.dtype, t.device))
+
+
+def _rows(name, t, rows, width):
+    """Refuse anything but a [>= rows, >= width] matrix with adjacent elements; returns its row stride."""
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width or (t.stride(1) != 1 and width > 1):
+        raise SVError(SV_EINVAL, "%s must be a [%d, %d] matrix with unit inner stride, got %s with strides %s"
+                      % (name, rows, width, tuple(t.shape), t.stride()))
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+def _launch_stream(stream, device):
+    """Raw handle of the stream to launch on; the tensors' device must be the current one."""
+    import torch
+    here = torch.cuda.current_device()
+    if device.type != "cuda" or device.index != here:
+        raise SVError(SV_EINVAL, "tensors on %s, current device cuda:%d" % (device, here))
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
 
 class Library:
@@ -491,6 +559,179 @@ class Library:
         self.check(self.lib.sv_rmsnorm(_ptr(x), x.stride(0), x.shape[0], x.shape[1], _ptr(weight), eps, _ptr(y),
                                        y.stride(0), _stream(stream)))
         return y
+
+    # ------------------------------------------------------------ attention
+    @staticmethod
+    def row_offsets(offsets):
+        """Host row offsets [B + 1] as the C calls take them (lists are accepted too, at some cost a call)."""
+        return offsets if isinstance(offsets, ctypes.Array) else (ctypes.c_int32 * len(offsets))(
+            *[int(v) for v in offsets])
+
+    @staticmethod
+    def kv_cache(k, v, k_scales=None, k_biases=None, v_scales=None, v_biases=None):
+        """A KVCache over device tensors: k, v bf16 [pages, heads, page, dim], or int32 words
+        [pages, heads, page, dim * bits / 32] with fp16 scales and biases [pages, heads, page, dim / 64]."""
+        import torch
+        side = [t for t in (k_scales, k_biases, v_scales, v_biases) if t is not None]
+        if k.dim() != 4 or k.shape != v.shape or k.device.type != "cuda" or len(side) not in (0, 4):
+            raise SVError(SV_EINVAL, "k and v must be equal 4-d CUDA tensors, scales and biases all given or none")
+        pages, heads, page, last = k.shape
+        if side:
+            _tensors(k.device, torch.int32, k, v)
+            _tensors(k.device, torch.float16, *side)
+            dim = side[0].shape[-1] * 64
+            bits = last * 32 // dim if dim else 0
+            if any(tuple(t.shape) != (pages, heads, page, dim // 64) for t in side) or last * 32 != dim * bits:
+                raise SVError(SV_EINVAL, "scales and biases must be [pages, heads, page, dim / 64]")
+        else:
+            _tensors(k.device, torch.bfloat16, k, v)
+            dim, bits = last, 16
+        if not all(t.is_contiguous() for t in [k, v] + side):
+            raise SVError(SV_EINVAL, "cache tensors must be contiguous")
+        ptrs = [t.data_ptr() for t in side] or [None] * 4
+        return KVCache(KVCacheView(k.data_ptr(), v.data_ptr(), *ptrs, pages, page, heads, dim, bits), [k, v] + side)
+
+    def kv_cache_alloc(self, n_pages, page_size, n_kv_heads, head_dim, bits, device="cuda"):
+        """A zero-filled cache (torch allocates it)."""
+        import torch
+        shape = (n_pages, n_kv_heads, page_size)
+        zeros = lambda last, dtype: torch.zeros(shape + (last,), dtype=dtype, device=device)  # noqa: E731
+        if bits == 16:
+            return self.kv_cache(zeros(head_dim, torch.bfloat16), zeros(head_dim, torch.bfloat16))
+        return self.kv_cache(zeros(head_dim * bits // 32, torch.int32), zeros(head_dim * bits // 32, torch.int32),
+                             *[zeros(head_dim // 64, torch.float16) for _ in range(4)])
+
+    @staticmethod
+    def kv_layers(caches):
+        return KVLayers(caches)
+
+    def qk_norm_rope(self, q, k, head_dim, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                     norm=True, interleaved=False, q_out=None, k_out=None, stream=None):
+        """(q_out, k_out).  q [rows, q_heads * head_dim], k [rows, kv_heads * head_dim] or None; the
+        rotary width is 2 * len(inv_freq) (no rotation without it); q_out = q works in place."""
+        import torch
+        rows, dev = q.shape[0], q.device
+        if q_out is None:
+            q_out = torch.empty((rows, q.shape[1]), dtype=q.dtype, device=dev)
+        mats = [("q", q), ("q_out", q_out)]
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((rows, k.shape[1]), dtype=k.dtype, device=dev)
+            mats += [("k", k), ("k_out", k_out)]
+        _tensors(dev, torch.bfloat16, *[m for _, m in mats], *[w for w in (q_weight, k_weight) if w is not None])
+        for w in (q_weight, k_weight):
+            if w is not None and (w.numel() != head_dim or not w.is_contiguous()):
+                raise SVError(SV_EINVAL, "a norm weight must be a contiguous [%d] tensor" % head_dim)
+        ld = [_rows(name, m, rows, (k if name[0] == "k" else q).shape[1]) for name, m in mats] + [0, 0]
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.numel()
+            _tensors(dev, torch.float32, inv_freq)
+            _tensors(dev, torch.int32, positions)
+            if positions.numel() < rows or not positions.is_contiguous() or not inv_freq.is_contiguous():
+                raise SVError(SV_EINVAL, "positions must be a contiguous [rows] tensor, inv_freq contiguous")
+        if head_dim < 1 or q.shape[1] % head_dim or (k is not None and k.shape[1] % head_dim):
+            raise SVError(SV_EINVAL, "q and k widths must be multiples of head_dim")
+        opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        if rows:
+            self.check(self.lib.sv_qk_norm_rope(
+                q.data_ptr(), ld[0], opt(k), ld[2], rows, q.shape[1] // head_dim,
+                0 if k is None else k.shape[1] // head_dim, head_dim, 1 if norm else 0, opt(q_weight), opt(k_weight), eps,
+                positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, rot,
+                1 if interleaved else 0, q_out.data_ptr(), ld[1], opt(k_out), ld[3], _launch_stream(stream, dev)))
+        return q_out, k_out
+
+    @staticmethod
+    def _sequences(device, offs, lens, table):
+        """Checks of the arrays that place requests in the cache; returns (B, rows, table width)."""
+        import torch
+        B = len(offs) - 1
+        _tensors(device, torch.int32, lens, table)
+        if table.dim() != 2 or table.shape[0] < B or lens.numel() < B or not table.is_contiguous() \
+                or not lens.is_contiguous():
+            raise SVError(SV_EINVAL, "block_table must be a contiguous [B, pages] tensor and the lengths [B], B = %d" % B)
+        return B, offs[B], table.shape[1]
+
+    def kv_append(self, cache, row_offsets, kv_len, block_table, k, v, stream=None):
+        """Rows of k and v [rows, kv_heads * head_dim] into the cache at kv_len[b], kv_len[b] + 1, ..."""
+        import torch
+        offs = self.row_offsets(row_offsets)
+        B, rows, pages = self._sequences(cache.device, offs, kv_len, block_table)
+        _tensors(cache.device, torch.bfloat16, k, v)
+        if rows:
+            self.check(self.lib.sv_kv_append(
+                cache.ref, B, offs, kv_len.data_ptr(), block_table.data_ptr(), pages, k.data_ptr(),
+                _rows("k", k, rows, cache.width), v.data_ptr(), _rows("v", v, rows, cache.width),
+                _launch_stream(stream, cache.device)))
+
+    def kv_read(self, cache, row_offsets, first, block_table, k=None, v=None, stream=None):
+        """(k, v) bf16 [rows, kv_heads * head_dim]: row i of request b from position first[b] + i."""
+        import torch
+        offs = self.row_offsets(row_offsets)
+        B, rows, pages = self._sequences(cache.device, offs, first, block_table)
+        if k is None:
+            k = torch.empty((rows, cache.width), dtype=torch.bfloat16, device=cache.device)
+        if v is None:
+            v = torch.empty((rows, cache.width), dtype=torch.bfloat16, device=cache.device)
+        _tensors(cache.device, torch.bfloat16, k, v)
+        if rows:
+            self.check(self.lib.sv_kv_read(
+                cache.ref, B, offs, first.data_ptr(), block_table.data_ptr(), pages, k.data_ptr(),
+                _rows("k", k, rows, cache.width), v.data_ptr(), _rows("v", v, rows, cache.width),
+                _launch_stream(stream, cache.device)))
+        return k, v
+
+    def tree_attention_workspace_bytes(self, cache, row_offsets, n_q_heads):
+        offs = self.row_offsets(row_offsets)
+        return self.lib.sv_tree_attention_workspace_bytes(cache.ref, len(offs) - 1, offs, n_q_heads)
+
+    def tree_attention(self, cache, row_offsets, kv_len, block_table, q, n_q_heads, scale=None, tree_mask=None, out=None,
+                       workspace=None, stream=None):
+        """out bf16 [rows, q_heads * head_dim]; tree_mask int64 [rows] (bit j: the row sees the request's
+        drafted row j), None for a chain; scale defaults to head_dim ** -0.5."""
+        import torch
+        offs = self.row_offsets(row_offsets)
+        dev = cache.device
+        B, rows, pages = self._sequences(dev, offs, kv_len, block_table)
+        width = n_q_heads * cache.view.head_dim
+        if out is None:
+            out = torch.empty((q.shape[0], width), dtype=torch.bfloat16, device=dev)
+        _tensors(dev, torch.bfloat16, q, out)
+        if tree_mask is not None:
+            _tensors(dev, torch.int64, tree_mask)
+            if tree_mask.numel() < rows or not tree_mask.is_contiguous():
+                raise SVError(SV_EINVAL, "tree_mask must be a contiguous [rows] tensor")
+        ldq, ldo = _rows("q", q, rows, width), _rows("out", out, rows, width)
+        if workspace is None:
+            workspace = torch.empty(max(256, self.tree_attention_workspace_bytes(cache, offs, n_q_heads)),
+                                    dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)  # the call outlives this tensor on that stream
+        elif workspace.device != dev:
+            raise SVError(SV_EINVAL, "workspace on %s, cache on %s" % (workspace.device, dev))
+        if rows:
+            self.check(self.lib.sv_tree_attention(
+                cache.ref, B, offs, kv_len.data_ptr(), block_table.data_ptr(), pages, q.data_ptr(), ldq, n_q_heads,
+                cache.view.head_dim ** -0.5 if scale is None else scale,
+                None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(), ldo, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), _launch_stream(stream, dev)))
+        return out
+
+    def kv_commit(self, caches, kv_len, block_table, path, path_len, stream=None):
+        """Move the drafted rows path[b, :path_len[b]] (int32) to the front of request b's drafted region, in
+        every cache of `caches` (a list of KVCache, or kv_layers() of one)."""
+        import torch
+        layers = caches if isinstance(caches, KVLayers) else KVLayers(caches)
+        dev = layers.device
+        _tensors(dev, torch.int32, kv_len, block_table, path, path_len)
+        B = kv_len.numel()
+        if block_table.dim() != 2 or path.dim() != 2 or block_table.shape[0] < B or path.shape[0] < B \
+                or path_len.numel() < B or not (block_table.is_contiguous() and path.is_contiguous()
+                                                and kv_len.is_contiguous() and path_len.is_contiguous()):
+            raise SVError(SV_EINVAL, "block_table [B, pages], path [B, n] and path_len [B] must be contiguous, B = %d" % B)
+        self.check(self.lib.sv_kv_commit(
+            layers.array, len(layers.array), B, kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+            path.data_ptr(), path.shape[1], path_len.data_ptr(), _launch_stream(stream, dev)))
 
     def residual_add(self, h, t, stream=None):
         self.check(self.lib.sv_residual_add(_ptr(h), h.stride(0), _ptr(t), t.stride(0), h.shape[0], h.shape[1],
