@@ -137,6 +137,21 @@ int encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
   return SV_OK;
 }
 
+// A [n2][n1][n0] tensor without gaps, in boxes of box0 x box1 x 1 with the 128-byte swizzle.
+int encode_tiled_3d_sw128(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t n0, uint64_t n1,
+                          uint64_t n2, uint64_t elem_bytes, uint32_t box0, uint32_t box1) {
+  auto fn = encode_fn();
+  if (!fn) return fail(SV_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {n0, n1, n2};
+  const cuuint64_t strides[2] = {n0 * elem_bytes, n0 * n1 * elem_bytes};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SV_ECUDA, "cuTensorMapEncodeTiled (cache) failed (CUresult %d)", (int)r);
+  return SV_OK;
+}
+
 // Codes as a 3D view (byte within a 128-byte piece, row, piece) so that one
 // copy brings all pieces of a stage: shared memory receives [piece][row][128 B]
 // with the 128-byte swizzle, the layout the consumers read.

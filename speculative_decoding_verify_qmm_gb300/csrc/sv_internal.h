@@ -110,6 +110,8 @@ int encode_weight_maps(CUtensorMap (&out)[3], const void* wq, const void* scales
 int fail(int status, const char* fmt, ...);
 int encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
                     uint64_t stride1_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw);
+int encode_tiled_3d_sw128(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t n0, uint64_t n1,
+                          uint64_t n2, uint64_t elem_bytes, uint32_t box0, uint32_t box1);
 // The wide-block matmul (33 <= M <= 512, tcgen05): workspace size and launch.
 size_t wide_bytes(int M, int N, int K, int bits);
 int wide_qmm(const uint32_t* wq, const uint16_t* scales, const uint16_t* biases, int N, int K, int bits,
