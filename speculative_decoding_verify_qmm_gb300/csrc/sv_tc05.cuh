@@ -63,14 +63,22 @@ __device__ __forceinline__ void tc05_mma_f16(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 // The same with the A operand in tensor memory: lane = row, each 32-bit column holds two adjacent k.
-__device__ __forceinline__ void tc05_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// The descriptor of B comes as its low and high words.
+__device__ __forceinline__ void tc05_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                                 bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
 }
 // Arrive (count 1) on an mbarrier once every tcgen05.mma this thread issued has completed.
 __device__ __forceinline__ void tc05_commit(uint64_t* bar) {
@@ -78,13 +86,11 @@ __device__ __forceinline__ void tc05_commit(uint64_t* bar) {
                : "memory");
 }
 
-// Descriptor of an MN-major operand in the 128-byte swizzle: one k is 64 adjacent elements (128 bytes), 8 k make a
-// 1024-byte group (the stride byte offset), and the next 64 elements of the other dimension lie `block` bytes on (the
-// leading byte offset).  A k-step of 16 advances the start address by 2048 bytes.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem_addr, uint32_t block) {
-  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// Words of such a descriptor.  Low: start address >> 4 (bits 0-13), leading byte offset >> 4 (16-29).  High: stride
+// byte offset >> 4 (0-13), version 1 (14), swizzle mode 2 = 128 bytes (29-31).
+// An MN-major operand in the 128-byte swizzle: one k is 64 adjacent elements (128 bytes), 8 k make a 1024-byte group
+// (the stride byte offset), and the next 64 elements of the other dimension lie the leading byte offset on.  A k-step
+// of 16 advances the start address by 2048 bytes.
 
 // Instruction descriptor of kind::f16 for fp16 or bf16 operands (both the same type: formats 0 or 1), fp32
 // accumulators; b_mn: B is MN-major (bit 16).

@@ -44,30 +44,25 @@ namespace sv {
 
 constexpr int TA_TILE = 128;                       // tokens per tile
 constexpr int TA_ROWS = 128;                       // rows per block: the lanes of tensor memory
-constexpr int TA_SOFT = 4, TA_XF = 8;              // softmax warps (0-3), transforming warps (4-11)
-constexpr int TA_PROD = TA_SOFT + TA_XF, TA_MMA = TA_PROD + 1;
-constexpr int TA_THREADS = (TA_MMA + 1) * 32;
+constexpr int TA_SOFT = 4, TA_TEAM = 4;            // softmax warps (0-3); warps of a transforming team
 constexpr int TA_PAD = 36;                         // floats per scratch row of 32 (16-byte aligned, conflict-free)
 constexpr int TA_FLAGS = 16;                       // segments whose flags are alive at once (ring depth / 2 at most)
 // tensor-memory columns
-constexpr uint32_t TA_S = 0, TA_O = 256, TA_P = 384, TA_Q = 448;
+constexpr uint32_t TA_S = 0, TA_O = 256, TA_Q = 384;  // two S buffers, each overwritten by its P; O; Q
 constexpr float TA_BIAS = 8.f, TA_GROW = 14.f;     // weights start at 2^8 at most and may grow to 2^14
 
+// Warps: softmax, transforming teams, the copying warp (16-bit caches), the MMA warp.
 template <int D, int BITS>
 struct TaShape {
+  static constexpr int TEAMS = BITS == 16 ? 1 : 3;
+  static constexpr int PROD = TA_SOFT + TEAMS * TA_TEAM, MMA = PROD + 1, THREADS = (MMA + 1) * 32;
   static constexpr int OP = TA_TILE * D * 2;                                       // one operand tile, 16 bits a value
-  static constexpr int CODES = BITS == 16 ? 0 : TA_TILE * D * BITS / 8;            // one raw tile
-  static constexpr int SIDE = BITS == 16 ? 0 : TA_TILE * (D / GROUP) * 2;          // its scales; its biases
-  static constexpr int RAW = CODES + 2 * SIDE;
   static constexpr int SCRATCH = TA_ROWS * TA_PAD * 4;
-  static constexpr int BUDGET = 222 * 1024 - SCRATCH - 1024;
-  static constexpr int OPS = BITS == 16 ? (BUDGET / OP > 12 ? 12 : BUDGET / OP) : (D == 128 ? 3 : 4);
-  static constexpr int RAWS_ALL = BITS == 16 ? 0 : (BUDGET - OPS * OP) / (RAW > 0 ? RAW : 1);
-  static constexpr int RAWS = RAWS_ALL > 12 ? 12 : RAWS_ALL;
-  static constexpr int SMEM = 1024 + OPS * OP + RAWS * RAW + SCRATCH;
-  static constexpr int LOADS = BITS == 16 ? OPS : RAWS;                            // slots the copies land in
-  static_assert(SMEM <= 224 * 1024, "shared memory");
-  static_assert(LOADS <= 2 * TA_FLAGS - 4, "flags");
+  static constexpr int OPS = D == 128 ? 6 : 12;                                    // ring of operand tiles
+  static constexpr int SMEM = 1024 + OPS * OP + SCRATCH;
+  static_assert(SMEM <= 220 * 1024, "shared memory");
+  static_assert(OPS % TEAMS == 0, "a team meets its slots in every turn, so it sees every phase of their barriers");
+  static_assert(OPS <= 2 * TA_FLAGS - 4, "flags");
 };
 
 struct TreeAttnParams {
@@ -169,6 +164,17 @@ __device__ __forceinline__ bool ta_item(int e, int n, int* tile) {
   return true;
 }
 
+// One operand tile of codes as the transforming warps need it: the cache's token index of each 16 tokens (-1: past the
+// end), and what is odd about it.
+struct TaPiece {
+  long long tok[TA_TILE / 16];
+  long long valid;              // tokens of the tile before the end of the sequence
+  long long drafted;            // first drafted token of the tile (TA_TILE and more: none)
+  long long is_v;
+  long long flag;               // the segment's flag in s_bad
+};
+constexpr int TA_PIECES = 12;   // descriptors in flight
+
 // Drafted tokens a row sees, as bits 0 .. m - 1.
 __device__ __forceinline__ uint64_t ta_mask(const TreeAttnParams& p, int row, int i, int m) {
   const uint64_t all = m == 64 ? ~0ull : (1ull << m) - 1;
@@ -197,12 +203,24 @@ __device__ __forceinline__ void ta_dequant(uint32_t w, __half2 s2, __half2 b2, u
     out[j] = *reinterpret_cast<const uint32_t*>(&v);
   }
 }
+// 16 bytes that are read once: kept out of L1.
+__device__ __forceinline__ uint4 ld_stream16(const uint8_t* a) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  return v;
+}
 __device__ __forceinline__ bool ta_half_bad(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
 
 __device__ __forceinline__ float ta_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// max of three (NaN operands are passed over, as by fmaxf)
+__device__ __forceinline__ float ta_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t ta_pack(float lo, float hi, bool bf16) {
   uint32_t r;
@@ -224,9 +242,17 @@ struct TaRing {
   }
 };
 
+// mbar_wait_bounded that looks at the clock (a slow read) only after some polls.
+__device__ __forceinline__ bool ta_poll(uint64_t* bar, uint32_t parity, volatile int* abort_v) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, abort_v);
+}
 // A whole warp waits; false for all lanes once any gave up (the reason is recorded once).
 __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile int* abort_v, unsigned err) {
-  bool ok = mbar_wait_bounded(bar, parity, abort_v);
+  bool ok = ta_poll(bar, parity, abort_v);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) {
     if (!*abort_v) raise_error(err);
@@ -239,46 +265,49 @@ __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ bool ta_fixed(const TaSeg& s, int j) { return (s.tile0 + j + 1) * TA_TILE > s.len; }
 
 template <int D, int BITS>
-__global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
+__global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   using Sh = TaShape<D, BITS>;
   constexpr bool RAW16 = BITS == 16;
   extern __shared__ uint8_t smem_raw[];
-  // load_*: the slots that copies land in.  op_*: operand slots (the same ones for a 16-bit cache).
-  __shared__ uint64_t load_full[12], load_empty[12], op_full[12], op_empty[12];
-  __shared__ uint64_t q_full, s_full[2], p_full, pv_done, fin_bar;
+  // operand slots: copied into (16-bit caches only), ready for the tensor cores, read
+  __shared__ uint64_t load_full[Sh::OPS], op_full[Sh::OPS], op_empty[Sh::OPS];
+  __shared__ uint64_t q_full, s_full[2], p_full[2], pv_done, fin_bar;
   __shared__ uint32_t s_tmem;
   __shared__ int abort_flag, s_bad[TA_FLAGS];
   __shared__ TaPlan plan;
+  __shared__ TaPiece pieces[RAW16 ? 1 : TA_PIECES];     // caches of codes: filled by the copying warp, read by one team each
+  __shared__ uint64_t piece_full[TA_PIECES], piece_empty[TA_PIECES];
   __shared__ float s_max[TA_ROWS], s_sum[TA_ROWS];
   __shared__ int s_ok[TA_SOFT];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const ops = smem;
-  uint8_t* const raws = smem + Sh::OPS * Sh::OP;
-  float* const scratch = reinterpret_cast<float*>(raws + Sh::RAWS * Sh::RAW);
+  float* const scratch = reinterpret_cast<float*>(smem + Sh::OPS * Sh::OP);
   volatile int* abort_v = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Sh::LOADS; ++i) {
-      mbar_init(&load_full[i], 1);
-      mbar_init(&load_empty[i], TA_XF);
-    }
     for (int i = 0; i < Sh::OPS; ++i) {
-      mbar_init(&op_full[i], TA_XF);
+      mbar_init(&load_full[i], 1);
+      mbar_init(&op_full[i], TA_TEAM);
       mbar_init(&op_empty[i], 1);
+    }
+    for (int i = 0; i < TA_PIECES; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], TA_TEAM);
     }
     mbar_init(&q_full, TA_SOFT);
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(&p_full, TA_SOFT);
+    mbar_init(&p_full[0], TA_SOFT);
+    mbar_init(&p_full[1], TA_SOFT);
     mbar_init(&pv_done, 1);
     mbar_init(&fin_bar, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < TA_FLAGS) s_bad[threadIdx.x] = 0;
-  if (warp == TA_MMA) {
+  if (warp == Sh::MMA) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
@@ -291,151 +320,201 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
   const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
   const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
 
-  if (warp == TA_PROD) {
-    // ============================================================ copies into the ring
-    const int shift = p.c.page_shift < 7 ? p.c.page_shift : 7, chunk = 1 << shift;   // tokens per copy
-    const int place_mask = (1 << p.c.page_shift) - 1;
-    constexpr int PER = RAW16 ? D / 64 : 3;            // copies per chunk: 64-wide halves, or codes / scales / biases
-    const int my_chunk = lane / PER, part = lane - my_chunk * PER;
-    TaRing<Sh::LOADS> ring;
-    bool ok = true;
-    for (long long u = u0; u < u1 && ok;) {
-      const TaSeg s = ta_segment(p, plan, u, u0, u1);
-      // the page of this lane's chunk of tile j
-      auto page_of = [&](int j) -> int {
-        const int t = (s.tile0 + j) * TA_TILE + (my_chunk << shift);
-        if (j >= s.n || my_chunk >= (TA_TILE >> shift) || t >= s.total) return 0;
-        int page = p.table[(size_t)s.b * p.table_pages + (t >> p.c.page_shift)];
-        if (page < 0 || page >= p.c.n_pages) {
-          raise_error(ERR_BAD_INPUT);
-          page = 0;                                    // stay inside the arrays: the result is undefined
-        }
-        return page;
-      };
-      // pages of the last two K tiles, and the next one's, fetched a tile ahead
-      int page_before = 0, page_k = 0, page_next = page_of(0);
-      for (int i = 0; i < 2 * s.n; ++i) {
-        int j;
-        const bool is_v = ta_item(i, s.n, &j);
-        if (!is_v) {
-          page_before = page_k;
-          page_k = page_next;
-          page_next = page_of(j + 1);
-        }
-        const int page = is_v && i != 2 * s.n - 1 ? page_before : page_k;
-        ok = ta_wait(RAW16 ? &op_empty[ring.slot] : &load_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
-        if (!ok) break;
-        const int t0 = (s.tile0 + j) * TA_TILE;
-        const int toks = s.total - t0 < TA_TILE ? s.total - t0 : TA_TILE;
-        const int chunks = (toks + chunk - 1) >> shift;
-        const uint32_t tx = (uint32_t)(chunks << shift) * (RAW16 ? D * 2 : D * BITS / 8 + 2 * (D / GROUP) * 2);
-        if (lane == 0) mbar_arrive_expect_tx(&load_full[ring.slot], tx);
-        __syncwarp();
-        if (my_chunk < chunks) {
-          const int place = (t0 + (my_chunk << shift)) & place_mask;
-          if constexpr (RAW16) {
+  if (warp == Sh::PROD) {
+    // ============================================================ copies of a 16-bit cache into the ring
+    if constexpr (RAW16) {
+      const int shift = p.c.page_shift < 7 ? p.c.page_shift : 7, chunk = 1 << shift;   // tokens per copy
+      const int place_mask = (1 << p.c.page_shift) - 1;
+      constexpr int PER = D / 64;                      // copies per chunk: 64-wide pieces of the head
+      const int my_chunk = lane / PER, part = lane - my_chunk * PER;
+      TaRing<Sh::OPS> ring;
+      bool ok = true;
+      for (long long u = u0; u < u1 && ok;) {
+        const TaSeg s = ta_segment(p, plan, u, u0, u1);
+        // the table's entry for this lane's chunk of tile j, checked when it is used: the load is a tile ahead
+        auto page_of = [&](int j) -> int {
+          const int t = (s.tile0 + j) * TA_TILE + (my_chunk << shift);
+          if (j >= s.n || my_chunk >= (TA_TILE >> shift) || t >= s.total) return 0;
+          return p.table[(size_t)s.b * p.table_pages + (t >> p.c.page_shift)];
+        };
+        int page_before = 0, page_k = 0, page_next = page_of(0);   // of the last two K tiles, and the next one's
+        for (int i = 0; i < 2 * s.n; ++i) {
+          int j;
+          const bool is_v = ta_item(i, s.n, &j);
+          if (!is_v) {
+            page_before = page_k;
+            page_k = page_next;
+            page_next = page_of(j + 1);
+          }
+          int page = is_v && i != 2 * s.n - 1 ? page_before : page_k;
+          ok = ta_wait(&op_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
+          if (!ok) break;
+          const int t0 = (s.tile0 + j) * TA_TILE;
+          const int toks = s.total - t0 < TA_TILE ? s.total - t0 : TA_TILE;
+          const int chunks = (toks + chunk - 1) >> shift;
+          if (lane == 0) mbar_arrive_expect_tx(&load_full[ring.slot], (uint32_t)(chunks << shift) * (D * 2));
+          __syncwarp();
+          if (my_chunk < chunks) {
+            if (page < 0 || page >= p.c.n_pages) {
+              raise_error(ERR_BAD_INPUT);
+              page = 0;                                // stay inside the arrays: the result is undefined
+            }
+            const int place = (t0 + (my_chunk << shift)) & place_mask;
             uint8_t* dst = ops + ring.slot * Sh::OP + part * (TA_TILE * 128) + (my_chunk << shift) * 128;
             tma_load_3d_plain(dst, is_v ? &p.tv : &p.tk, &load_full[ring.slot], part * 64, place, page * p.c.heads + s.h);
-          } else {
-            const size_t tok = kv_token(p.c, page, s.h, place);
-            uint8_t* raw = raws + ring.slot * Sh::RAW;
-            if (part == 0) {
-              const uint8_t* src = (is_v ? p.c.p.v : p.c.p.k) + tok * (D * BITS / 8);
-              bulk_load_plain(raw + (my_chunk << shift) * (D * BITS / 8), src, (uint32_t)chunk * (D * BITS / 8),
-                              &load_full[ring.slot]);
-            } else {
-              const __half* src = part == 1 ? (is_v ? p.c.p.vs : p.c.p.ks) : (is_v ? p.c.p.vb : p.c.p.kb);
-              bulk_load_plain(raw + Sh::CODES + (part - 1) * Sh::SIDE + (my_chunk << shift) * (D / GROUP) * 2,
-                              src + tok * (D / GROUP), (uint32_t)chunk * (D / GROUP) * 2, &load_full[ring.slot]);
-            }
           }
+          ring.next();
         }
+        u += s.n;
+      }
+      // every copy is waited for by its reader; after a failure, give those in flight time to land
+      if (!ok || *abort_v) {
+        const unsigned long long w0 = global_ns();
+        while (global_ns() - w0 < 50000ull) __nanosleep(1000);
+      }
+    } else {
+      // ========================================================== descriptors for the transforming warps
+      TaRing<TA_PIECES> ring;
+      const int pm = (1 << p.c.page_shift) - 1;
+      int n_seg = 0;
+      bool ok = true;
+      for (long long u = u0; u < u1 && ok; ++n_seg) {
+        const TaSeg s = ta_segment(p, plan, u, u0, u1);
+        auto page_of = [&](int j) -> int {             // of 16-token piece `lane` of tile j; checked when it is used
+          const int t = (s.tile0 + j) * TA_TILE + 16 * lane;
+          if (j >= s.n || lane >= TA_TILE / 16 || t >= s.total) return 0;
+          return p.table[(size_t)s.b * p.table_pages + (t >> p.c.page_shift)];
+        };
+        int page_before = 0, page_k = 0, page_next = page_of(0);   // of the last two K tiles, and the next one's
+        for (int i = 0; i < 2 * s.n; ++i) {
+          int j;
+          const bool is_v = ta_item(i, s.n, &j);
+          if (!is_v) {
+            page_before = page_k;
+            page_k = page_next;
+            page_next = page_of(j + 1);
+          }
+          int page = is_v && i != 2 * s.n - 1 ? page_before : page_k;
+          ok = ta_wait(&piece_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
+          if (!ok) break;
+          const int t0 = (s.tile0 + j) * TA_TILE, t = t0 + 16 * lane;
+          if ((unsigned)page >= (unsigned)p.c.n_pages) {
+            raise_error(ERR_BAD_INPUT);
+            page = 0;                                  // stay inside the arrays: the result is undefined
+          }
+          // one store for the whole descriptor: lane i writes its i-th word
+          long long word = t < s.total ? (long long)kv_token(p.c, page, s.h, t & pm) : -1;
+          word = lane == 8 ? s.total - t0 : (lane == 9 ? s.len - t0 : word);
+          word = lane == 10 ? (long long)is_v : (lane == 11 ? n_seg % TA_FLAGS : word);
+          if (lane < (int)(sizeof(TaPiece) / 8)) reinterpret_cast<long long*>(&pieces[ring.slot])[lane] = word;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&piece_full[ring.slot]);
+          ring.next();
+        }
+        u += s.n;
+      }
+      // the end: one descriptor for each team
+      for (int e = 0; e < Sh::TEAMS && ok; ++e) {
+        ok = ta_wait(&piece_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
+        if (!ok) break;
+        if (lane < TA_TILE / 16) pieces[ring.slot].tok[lane] = -1;
+        if (lane == 8) pieces[ring.slot].valid = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_full[ring.slot]);
         ring.next();
       }
-      u += s.n;
     }
-    // every copy is waited for by its reader; after a failure, give those in flight time to land
-    if (!ok || *abort_v) {
-      const unsigned long long w0 = global_ns();
-      while (global_ns() - w0 < 50000ull) __nanosleep(1000);
-    }
-  } else if (warp == TA_MMA) {
+  } else if (warp == Sh::MMA) {
     // ============================================================ MMA issue
-    if (lane == 0) {
+    // The whole warp runs the loop and one lane issues, so that descriptors and addresses live in uniform registers.
+    {
       TaRing<Sh::OPS> ring;
       uint32_t n_q = 0, n_s = 0, n_p = 0;               // phases seen of each barrier
       bool ok = true;
       constexpr uint32_t ID_S = f16_idesc_ex(TA_ROWS, TA_TILE, RAW16, false);
       constexpr uint32_t ID_O = f16_idesc_ex(TA_ROWS, D, RAW16, true);
+      const bool issuer = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t ops0 = (__shfl_sync(0xffffffffu, smem_u32(ops), 0) & 0x3FFFFu) >> 4;
+      // descriptors differ in the start address alone
+      constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+      constexpr uint32_t LO_K = 1u << 16, LO_V = (uint32_t)(TA_TILE * 128 >> 4) << 16;
       for (long long u = u0; u < u1 && ok;) {
-        const TaSeg s = ta_segment(p, plan, u, u0, u1);
-        ok = mbar_wait_bounded(&q_full, n_q++ & 1, abort_v);
-        for (int i = 0; i < 2 * s.n && ok; ++i) {
-          int j;
-          const bool is_v = ta_item(i, s.n, &j);
-          ok = mbar_wait_bounded(&op_full[ring.slot], ring.phase, abort_v);
-          if (ok && is_v) ok = mbar_wait_bounded(&p_full, n_p++ & 1, abort_v);
+        int n;
+        {
+          const TaSeg s = ta_segment(p, plan, u, u0, u1);
+          n = __shfl_sync(0xffffffffu, s.n, 0);
+        }
+        ok = ta_wait(&q_full, n_q++ & 1, abort_v, ERR_TIMEOUT_FULL);
+        for (int i = 0; i < 2 * n && ok; ++i) {
+          const bool is_v = i == 2 * n - 1 || (i > 0 && !(i & 1));
+          ok = ta_wait(&op_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
+          if (ok && is_v) ok = ta_wait(&p_full[n_p & 1], (n_p >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
           if (!ok) break;
           tc05_fence_after();
-          const uint32_t base = smem_u32(ops + ring.slot * Sh::OP);
+          const uint32_t base = ops0 + ring.slot * (Sh::OP >> 4);
           if (!is_v) {
-            // S buffer of tile n_s: its last reader handed over P of tile n_s - 2, waited for above
+            // S buffer of tile n_s: P of tile n_s - 2 lies there, whose product was issued before (MMAs run in order)
+            const uint32_t d = tm + TA_S + 128 * (n_s & 1), lo = base | LO_K;
+            if (issuer) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc05_mma_f16_ts(tmem + TA_S + 128 * (n_s & 1), tmem + TA_Q + 8 * kk,
-                              sw128_desc(base + (kk >> 2) * (TA_TILE * 128) + (kk & 3) * 32), ID_S, kk > 0);
-            tc05_commit(&s_full[n_s & 1]);
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc05_mma_f16_ts(d, tm + TA_Q + 8 * kk, lo + (kk >> 2) * (TA_TILE * 128 >> 4) + (kk & 3) * 2, HI, ID_S, kk > 0);
+              tc05_commit(&s_full[n_s & 1]);
+              tc05_commit(&op_empty[ring.slot]);
+            }
             ++n_s;
           } else {
+            const uint32_t a = tm + TA_S + 128 * (n_p & 1), lo = base | LO_V;
+            const bool first = i < 3 && !(i == 1 && n > 1);   // V of the segment's first tile: item 2, or 1 of 2
+            if (issuer) {
 #pragma unroll
-            for (int kk = 0; kk < TA_TILE / 16; ++kk)
-              tc05_mma_f16_ts(tmem + TA_O, tmem + TA_P + 8 * kk, sw128_desc_mn(base + kk * 2048, TA_TILE * 128), ID_O,
-                              j > 0 || kk > 0);
-            tc05_commit(&pv_done);
+              for (int kk = 0; kk < TA_TILE / 16; ++kk)
+                tc05_mma_f16_ts(tm + TA_O, a + 8 * kk, lo + kk * (2048 >> 4), HI, ID_O, !first || kk > 0);
+              tc05_commit(&pv_done);
+              tc05_commit(&op_empty[ring.slot]);
+            }
+            ++n_p;
           }
-          tc05_commit(&op_empty[ring.slot]);
+          __syncwarp();
           ring.next();
         }
-        u += s.n;
-      }
-      if (!ok) {
-        if (!*abort_v) raise_error(ERR_TIMEOUT_FULL);
-        *abort_v = 1;
+        u += n;
       }
       // no MMA may still be running when the tensor memory is freed: this wait
       // ignores the abort flag and ends only on completion or the time limit
-      tc05_commit(&fin_bar);
-      volatile int never = 0;
-      mbar_wait_bounded(&fin_bar, 0, &never);
+      if (issuer) {
+        tc05_commit(&fin_bar);
+        volatile int never = 0;
+        mbar_wait_bounded(&fin_bar, 0, &never);
+      }
+      __syncwarp();
     }
   } else if (warp >= TA_SOFT) {
-    // ============================================================ codes -> fp16 operands; V's odd places
-    const int t = (threadIdx.x - TA_SOFT * 32) & (TA_TILE - 1), hp = (threadIdx.x - TA_SOFT * 32) / TA_TILE;
-    TaRing<Sh::LOADS> in;
-    TaRing<Sh::OPS> to;
-    int n_seg = 0;
-    bool ok = true;
-    for (long long u = u0; u < u1 && ok; ++n_seg) {
-      const TaSeg s = ta_segment(p, plan, u, u0, u1);
-      for (int i = 0; i < 2 * s.n; ++i) {
-        int j;
-        const bool is_v = ta_item(i, s.n, &j);
-        ok = ta_wait(&load_full[in.slot], in.phase, abort_v, ERR_TIMEOUT_FULL);
-        if (!ok) break;
-        const bool fix = is_v && ta_fixed(s, j);
-        const int pos = (s.tile0 + j) * TA_TILE + t;
-        const bool past = pos >= s.total, drafted = pos >= s.len && !past;
-        bool odd = false;
-        if constexpr (RAW16) {
-          if (fix) {
+    const int team = (warp - TA_SOFT) / TA_TEAM, tw = (warp - TA_SOFT) % TA_TEAM;
+    const int t = 32 * tw + lane;                       // this lane's token of a tile
+    if constexpr (RAW16) {
+      // ========================================================== a 16-bit cache: V's odd places
+      TaRing<Sh::OPS> ring;
+      int n_seg = 0;
+      bool ok = true;
+      for (long long u = u0; u < u1 && ok; ++n_seg) {
+        const TaSeg s = ta_segment(p, plan, u, u0, u1);
+        for (int i = 0; i < 2 * s.n; ++i, ring.next()) {
+          int j;
+          const bool is_v = ta_item(i, s.n, &j);
+          ok = ta_wait(&load_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
+          if (!ok) break;
+          const int pos = (s.tile0 + j) * TA_TILE + t;
+          if (is_v && ta_fixed(s, j)) {
             // Rows past the end are zeroed (their weight is 0, and 0 * NaN would not be); so are a drafted row's
             // infinities and NaN, which only rows that see it may get (added in at the end of the segment).
-            if (past || drafted) {
-              constexpr int CH = D / 16;                // 16-byte chunks of half a row
+            if (pos >= s.len) {
+              const bool past = pos >= s.total;
+              bool odd = false;
 #pragma unroll
-              for (int cc = 0; cc < CH; ++cc) {
-                const int c = hp * CH + cc;             // chunk of the row, as it lies: the order does not matter here
-                uint4* at = reinterpret_cast<uint4*>(ops + in.slot * Sh::OP + (c >> 3) * (TA_TILE * 128) + t * 128 + ((c & 7) << 4));
+              for (int c = 0; c < D / 8; ++c) {         // chunks of the row as they lie: the order does not matter here
+                uint4* at = reinterpret_cast<uint4*>(ops + ring.slot * Sh::OP + (c >> 3) * (TA_TILE * 128) + t * 128 + ((c & 7) << 4));
                 if (past) {
                   *at = make_uint4(0, 0, 0, 0);
                 } else {
@@ -450,71 +529,136 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
                   if (hit) { *at = v; odd = true; }
                 }
               }
+              if (odd) s_bad[n_seg % TA_FLAGS] = 1;
             }
-            if (odd) s_bad[n_seg % TA_FLAGS] = 1;
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&op_full[in.slot]);
-          in.next();
-        } else {
-          ok = ta_wait(&op_empty[to.slot], to.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
-          if (!ok) break;
-          const uint8_t* raw = raws + in.slot * Sh::RAW;
-          constexpr int G = D / GROUP;
-          const __half* sc = reinterpret_cast<const __half*>(raw + Sh::CODES) + t * G;
-          const __half* bi = reinterpret_cast<const __half*>(raw + Sh::CODES + Sh::SIDE) + t * G;
-          __half sg[G], bg[G];
-          if constexpr (G == 2) {
-            const uint32_t a = *reinterpret_cast<const uint32_t*>(sc), b = *reinterpret_cast<const uint32_t*>(bi);
-            sg[0] = __ushort_as_half((unsigned short)a); sg[1] = __ushort_as_half((unsigned short)(a >> 16));
-            bg[0] = __ushort_as_half((unsigned short)b); bg[1] = __ushort_as_half((unsigned short)(b >> 16));
-          } else {
-            sg[0] = sc[0];
-            bg[0] = bi[0];
-          }
-          if (fix) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const bool wild = ta_half_bad(__half_as_ushort(sg[g])) || ta_half_bad(__half_as_ushort(bg[g]));
-              if (past || (drafted && wild)) sg[g] = bg[g] = __ushort_as_half((unsigned short)0);
-              odd |= drafted && wild;
-            }
-            if (odd) s_bad[n_seg % TA_FLAGS] = 1;
-          }
-          // A thread takes every other 16 bytes of its token's codes in an order that keeps 8 neighbouring lanes
-          // (tokens) on 8 different bank groups, both for these loads and for the swizzled stores.
-          constexpr int PARTS = D * BITS / 128, PERT = 128 / BITS;   // 16-byte parts of a row, codes in one
-          const int f = PARTS == 8 ? t & 7
-                        : (PARTS == 4 ? (BITS == 4 ? (t >> 1) & 3 : (((t >> 1) & 1) << 1) | (((t >> 1) ^ (t >> 2)) & 1)) : 0);
-          uint8_t* row = ops + to.slot * Sh::OP + t * 128;
-#pragma unroll
-          for (int x = 0; x < PARTS / 2; ++x) {
-            const int part = (hp * (PARTS / 2) + x) ^ f;
-            const uint4 v = *reinterpret_cast<const uint4*>(raw + t * (D * BITS / 8) + part * 16);
-            const int g = G == 1 ? 0 : part * PERT / GROUP;
-            const __half2 s2 = __half2half2(G == 2 && g ? sg[G - 1] : sg[0]), b2 = __half2half2(G == 2 && g ? bg[G - 1] : bg[0]);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[64 / BITS];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) ta_dequant<BITS>(w[y], s2, b2, o + y * (16 / BITS));
-            uint8_t* half = row + (part * PERT / 64) * (TA_TILE * 128);
-            const int c0 = part * PERT / 8 & 7;
-#pragma unroll
-            for (int y = 0; y < PERT / 8; ++y)
-              *reinterpret_cast<uint4*>(half + (((c0 + y) ^ (t & 7)) << 4)) = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-          }
-          fence_proxy_async_smem();  // the tensor cores read these writes through the async proxy
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&op_full[to.slot]);
-            mbar_arrive(&load_empty[in.slot]);
-          }
-          in.next();
-          to.next();
+          if (lane == 0) mbar_arrive(&op_full[ring.slot]);
         }
+        u += s.n;
       }
-      u += s.n;
+    } else {
+      // ========================================================== codes -> fp16 operands
+      // A team takes every third operand tile, a warp 32 of its tokens.  Codes come from global memory in 16-byte
+      // loads, LPT neighbouring lanes per token; the registers of a step are loaded for the team's next tile as soon
+      // as they are used, so the loads of a whole tile are always on their way.
+      constexpr int ROWB = D * BITS / 8, LPT = ROWB / 16, TPS = 32 / LPT, PERT = 128 / BITS;  // codes per 16 bytes
+      constexpr int NCH = PERT / 8, G = D / GROUP;      // 16-byte operand chunks a lane makes per step; groups per token
+      const int part = lane & (LPT - 1), sub = lane / LPT;
+      const int grp = part * PERT / GROUP, c0 = (part * PERT / 8) & 7;
+      // Which of its chunks a lane stores first, so that 8 neighbouring lanes meet 8 different bank groups.
+      const int sel = LPT == 8 ? part >> 2 : (NCH == 4 && LPT == 4 ? (part >> 1) | ((sub & 1) << 1) : 0);
+      const uint32_t pick = G == 2 && grp ? 0x3232 : 0x1010;
+      uint8_t* const mine = ops + (part * PERT / 64) * (TA_TILE * 128) + (32 * tw + sub) * 128;
+      TaRing<Sh::OPS> ring;
+      TaRing<TA_PIECES> ahead, here;
+      for (int i = 0; i < team; ++i) {
+        ring.next();
+        ahead.next();
+        here.next();
+      }
+      uint4 raw[LPT];
+      uint32_t sc = 0, bi = 0;                          // scales and biases of this lane's token (two groups, or one)
+      const uint8_t* at[2] = {};                        // the warp's two 16-token halves (null: past the end)
+      bool live = true;
+      // the next tile's addresses, scales and biases
+      auto locate = [&]() -> bool {
+        if (!ta_wait(&piece_full[ahead.slot], ahead.phase, abort_v, ERR_TIMEOUT_FULL)) return false;
+        const TaPiece& x = pieces[ahead.slot];
+        sc = bi = 0;
+        const int valid = (int)x.valid;
+        live = valid > 0;
+        const bool is_v = x.is_v;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const long long tok = x.tok[2 * tw + hf];
+          at[hf] = tok < 0 ? nullptr : (is_v ? p.c.p.v : p.c.p.k) + tok * ROWB + lane * 16;
+          if (tok >= 0 && lane / 16 == hf && t < valid) {
+            const size_t g = ((size_t)tok + (lane & 15)) * G;
+            const __half *ps = (is_v ? p.c.p.vs : p.c.p.ks) + g, *pb = (is_v ? p.c.p.vb : p.c.p.kb) + g;
+            if constexpr (G == 2) {
+              sc = *reinterpret_cast<const uint32_t*>(ps);
+              bi = *reinterpret_cast<const uint32_t*>(pb);
+            } else {
+              sc = *reinterpret_cast<const unsigned short*>(ps);
+              bi = *reinterpret_cast<const unsigned short*>(pb);
+            }
+          }
+        }
+        for (int i = 0; i < Sh::TEAMS; ++i) ahead.next();
+        return true;
+      };
+      auto fetch = [&](int i) {
+        const int hf = i * TPS / 16;
+        if (at[hf]) raw[i] = ld_stream16(at[hf] + (i * TPS - 16 * hf) * ROWB);
+      };
+#pragma unroll
+      for (int i = 0; i < LPT; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+      bool ok = locate();
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < LPT; ++i) fetch(i);
+      }
+      while (ok && live) {
+        uint32_t sv = sc, bv = bi;
+        ok = ta_wait(&op_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
+        if (!ok) break;
+        const TaPiece& x = pieces[here.slot];
+        if (x.is_v && x.drafted < TA_TILE) {
+          // A V row past the end becomes zero (its weight is 0, and 0 * NaN would not be); so does a drafted row's
+          // group that reads as NaN, which only rows that see it may get (added in at the end of the segment).
+          const bool past = t >= x.valid, drafted = t >= x.drafted && !past;
+          bool odd = false;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const bool wild = ta_half_bad(sv >> (16 * g)) || ta_half_bad(bv >> (16 * g));
+            if (past || (drafted && wild)) {
+              sv &= ~(0xffffu << (16 * g));
+              bv &= ~(0xffffu << (16 * g));
+            }
+            odd |= drafted && wild;
+          }
+          if (odd) s_bad[x.flag] = 1;
+        }
+        uint8_t* const dst = mine + ring.slot * Sh::OP;
+#pragma unroll
+        for (int i = 0; i < LPT; ++i) {
+          uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const uint32_t s1 = __shfl_sync(0xffffffffu, sv, i * TPS + sub), b1 = __shfl_sync(0xffffffffu, bv, i * TPS + sub);
+          const uint32_t sp = __byte_perm(s1, 0, pick), bp = __byte_perm(b1, 0, pick);
+          const __half2 s2 = *reinterpret_cast<const __half2*>(&sp), b2 = *reinterpret_cast<const __half2*>(&bp);
+          // chunk y comes from the words of chunk y ^ sel
+          if constexpr (NCH == 4 && LPT == 4) {
+            if (sel & 1) { const uint32_t a = w[0], b = w[2]; w[0] = w[1]; w[1] = a; w[2] = w[3]; w[3] = b; }
+          }
+          if constexpr (LPT == 8 || (NCH == 4 && LPT == 4)) {
+            if (sel & (NCH / 2)) { const uint32_t a = w[0], b = w[1]; w[0] = w[2]; w[2] = a; w[1] = w[3]; w[3] = b; }
+          }
+          uint32_t o[64 / BITS];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) ta_dequant<BITS>(w[y], s2, b2, o + y * (16 / BITS));
+          const int xr = (i * TPS + sub) & 7;           // the token's row in its swizzle group
+#pragma unroll
+          for (int y = 0; y < NCH; ++y)
+            *reinterpret_cast<uint4*>(dst + i * TPS * 128 + (((c0 + (y ^ sel)) ^ xr) << 4)) =
+                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+        fence_proxy_async_smem();  // the tensor cores read these writes through the async proxy
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&op_full[ring.slot]);
+          mbar_arrive(&piece_empty[here.slot]);
+        }
+        for (int i = 0; i < Sh::TEAMS; ++i) {
+          ring.next();
+          here.next();
+        }
+        ok = locate();
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < LPT; ++i) fetch(i);
+      }
     }
   } else {
     // ============================================================ softmax, and the ends of segments
@@ -534,52 +678,50 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
       const uint64_t bits = real ? ta_mask(p, row, di, s.m) : 0;
       float f;                                          // score -> exponent of 2
       {
-        uint32_t w[D / 2];
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)row * p.ldq + (s.h * p.group + hg) * D);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = real ? src[c] : make_uint4(0, 0, 0, 0);
-          w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
-        }
         const bool minus = p.scale < 0.f;               // the sign goes into q, so a larger S is a larger score
         f = fabsf(p.scale) * 1.4426950408889634f;
-        if constexpr (RAW16) {
-#pragma unroll
-          for (int c = 0; c < D / 2; ++c) w[c] ^= minus ? 0x80008000u : 0u;
-        } else {
+        float up = minus ? -1.f : 1.f;
+        if constexpr (!RAW16) {
           float mx = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 2; ++c)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[c] << 16)), fabsf(__uint_as_float(w[c] & 0xffff0000u))));
-          const int ex = scale_exponent(mx);
-          const float up = minus ? -pow2_exact(ex) : pow2_exact(ex);
-          f *= pow2_exact(-ex);
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
-            float x[8];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              x[2 * y] = __uint_as_float(w[4 * c + y] << 16) * up;
-              x[2 * y + 1] = __uint_as_float(w[4 * c + y] & 0xffff0000u) * up;
-            }
+            const uint4 v = real ? src[c] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              w[4 * c + y] = BITS == 4 ? ta_pack(x[y], x[y + 4], false) : ta_pack(x[2 * y], x[2 * y + 1], false);
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u))));
           }
+          const int ex = scale_exponent(mx);
+          up *= pow2_exact(ex);
+          f *= pow2_exact(-ex);
         }
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t x[32];
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[16];
 #pragma unroll
-          for (int y = 0; y < 32; ++y) x[y] = w[32 * c + y];
-          tmem_st32(tmem + TA_Q + lanes + 32 * c, x);
-        }
-        if (s.split > 1) {                              // the blocks of P off the diagonal
-          uint32_t x[32];
+          for (int z = 0; z < 4; ++z) {
+            const uint4 v = real ? src[4 * c + z] : make_uint4(0, 0, 0, 0);
+            x[4 * z] = v.x; x[4 * z + 1] = v.y; x[4 * z + 2] = v.z; x[4 * z + 3] = v.w;
+          }
 #pragma unroll
-          for (int y = 0; y < 32; ++y) x[y] = 0;
-          tmem_st32(tmem + TA_P + lanes, x);
-          tmem_st32(tmem + TA_P + lanes + 32, x);
+          for (int z = 0; z < 4; ++z) {
+            if constexpr (RAW16) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) x[4 * z + y] ^= minus ? 0x80008000u : 0u;
+            } else {
+              float e[8];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                e[2 * y] = __uint_as_float(x[4 * z + y] << 16) * up;
+                e[2 * y + 1] = __uint_as_float(x[4 * z + y] & 0xffff0000u) * up;
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                x[4 * z + y] = BITS == 4 ? ta_pack(e[y], e[y + 4], false) : ta_pack(e[2 * y], e[2 * y + 1], false);
+            }
+          }
+          tmem_st16(tmem + TA_Q + lanes + 16 * c, x);
         }
         tmem_st_wait();
         tc05_fence_before();
@@ -612,12 +754,11 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
             for (int x = 0; x < 32; ++x) mx = fmaxf(mx, m >> x & 1 ? __uint_as_float(v[x]) : -INFINITY);
           } else {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(v[x]));
+            for (int x = 0; x < 32; x += 2) mx = ta_max3(mx, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
           }
         }
         const float top = mx == -INFINITY ? mx : mx * f;
         const bool grown = top - ref > TA_GROW;         // false for -inf - -inf
-        bool waited = j == 0;
         if (__any_sync(0xffffffffu, grown)) {
           float fix = 1.f;
           if (grown) {
@@ -627,9 +768,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
             sum *= fix;
           }
           if (j > 0) {
+            // S of this tile is there, so the product before the last has ended: one phase is open at most
             ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);
             if (!ok) break;
-            waited = true;
             tc05_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -642,36 +783,39 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
           }
         }
         const float sub = ref == -INFINITY ? 0.f : ref;
-        if (!waited) {                                  // P is free once the product before has read it
-          ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);
-          if (!ok) break;
-          tc05_fence_after();
-        }
+        // P takes the place of S, column by column behind the reads
         for (int c = c_first; c < c_first + nc; ++c) {
           if (nc > 1) tmem_ld32(sbuf + 32 * c, v);
           const uint32_t m = masked ? seen(c) : 0xffffffffu;
           uint32_t w[16];
-          float a0 = 0.f, a1 = 0.f;
+          float2 acc = make_float2(0.f, 0.f);
+          const float2 f2 = make_float2(f, f), n2 = make_float2(-sub, -sub);
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            float e0 = ta_exp2(fmaf(__uint_as_float(v[2 * x]), f, -sub));
-            float e1 = ta_exp2(fmaf(__uint_as_float(v[2 * x + 1]), f, -sub));
+            const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), f2, n2);
+            float2 e = make_float2(ta_exp2(z.x), ta_exp2(z.y));
             if (masked) {
-              e0 = m >> (2 * x) & 1 ? e0 : 0.f;
-              e1 = m >> (2 * x + 1) & 1 ? e1 : 0.f;
+              e.x = m >> (2 * x) & 1 ? e.x : 0.f;
+              e.y = m >> (2 * x + 1) & 1 ? e.y : 0.f;
             }
-            a0 += e0;
-            a1 += e1;
-            w[x] = ta_pack(e0, e1, RAW16);
+            acc = __fadd2_rn(acc, e);
+            w[x] = ta_pack(e.x, e.y, RAW16);
           }
-          sum += a0 + a1;
-          tmem_st16(tmem + TA_P + lanes + 16 * c, w);
+          sum += acc.x + acc.y;
+          tmem_st16(sbuf + 16 * c, w);
+        }
+        if (s.split > 1) {                              // the blocks of P off the diagonal
+          const uint32_t zero[16] = {};
+          for (int c = 0; c < 4; ++c)
+            if (c < c_first || c >= c_first + nc) tmem_st16(sbuf + 16 * c, zero);
         }
         tmem_st_wait();
         tc05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full);
+        if (lane == 0) mbar_arrive(&p_full[n_tile & 1]);
       }
+      // the last product; the one before may be out too, and each phase has to be seen
+      if (ok) ok = ta_wait(&pv_done, (n_tile - 2) & 1, abort_v, ERR_TIMEOUT_FULL);
       if (ok) ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);
       // all four warps meet before the exchange, and go on together or not at all
       s_max[L] = ref;
@@ -749,7 +893,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) tree_attn_kernel(const __grid_c
   }
   tc05_fence_before();
   __syncthreads();
-  if (warp == TA_MMA) {
+  if (warp == Sh::MMA) {
     tc05_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -831,7 +975,7 @@ static cudaError_t launch_tree_attn(const TreeAttnParams& p, bool join, cudaStre
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3(p.grid), dim3(TA_THREADS), Sh::SMEM, s, attr);
+  cudaLaunchConfig_t cfg = pdl_config(dim3(p.grid), dim3(Sh::THREADS), Sh::SMEM, s, attr);
   e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, BITS>, p);
   if (e != cudaSuccess || !join) return e;
   const long long pairs = (long long)p.map.offs[p.map.B] * p.c.heads * p.group;
