@@ -1,0 +1,138 @@
+// Shared by the kernel of tree attention and the join: their parameters, how the work is dealt, and how a finished run of an item is
+// written.
+//
+// Every (request, key head, block of rows) is an item of ceil(tokens / unit) units; the units of all items, in order, are
+// dealt to the CTAs in equal contiguous runs, so ragged lengths balance and one long sequence fills the GPU.  A CTA that has
+// an item whole writes the output; parts of an item leave fp32 sums (with their maximum and weight) in the workspace, and a
+// second kernel joins them in CTA order.  Each CTA has at most two such parts: its first run and its last.
+#pragma once
+
+#include "sv_kv.cuh"
+
+namespace sv {
+
+constexpr int TA_UNIT_SHIFT = 7;                   // log2 of the tokens dealt at once: a tile of the kernel
+constexpr float TA_BIAS = 8.f, TA_GROW = 14.f;     // weights start at 2^8 at most and may grow to 2^14
+
+struct TreeAttnParams {
+  CUtensorMap tk, tv;        // 16-bit caches: [pages * heads][page][dim], boxes of 64 x min(page, 128)
+  KvCache c;
+  RowMap map;
+  const int32_t *kv_len, *table;
+  int table_pages;
+  const __nv_bfloat16* q; int ldq;
+  int group;                 // query heads per key head
+  float scale;
+  const uint64_t* mask;
+  __nv_bfloat16* out; int ldo;
+  float* partial;            // [2 * grid][block][dim] sums of the CTAs' unfinished items
+  float* stats;              // [2 * grid][2][block]: their maximum (as an exponent of 2) and weight
+  int grid;
+  int block;                 // rows (drafted row x query head of the group) per item
+};
+
+// What every CTA derives from the lengths: prefix sums of units.
+struct TaPlan {
+  long long pre[MAX_BATCH + 1];   // units of the requests before b
+  int len[MAX_BATCH];             // committed tokens, brought into the table's range
+};
+
+__host__ __device__ __forceinline__ int ta_blocks(int rows, int block) { return (rows + block - 1) / block; }
+
+// By one warp.
+__device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool report) {
+  const int lane = threadIdx.x & 31;
+  const RowMap& map = p.map;
+  const long long cap = (long long)p.table_pages << p.c.page_shift;   // at least every request's rows (checked by the host)
+  long long run = 0;
+  for (int b0 = 0; b0 < map.B; b0 += 32) {
+    const int b = b0 + lane;
+    long long units = 0;
+    if (b < map.B) {
+      const int m = map.offs[b + 1] - map.offs[b];
+      long long len = p.kv_len[b];
+      if (m && (len < 0 || len + m > cap)) {
+        if (report) raise_error(ERR_BAD_INPUT);
+        len = len < 0 ? 0 : cap - m;
+      }
+      plan->len[b] = (int)len;
+      if (m) units = (long long)p.c.heads * ta_blocks(m * p.group, p.block) * ((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT);
+    }
+    long long inc = units;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += up;
+    }
+    if (b < map.B) plan->pre[b + 1] = run + inc;
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) plan->pre[0] = 0;
+}
+
+// A run of units of one item in one CTA.
+struct TaSeg {
+  int b, h, rb, m, row0, rows;   // request, key head, row block; drafted rows, first row, rows of the block
+  int tile0, n, nt, len, total;  // first unit, units, the item's units; committed and all tokens
+  bool first;                    // starts at the CTA's first unit
+};
+__device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPlan& plan, long long u, long long u0, long long u1) {
+  int lo = 0, hi = p.map.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (plan.pre[mid] <= u) lo = mid; else hi = mid;
+  }
+  TaSeg s;
+  s.b = lo;                      // pre[lo] <= u < pre[lo + 1]: a request with units (the last of equal prefixes)
+  s.row0 = p.map.offs[lo];
+  s.m = p.map.offs[lo + 1] - s.row0;
+  s.len = plan.len[lo];
+  s.total = s.len + s.m;
+  s.nt = (s.total + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
+  const unsigned long long local = (unsigned long long)(u - plan.pre[lo]);
+  const int item = (int)(local / (unsigned)s.nt);
+  s.tile0 = (int)(local - (unsigned long long)item * (unsigned)s.nt);
+  const int nrb = ta_blocks(s.m * p.group, p.block);
+  s.h = item / nrb;
+  s.rb = item - s.h * nrb;
+  const int left = s.m * p.group - s.rb * p.block;
+  s.rows = left < p.block ? left : p.block;
+  const long long can = u1 - u;
+  s.n = s.nt - s.tile0 < can ? s.nt - s.tile0 : (int)can;
+  s.first = u == u0;
+  return s;
+}
+
+// Drafted tokens a row sees, as bits 0 .. m - 1.
+__device__ __forceinline__ uint64_t ta_mask(const TreeAttnParams& p, int row, int i, int m) {
+  const uint64_t all = m == 64 ? ~0ull : (1ull << m) - 1;
+  return (p.mask ? p.mask[row] : (i == 63 ? ~0ull : (1ull << (i + 1)) - 1)) & all;
+}
+
+template <int BITS>
+__device__ __forceinline__ float ta_cache_value(const uint8_t* codes, const __half* s, const __half* b, size_t tok, int dim, int d) {
+  if constexpr (BITS == 16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(codes)[tok * dim + d]);
+  const size_t g = tok * (dim / GROUP) + d / GROUP;
+  const uint32_t code = BITS == 8 ? codes[tok * dim + d] : (codes[(tok * dim + d) >> 1] >> (4 * (d & 1))) & 15u;
+  return fmaf(__half2float(s[g]), (float)code, __half2float(b[g]));
+}
+
+__device__ __forceinline__ float ta_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t ta_pack(float lo, float hi, bool bf16) {
+  uint32_t r;
+  if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ bool ta_half_bad(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
+
+// Where a CTA's run of an item leaves its partial sums.
+__device__ __forceinline__ size_t ta_slot(const TaSeg& s) { return 2 * (size_t)blockIdx.x + (s.first ? 0 : 1); }
+
+cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t s);
+
+}  // namespace sv

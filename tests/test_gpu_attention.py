@@ -7,13 +7,13 @@ Tolerances, from the arithmetic (u = half a step: bf16 2^-8, fp16 2^-11, fp32 2^
   32 u32 (|x_i| + |x_j|) covers them.
 * cache: codes, scales and biases are equal to the last bit (the format's roundings are IEEE fp32 and fp16); read back
   values carry one fp32 and one bf16 rounding.
-* attention: with e_t the error of the exponent of token t and r the relative error of a weight and a
+* attention: with e_t the error of the exponent of token t, w the relative error of a weight and r that of a weight and a
   value together, out_d moves by at most  (sum_t p_t |v_td| x_t + |out_d| sum_t p_t y_t) / (1 - sum_t p_t y_t),
-  x_t = exp(r + e_t) - 1, y_t = exp(e_t) - 1.
+  x_t = exp(r + e_t) - 1, y_t = exp(w + e_t) - 1: the sum of the weights may be taken before or after their rounding.
   e_t: for codes, K enters the product as fp16 (2^-11 per element) - scale sum_d |q_d k_td| 2^-11 - and fp32
   accumulation adds (dim + 8) u32 of the same sum; the exponent itself (a product and a subtraction in fp32 and the
-  hardware exponential, 2^-22) adds 8 u32 (|score| + 1).  r: the weight is rounded to 16 bits, 2^-8 over a bf16
-  cache and 2^-11 over codes, V enters as fp16 over codes (2^-11), and the sum over T tokens in fp32 adds
+  hardware exponential, 2^-22) adds 8 u32 (|score| + 1).  w: the weight is rounded to 16 bits, 2^-8 over a bf16
+  cache and 2^-11 over codes; V enters as fp16 over codes (another 2^-11); the sum over T tokens in fp32 adds
   (log2 T + 16) u32 in any tree of 128-token tiles.  Last, one bf16 rounding of the output.
 """
 
@@ -341,9 +341,10 @@ def check_attention(got, cache, bits, offs, lens, table, page, q, masks, hq, sca
                 want = p @ vv
                 mag = abs(scale) * (np.abs(kk) @ np.abs(qi[h]))
                 e = mag * ((2.0 ** -11 if bits != 16 else 0.0) + (d + 8) * U32) + 8 * U32 * (np.abs(z) + np.abs(z).max() + 1)
-                rr = (2.0 ** -8 if bits == 16 else 2.0 ** -10) + (np.log2(len(at) + 1) + 16) * U32
+                rw = (2.0 ** -8 if bits == 16 else 2.0 ** -11) + (np.log2(len(at) + 1) + 16) * U32
+                rr = rw + (0.0 if bits == 16 else 2.0 ** -11)
                 w = np.expm1(e + rr)                       # a weight's relative change, not to first order only
-                den = p @ np.expm1(e)
+                den = p @ np.expm1(e + rw)
                 assert den < 0.5
                 bound = (p @ (np.abs(vv) * w[:, None]) + np.abs(want) * den) / (1 - den)
                 bound = bound * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(want) + 1e-30
