@@ -19,6 +19,8 @@
 // untouched.  Codes are dequantized by four teams of four warps into fp16 in the operand layout, fp16(s * c + b) with the
 // exact code (half an fp16 step), and Q enters as fp16 scaled by a power of two per row, exact for every bf16 value
 // within 2^29 of the row's largest.
+#include <type_traits>
+
 #include "sv_tc05.cuh"
 #include "tree_attn.cuh"
 
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       here.next(team);
       uint4 raw[LPT];
       uint32_t sc = 0, bi = 0;                          // scales and biases of this lane's token (two groups, or one)
-      const uint8_t* at[2] = {};                        // the warp's two 16-token halves (null: past the end)
+      const uint8_t* at[2] = {};                        // the warp's two 16-token halves
       bool live = true;
       // the next tile's addresses, scales and biases
       auto locate = [&]() -> bool {
@@ -497,7 +499,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const long long tok = x.tok[2 * tw + hf];
-          at[hf] = tok < 0 ? nullptr : (is_v ? p.c.p.v : p.c.p.k) + tok * ROWB + lane * 16;
+          // (past the end, the cache's first tokens stand in: the loads need no branch, and nothing comes of them)
+          at[hf] = (is_v ? p.c.p.v : p.c.p.k) + (tok < 0 ? 0 : tok) * ROWB + lane * 16;
           if (tok >= 0 && lane / 16 == hf && t < valid) {
             const size_t g = ((size_t)tok + (lane & 15)) * G;
             const __half *ps = (is_v ? p.c.p.vs : p.c.p.ks) + g, *pb = (is_v ? p.c.p.vb : p.c.p.kb) + g;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       };
       auto fetch = [&](int i) {
         const int hf = i * TPS / 16;
-        if (at[hf]) raw[i] = ld_stream16(at[hf] + (i * TPS - 16 * hf) * ROWB);
+        raw[i] = ld_stream16(at[hf] + (i * TPS - 16 * hf) * ROWB);
       };
 #pragma unroll
       for (int i = 0; i < LPT; ++i) raw[i] = make_uint4(0, 0, 0, 0);
@@ -664,10 +667,12 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         ok = ta_wait(&s_full[n_tile & 1], (n_tile >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
         if (ok && j > 0) ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);   // P, O and L are free
         tc05_fence_after();
-        // does row r see this token?
-        auto seen = [&](int r) -> bool { return back < 0 || (back < 64 && (s_mask[r] >> back & 1)); };
+        // Does row r see this token?  Without branches, here and below: a branch per row would keep the rows' chains of
+        // load, multiply-add, exponential and rounding from overlapping (47 cycles a row against 6).
+        auto seen = [&](int r) -> bool { return (back < 0) | ((back < 64) & ((uint32_t)(s_mask[r] >> (back & 63)) & 1u)); };
         // the tile's weights into P; true if some visible score has outgrown its row's reference
-        auto weigh = [&]() -> bool {
+        auto weigh_tile = [&](auto is_masked) -> bool {
+          constexpr bool MASKED = decltype(is_masked)::value;
           float most = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < N; c += 32) {
@@ -685,7 +690,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
                 const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[16 * hf + 2 * x]), __uint_as_float(v[16 * hf + 2 * x + 1])),
                                             make_float2(fr.x, fr.y), make_float2(fr.z, fr.w));
                 float2 e = make_float2(ta_exp2(z.x), ta_exp2(z.y));
-                if (masked) {
+                if constexpr (MASKED) {
                   const bool s0 = seen(r), s1 = seen(r + 1);
                   most = ta_max3(most, s0 ? z.x : -INFINITY, s1 ? z.y : -INFINITY);
                   e.x = s0 ? e.x : 0.f;
@@ -702,6 +707,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
           }
           return most > TA_GROW;
         };
+        auto weigh = [&]() -> bool { return masked ? weigh_tile(std::true_type{}) : weigh_tile(std::false_type{}); };
         bool again = true;                              // until every row has a reference, tiles go the long way
         if (all_set) {
           bool grown = false;
@@ -722,22 +728,23 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
             break;
           }
           // ------------------------------------------------------ new references
+          auto maxima = [&](auto is_masked) {
 #pragma unroll 1
-          for (int c = 0; c < N; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(sbuf + c, v);
-            int mine = 0;
+            for (int c = 0; c < N; c += 16) {
+              float v[16];
+              tmem_ld16(sbuf + c, v);
+              int mine = 0;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int r = c + x;
-              const float f = reinterpret_cast<const float*>(&s_fr[(r < N ? r : 0) / 2])[r & 1];
-              float z = __uint_as_float(v[x]) * f;
-              if (masked && !(r < N && seen(r))) z = -INFINITY;
-              const int top = __reduce_max_sync(0xffffffffu, ta_key(z));
-              if (lane == x) mine = top;
+              for (int x = 0; x < 16; ++x) {
+                float z = v[x] * reinterpret_cast<const float*>(&s_fr[(c + x) / 2])[x & 1];
+                if constexpr (decltype(is_masked)::value) z = seen(c + x) ? z : -INFINITY;
+                const int top = __reduce_max_sync(0xffffffffu, ta_key(z));
+                mine = lane == x ? top : mine;
+              }
+              if (lane < 16) s_key[warp][c + lane] = mine;
             }
-            if (c + lane < N) s_key[warp][c + lane] = mine;
-          }
+          };
+          if (masked) maxima(std::true_type{}); else maxima(std::false_type{});
           named_bar_sync(1, TA_SOFT * 32);
           bool late = false;
           if (t < N) {
@@ -785,29 +792,39 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       if (lane == 0) s_failed[warp] = !ok;
       if (ta_any(!ok)) break;
       tc05_fence_after();
-      if (t < D) {
+      // codes of 4 bits stand at another position inside each 8 elements
+      const int d = BITS == 4 ? (t & ~7) + ((t & 7) >> 1) + 4 * (t & 1) : t;
+      auto finish = [&](auto is_whole) {
 #pragma unroll 1
         for (int c = 0; c < N; c += 16) {
           float o[16], l[16];
           tmem_ld16(tmem + lanes + TA_O + c, o);
           tmem_ld16(tmem + lanes + TA_L + c, l);
-          // codes of 4 bits stand at another position inside each 8 elements
-          const int d = BITS == 4 ? (t & ~7) + ((t & 7) >> 1) + 4 * (t & 1) : t;
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const int r = c + x;
-            if (r >= s.rows) continue;
-            float val = o[x];
-            if (whole) val = l[x] == 0.f ? 0.f : val / l[x];
-            if (whole) p.out[s_out[r] + d] = __float2bfloat16_rn(val);
-            else p.partial[s_out[r] + d] = val;
-            if (!whole && t == 0) {
-              // the reference that the sums stand at: minus nref (a row without one has no weight)
-              p.stats[2 * slot * p.block + r] = l[x] == 0.f ? -INFINITY : -reinterpret_cast<const float*>(&s_fr[r / 2])[2 + (r & 1)];
-              p.stats[(2 * slot + 1) * p.block + r] = l[x];
+            const bool there = c + x < s.rows;
+            if constexpr (decltype(is_whole)::value) {
+              const float val = l[x] == 0.f ? 0.f : __fdividef(o[x], l[x]);   // a row that saw nothing is zero
+              if (there) p.out[s_out[c + x] + d] = __float2bfloat16_rn(val);
+            } else {
+              if (there) p.partial[s_out[c + x] + d] = o[x];
+            }
+          }
+          if constexpr (!decltype(is_whole)::value) {
+            float mine = 0.f;                           // every lane has every row's weight: lane x keeps row x's
+#pragma unroll
+            for (int x = 0; x < 16; ++x) mine = lane == x ? l[x] : mine;
+            if (t < 16 && c + t < s.rows) {
+              // the reference that the sums stand at (a row without weight has none)
+              p.stats[2 * slot * p.block + c + t] =
+                  mine == 0.f ? -INFINITY : -reinterpret_cast<const float*>(&s_fr[(c + t) / 2])[2 + (t & 1)];
+              p.stats[(2 * slot + 1) * p.block + c + t] = mine;
             }
           }
         }
+      };
+      if (t < D) {
+        if (whole) finish(std::true_type{}); else finish(std::false_type{});
       }
       if (s_bad[n_seg % TA_FLAGS] && t < D) {
         // V held infinities or NaN in drafted tokens, which were left out of the products: the rows that see one get it here
