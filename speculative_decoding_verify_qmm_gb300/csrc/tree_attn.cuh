@@ -12,7 +12,6 @@
 namespace sv {
 
 constexpr int TA_UNIT_SHIFT = 7;                   // log2 of the tokens dealt at once: a tile of the kernel
-constexpr float TA_BIAS = 8.f, TA_GROW = 14.f;     // weights start at 2^8 at most and may grow to 2^14
 
 struct TreeAttnParams {
   CUtensorMap tk, tv;        // 16-bit caches: [pages * heads][page][dim], boxes of 64 x min(page, 128)

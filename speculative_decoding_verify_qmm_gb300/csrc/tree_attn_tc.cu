@@ -11,12 +11,12 @@
 //   L  [any x row]  += 1 P^T       the rows' weights, from a tile of ones
 // S, O and L are in tensor memory.  A thread owns one token of the tile, so its softmax needs no neighbour: the weight is
 // 2^(S f_r - ref_r) with a reference per row that all threads share.  The reference moves only when some score has outgrown
-// it by 2^14 (it is set 2^8 above the row's largest score of the moment): one barrier with an OR per tile finds that out,
+// it (by 2^15 in fp16, 2^60 in bf16): one barrier with an OR per tile finds that out,
 // after P is written; then, rarely, the tile's row maxima are taken, O and L are rescaled, and P is written again.
 // The end of an item needs no exchange: a lane has one element of every row.
 //
 // Bound by memory for few rows; tiles of 128 tokens, dealt to one CTA per SM.  16-bit caches go from TMA to the tensor cores
-// untouched.  Codes are dequantized by four teams of four warps into fp16 in the operand layout, fp16(s * c + b) with the
+// untouched.  Codes are dequantized by three teams of four warps into fp16 in the operand layout, fp16(s * c + b) with the
 // exact code (half an fp16 step), and Q enters as fp16 scaled by a power of two per row, exact for every bf16 value
 // within 2^29 of the row's largest.
 #include <type_traits>
@@ -27,20 +27,25 @@
 namespace sv {
 
 constexpr int TA_TILE = 128;                       // tokens per tile: the lanes of tensor memory
-constexpr int TA_SOFT = 4, TA_TEAM = 4;            // softmax warps (0-3); warps of a transforming team
+constexpr int TA_GROUP = 4, TA_SOFT = 2 * TA_GROUP;  // two groups of four softmax warps (0-7), for even and odd tiles
+constexpr int TA_TEAM = 4;                         // warps of a transforming team
 constexpr int TA_FLAGS = 16;                       // segments whose flags are alive at once (ring depth / 2 at most)
 constexpr uint32_t TA_S = 0, TA_O = 256, TA_L = 384;  // tensor-memory columns: two S buffers of 128; O; L
 
 // NB: rows per item at most.  Warps: softmax, transforming teams, the copying warp, the MMA warp.
 template <int D, int BITS, int NB>
 struct TaShape {
-  static constexpr int TEAMS = BITS == 16 ? 1 : 4;
+  static constexpr int TEAMS = BITS == 16 ? 1 : 3;
   static constexpr int PROD = TA_SOFT + TEAMS * TA_TEAM, MMA = PROD + 1, THREADS = (MMA + 1) * 32;
   static constexpr int OP = TA_TILE * D * 2;                                       // one operand tile, 16 bits a value
   static constexpr int Q = NB * D * 2, P = NB / 64 * TA_TILE * 128, ONES = 1024;
-  static constexpr int FIT = (219 * 1024 - Q - P - ONES) / OP;
-  static constexpr int OPS = BITS == 16 ? (FIT > 10 ? 10 : FIT) : 4;               // ring of operand tiles
-  static constexpr int SMEM = 1024 + OPS * OP + Q + P + ONES;
+  static constexpr int FIT = (218 * 1024 - Q - 2 * P - ONES) / OP;
+  static constexpr int OPS = BITS == 16 ? (FIT > 10 ? 10 : FIT) : 3;               // ring of operand tiles
+  static constexpr int SMEM = 1024 + OPS * OP + Q + 2 * P + ONES;
+  // A weight enters the second product in 16 bits: bf16 has room for any score difference that fp32 sums can bear, fp16
+  // for 2^15; there the reference starts 2^5 below the largest score of its tile, so that weights down to 2^-29 of it keep
+  // all their bits.
+  static constexpr float BIAS = BITS == 16 ? 0.f : 5.f, GROW = BITS == 16 ? 60.f : 15.f;
   static_assert(SMEM <= 220 * 1024, "shared memory");
   static_assert(OPS % TEAMS == 0, "a team meets its slots in every turn, so it sees every phase of their barriers");
   static_assert(OPS <= 2 * TA_FLAGS - 4, "flags");
@@ -149,15 +154,16 @@ __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ bool ta_fixed(const TaSeg& s, int j) { return (s.tile0 + j + 1) * TA_TILE > s.len; }
 
 // Barrier of the softmax warps that returns whether any of them brought true.
-__device__ __forceinline__ bool ta_any(bool mine) {
+template <int THREADS>
+__device__ __forceinline__ bool ta_any(int id, bool mine) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)mine)
+      : "r"((uint32_t)mine), "r"(id), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
   extern __shared__ uint8_t smem_raw[];
   // operand slots: copied into (16-bit caches only), ready for the tensor cores, read
   __shared__ uint64_t load_full[Sh::OPS], op_full[Sh::OPS], op_empty[Sh::OPS];
-  __shared__ uint64_t q_full, s_full[2], p_full, pv_done, fin_bar;
+  __shared__ uint64_t q_full, s_full[2], p_full[2], pv_done[2], checked[2], run_done, fin_bar;   // [tile parity]
   __shared__ uint32_t s_tmem;
   __shared__ int abort_flag, s_bad[TA_FLAGS];
   __shared__ TaPlan plan;
@@ -186,14 +192,16 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
   __shared__ uint64_t s_mask[NB];
   __shared__ long long s_out[NB];
   // of a slow tile: row maxima per warp, rescaling factors, whether some row has no reference yet
-  __shared__ int s_key[TA_SOFT][NB];
+  __shared__ int s_key[TA_GROUP][NB];
   __shared__ float s_fix[NB];
+  __shared__ bool s_unset[NB];                           // rows without a reference yet
   __shared__ int s_failed[TA_SOFT];
+  __shared__ volatile int s_version, s_all_set;          // of the references: counts their changes; every row has one
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const ops = smem;
   uint8_t* const s_q = smem + Sh::OPS * Sh::OP;
   uint8_t* const s_p = s_q + Sh::Q;
-  uint8_t* const s_ones = s_p + Sh::P;
+  uint8_t* const s_ones = s_p + 2 * Sh::P;
   volatile int* abort_v = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -209,15 +217,19 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       mbar_init(&piece_empty[i], TA_TEAM);
     }
     mbar_init(&q_full, 1);
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(&p_full, 1);
-    mbar_init(&pv_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 1);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&checked[i], 1);
+    }
+    mbar_init(&run_done, 1);
     mbar_init(&fin_bar, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < TA_FLAGS) s_bad[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s_version = 0;
   if (threadIdx.x >= 64 && threadIdx.x < 128) {          // 1 KB of ones, in the operand type
     const uint32_t one = RAW16 ? 0x3f803f80u : 0x3c003c00u;
     reinterpret_cast<uint4*>(s_ones)[threadIdx.x - 64] = make_uint4(one, one, one, one);
@@ -370,7 +382,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         for (int i = 0; i < 2 * n && ok; ++i) {
           const bool is_v = i == 2 * n - 1 || (i > 0 && !(i & 1));
           ok = ta_wait(&op_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
-          if (ok && is_v) ok = ta_wait(&p_full, n_p & 1, abort_v, ERR_TIMEOUT_FULL);
+          if (ok && is_v) ok = ta_wait(&p_full[n_p & 1], (n_p >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
           if (!ok) break;
           tc05_fence_after();
           const uint32_t base = ops0 + ring.slot * (Sh::OP >> 4);
@@ -387,7 +399,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
             }
             ++n_s;
           } else {
-            const uint32_t lo = base | LO_V, plo = p0 | LO_P, ones = ones0 | LO_K;
+            const uint32_t lo = base | LO_V, plo = (p0 + (n_p & 1) * (Sh::P >> 4)) | LO_P, ones = ones0 | LO_K;
             const bool more = !(i < 3 && !(i == 1 && n > 1));   // V of the segment's first tile: item 2, or 1 of 2
             if (issuer) {
 #pragma unroll
@@ -395,7 +407,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
                 tc05_mma_f16_lohi(tm + TA_O, lo + kk * (2048 >> 4), HI, plo + kk * (2048 >> 4), HI, id_o, more || kk > 0);
                 tc05_mma_f16_lohi(tm + TA_L, ones, HI_ONES, plo + kk * (2048 >> 4), HI, id_l, more || kk > 0);
               }
-              tc05_commit(&pv_done);
+              tc05_commit(&pv_done[n_p & 1]);
+              if (i == 2 * n - 1) tc05_commit(&run_done);
               tc05_commit(&op_empty[ring.slot]);
             }
             ++n_p;
@@ -585,9 +598,13 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
     }
   } else {
     // ============================================================ softmax, and the ends of segments
-    const int t = threadIdx.x;                          // this thread's token of a tile, and lane of tensor memory
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    uint32_t n_tile = 0;                                // tiles so far: phases of s_full, pv_done
+    // The groups take turns: one weighs its tile while the other's is in the second product.  References change rarely and
+    // one tile at a time: a tile is "checked" once it is known that its scores fit them (or they have been changed to), and
+    // the next tile is not before.  A group that weighed its tile with references that changed meanwhile weighs it again.
+    const int group = warp / TA_GROUP, gw = warp % TA_GROUP, bar = 1 + group;
+    const int t = threadIdx.x % 128;                    // this thread's token of a tile, and lane of tensor memory
+    const uint32_t lanes = (uint32_t)(32 * gw) << 16;
+    uint32_t n0 = 0;                                    // tiles of the runs before: a tile's number gives group and phases
     int n_seg = 0;
     for (long long u = u0; u < u1; ++n_seg) {
       const TaSeg s = ta_segment(p, plan, u, u0, u1);
@@ -598,7 +615,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       // ---------------------------------------------------------- Q into its operand layout, and the rows' constants
       {
         constexpr int CH = D / 8, ROWS = TA_SOFT * 32 / CH;                // 16-byte pieces of a row; rows per pass
-        const int c = t % CH, r_in = t / CH;
+        const int c = threadIdx.x % CH, r_in = threadIdx.x / CH;
         const bool minus = p.scale < 0.f;                                 // the sign goes into q
         for (int r0 = 0; r0 < N; r0 += 2 * ROWS) {
           uint4 raw[2];
@@ -650,22 +667,25 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
                 float* fr = reinterpret_cast<float*>(&s_fr[r / 2]);
                 fr[r & 1] = f;
                 fr[2 + (r & 1)] = 0.f;
+                s_unset[r] = true;
               }
             }
           }
         }
         fence_proxy_async_smem();
-        named_bar_sync(1, TA_SOFT * 32);
-        if (t == 0) mbar_arrive(&q_full);
+        if (threadIdx.x == 0) s_all_set = 0;
+        named_bar_sync(3, TA_SOFT * 32);
+        if (threadIdx.x == 0) mbar_arrive(&q_full);
       }
-      bool unset = true, all_set = false, ok = true;    // row t has no reference yet; every row has one
+      bool ok = true;
       // ---------------------------------------------------------- tiles
-      for (int j = 0; j < s.n; ++j, ++n_tile) {
-        const uint32_t sbuf = tmem + TA_S + 128 * (n_tile & 1) + lanes;
+      for (int j = (group ^ n0) & 1; j < s.n; j += 2) {
+        const uint32_t n_tile = n0 + j, turn = n_tile >> 1;
+        const uint32_t sbuf = tmem + TA_S + 128 * group + lanes, pbuf = smem_u32(s_p) + group * Sh::P;
         const int t0 = (s.tile0 + j) * TA_TILE, back = t0 + t - s.len;   // the token's place among the drafts
         const bool masked = t0 + TA_TILE > s.len;
-        ok = ta_wait(&s_full[n_tile & 1], (n_tile >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
-        if (ok && j > 0) ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);   // P, O and L are free
+        ok = ta_wait(&s_full[group], turn & 1, abort_v, ERR_TIMEOUT_FULL);
+        if (ok && turn > 0) ok = ta_wait(&pv_done[group], (turn - 1) & 1, abort_v, ERR_TIMEOUT_FULL);   // P is free
         tc05_fence_after();
         // Does row r see this token?  Without branches, here and below: a branch per row would keep the rows' chains of
         // load, multiply-add, exponential and rounding from overlapping (47 cycles a row against 6).
@@ -678,7 +698,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
           for (int c = 0; c < N; c += 32) {
             uint32_t v[32];
             tmem_ld32(sbuf + c, v);
-            const uint32_t row = smem_u32(s_p) + (c >> 6) * (TA_TILE * 128) + t * 128;
+            const uint32_t row = pbuf + (c >> 6) * (TA_TILE * 128) + t * 128;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               if (hf && c + 16 >= N) break;
@@ -705,28 +725,28 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
                 sts128(row + (((((c & 63) >> 3) + 2 * hf + y) ^ (t & 7)) << 4), w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
             }
           }
-          return most > TA_GROW;
+          return most > Sh::GROW;
         };
         auto weigh = [&]() -> bool { return masked ? weigh_tile(std::true_type{}) : weigh_tile(std::false_type{}); };
-        bool again = true;                              // until every row has a reference, tiles go the long way
-        if (all_set) {
-          bool grown = false;
-          if (ok) {
-            grown = weigh();
-            fence_proxy_async_smem();
-            tc05_fence_before();
-          }
-          if (lane == 0) s_failed[warp] = !ok;
-          again = ta_any(grown || !ok);
-        } else {
-          if (lane == 0) s_failed[warp] = !ok;
-          ta_any(false);
-        }
-        if (again) {
-          if (s_failed[0] || s_failed[1] || s_failed[2] || s_failed[3]) {  // all four warps leave together
-            ok = false;
+        // until every row has a reference, tiles go the long way
+        const int version = s_version;
+        const bool known = s_all_set;
+        bool grown = false;
+        if (ok && known) grown = weigh();
+        if (ok && n_tile > 0) ok = ta_wait(&checked[group ^ 1], ((n_tile - 1) >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
+        const bool all_known = s_all_set;
+        if (ok && all_known && (!known || version != s_version)) grown = weigh();
+        fence_proxy_async_smem();
+        tc05_fence_before();
+        if (lane == 0) s_failed[warp] = !ok;
+        if (ta_any<128>(bar, grown || !ok || !all_known)) {
+          if (s_failed[4 * group] || s_failed[4 * group + 1] || s_failed[4 * group + 2] || s_failed[4 * group + 3]) {
+            ok = false;                                 // all four warps leave together
             break;
           }
+          // O and L are to be rescaled: the product of the tile before has to be over (the one before that is)
+          if (j > 0) ok = ta_wait(&pv_done[group ^ 1], ((n_tile - 1) >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
+          tc05_fence_after();
           // ------------------------------------------------------ new references
           auto maxima = [&](auto is_masked) {
 #pragma unroll 1
@@ -741,28 +761,32 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
                 const int top = __reduce_max_sync(0xffffffffu, ta_key(z));
                 mine = lane == x ? top : mine;
               }
-              if (lane < 16) s_key[warp][c + lane] = mine;
+              if (lane < 16) s_key[gw][c + lane] = mine;
             }
           };
           if (masked) maxima(std::true_type{}); else maxima(std::false_type{});
-          named_bar_sync(1, TA_SOFT * 32);
+          named_bar_sync(bar, 128);
           bool late = false;
           if (t < N) {
             const float top = ta_unkey(max(max(s_key[0][t], s_key[1][t]), max(s_key[2][t], s_key[3][t])));
             float* nref = &reinterpret_cast<float*>(&s_fr[t / 2])[2 + (t & 1)];
             float fix = 1.f;
-            if (unset) {                                // no weight so far: O and L are zero (or NaN, which stays)
-              unset = !(top > -INFINITY);               // nothing visible yet (or a NaN, which needs no reference)
-              if (!unset) *nref = TA_BIAS - top;
-            } else if (top + *nref > TA_GROW) {
-              const float now = TA_BIAS - top;
+            if (s_unset[t]) {                           // no weight so far: O and L are zero (or NaN, which stays)
+              s_unset[t] = !(top > -INFINITY);          // nothing visible yet (or a NaN, which needs no reference)
+              if (!s_unset[t]) *nref = Sh::BIAS - top;
+            } else if (top + *nref > Sh::GROW) {
+              const float now = Sh::BIAS - top;
               fix = ta_exp2(now - *nref);
               *nref = now;
             }
             s_fix[t] = fix;
-            late = unset && t < s.rows;
+            late = s_unset[t] && t < s.rows;
           }
-          all_set = !ta_any(late);
+          late = ta_any<128>(bar, late);
+          if (t == 0) {
+            s_all_set = !late;
+            ++s_version;
+          }
           if (j > 0) {
 #pragma unroll 1
             for (int c = 0; c < 2 * N; c += 16) {       // O, then L
@@ -772,9 +796,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
               tmem_ld16(at, o);
               uint32_t x[16];
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                x[y] = __float_as_uint(o[y] * s_fix[r + y]);
-              }
+              for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(o[y] * s_fix[r + y]);
               tmem_st16(at, x);
             }
             tmem_st_wait();
@@ -782,21 +804,27 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
           weigh();
           fence_proxy_async_smem();
           tc05_fence_before();
-          named_bar_sync(1, TA_SOFT * 32);
+          if (lane == 0) s_failed[warp] = !ok;
+          if (ta_any<128>(bar, !ok)) {
+            ok = false;
+            break;
+          }
         }
-        if (t == 0) mbar_arrive(&p_full);
+        if (t == 0) {
+          mbar_arrive(&p_full[group]);
+          mbar_arrive(&checked[group]);
+        }
       }
-      if (!ok) break;
+      n0 += s.n;
       // ---------------------------------------------------------- the end of the run: lane = element, column = row
-      ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);
-      if (lane == 0) s_failed[warp] = !ok;
-      if (ta_any(!ok)) break;
+      if (ok) ok = ta_wait(&run_done, n_seg & 1, abort_v, ERR_TIMEOUT_FULL);
+      if (ta_any<256>(3, !ok)) break;                   // both groups go on together or not at all
       tc05_fence_after();
       // codes of 4 bits stand at another position inside each 8 elements
       const int d = BITS == 4 ? (t & ~7) + ((t & 7) >> 1) + 4 * (t & 1) : t;
       auto finish = [&](auto is_whole) {
 #pragma unroll 1
-        for (int c = 0; c < N; c += 16) {
+        for (int c = 16 * group; c < N; c += 32) {
           float o[16], l[16];
           tmem_ld16(tmem + lanes + TA_O + c, o);
           tmem_ld16(tmem + lanes + TA_L + c, l);
@@ -826,10 +854,11 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       if (t < D) {
         if (whole) finish(std::true_type{}); else finish(std::false_type{});
       }
-      if (s_bad[n_seg % TA_FLAGS] && t < D) {
+      if (s_bad[n_seg % TA_FLAGS]) {
         // V held infinities or NaN in drafted tokens, which were left out of the products: the rows that see one get it here
+        named_bar_sync(3, TA_SOFT * 32);                // the values to add to are written
 #pragma unroll 1
-        for (int r = 0; r < s.rows; ++r) {
+        for (int r = group; t < D && r < s.rows; r += 2) {
           float extra = 0.f;
 #pragma unroll 1
           for (int i = 0; i < s.m; ++i) {
@@ -847,9 +876,9 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         }
       }
       tc05_fence_before();
-      named_bar_sync(1, TA_SOFT * 32);                  // the rows' constants and O are free for the next run
+      named_bar_sync(3, TA_SOFT * 32);                  // the rows' constants and O are free for the next run
       tc05_fence_after();
-      if (t == 0) s_bad[n_seg % TA_FLAGS] = 0;
+      if (threadIdx.x == 0) s_bad[n_seg % TA_FLAGS] = 0;
     }
   }
   tc05_fence_before();
