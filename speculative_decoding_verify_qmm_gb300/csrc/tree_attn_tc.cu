@@ -30,17 +30,22 @@ constexpr int TA_TILE = 128;                       // tokens per tile: the lanes
 constexpr int TA_GROUP = 4, TA_SOFT = 2 * TA_GROUP;  // two groups of four softmax warps (0-7), for even and odd tiles
 constexpr int TA_TEAM = 4;                         // warps of a transforming team
 constexpr int TA_FLAGS = 16;                       // segments whose flags are alive at once (ring depth / 2 at most)
-constexpr uint32_t TA_S = 0, TA_O = 256, TA_L = 384;  // tensor-memory columns: two S buffers of 128; O; L
+constexpr uint32_t TA_S = 0, TA_O = 256, TA_L = 384;  // tensor-memory columns: the S buffers; O; L
 
 // NB: rows per item at most.  Warps: softmax, transforming teams, the copying warp, the MMA warp.
 template <int D, int BITS, int NB>
 struct TaShape {
-  static constexpr int TEAMS = BITS == 16 ? 1 : 3;
-  static constexpr int PROD = TA_SOFT + TEAMS * TA_TEAM, MMA = PROD + 1, THREADS = (MMA + 1) * 32;
+  // Items of up to 64 rows: two issuing warps, one for each product (an instruction takes its warp some 70 cycles to issue,
+  // more than such an item's products run), and a ring in which K and V alternate.  Wider items need the shared memory for
+  // Q and P: three slots, one issuing warp, K a tile ahead of V.
+  static constexpr bool SPLIT = NB == 64;
+  static constexpr int SB = 256 / NB;                                              // S buffers
+  static constexpr int TEAMS = BITS == 16 ? 1 : (SPLIT ? 4 : 3);
+  static constexpr int PROD = TA_SOFT + TEAMS * TA_TEAM, MMA = PROD + 1, MMA2 = MMA + SPLIT, THREADS = (MMA2 + 1) * 32;
   static constexpr int OP = TA_TILE * D * 2;                                       // one operand tile, 16 bits a value
   static constexpr int Q = NB * D * 2, P = NB / 64 * TA_TILE * 128, ONES = 1024;
   static constexpr int FIT = (218 * 1024 - Q - 2 * P - ONES) / OP;
-  static constexpr int OPS = BITS == 16 ? (FIT > 10 ? 10 : FIT) : 3;               // ring of operand tiles
+  static constexpr int OPS = BITS == 16 ? (FIT > 10 ? 10 : (SPLIT ? FIT & ~1 : FIT)) : (SPLIT ? 4 : 3);  // ring of operand tiles
   static constexpr int SMEM = 1024 + OPS * OP + Q + 2 * P + ONES;
   // A weight enters the second product in 16 bits: bf16 has room for any score difference that fp32 sums can bear, fp16
   // for 2^15; there the reference starts 2^5 below the largest score of its tile, so that weights down to 2^-29 of it keep
@@ -48,16 +53,20 @@ struct TaShape {
   static constexpr float BIAS = BITS == 16 ? 0.f : 5.f, GROW = BITS == 16 ? 60.f : 15.f;
   static_assert(SMEM <= 220 * 1024, "shared memory");
   static_assert(OPS % TEAMS == 0, "a team meets its slots in every turn, so it sees every phase of their barriers");
+  static_assert(!SPLIT || OPS % 2 == 0, "each product's slots are its own");
   static_assert(OPS <= 2 * TA_FLAGS - 4, "flags");
 };
 
-// Order of a segment's operand tiles: K0, K1, V0, K2, V1, ..., V(n-1).
+// Order of a run's operand tiles.  SPLIT: K0, V0, K1, V1, ...; else K0, K1, V0, K2, V1, ..., V(n-1).  Sets the tile; true: V.
+template <bool SPLIT>
 __device__ __forceinline__ bool ta_item(int e, int n, int* tile) {
-  if (e == 0) { *tile = 0; return false; }
-  if (e == 2 * n - 1) { *tile = n - 1; return true; }
-  if (e & 1) { *tile = (e + 1) / 2; return false; }
-  *tile = e / 2 - 1;
-  return true;
+  if constexpr (SPLIT) {
+    *tile = e >> 1;
+    return e & 1;
+  }
+  const bool is_v = e == 2 * n - 1 || (e > 0 && !(e & 1));
+  *tile = e == 2 * n - 1 ? n - 1 : (is_v ? e / 2 - 1 : (e + 1) / 2);
+  return is_v;
 }
 
 // One operand tile of codes as the transforming warps need it: the cache's token index of each 16 tokens (-1: past the
@@ -181,7 +190,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
   extern __shared__ uint8_t smem_raw[];
   // operand slots: copied into (16-bit caches only), ready for the tensor cores, read
   __shared__ uint64_t load_full[Sh::OPS], op_full[Sh::OPS], op_empty[Sh::OPS];
-  __shared__ uint64_t q_full, s_full[2], p_full[2], pv_done[2], checked[2], run_done, fin_bar;   // [tile parity]
+  __shared__ uint64_t q_full, s_full[Sh::SB], s_free[Sh::SB], run_done, fin_bar[2];
+  __shared__ uint64_t p_full[2], pv_done[2], checked[2];  // [tile parity]
   __shared__ uint32_t s_tmem;
   __shared__ int abort_flag, s_bad[TA_FLAGS];
   __shared__ TaPlan plan;
@@ -217,14 +227,18 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       mbar_init(&piece_empty[i], TA_TEAM);
     }
     mbar_init(&q_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < Sh::SB; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&p_full[i], 1);
       mbar_init(&pv_done[i], 1);
       mbar_init(&checked[i], 1);
     }
     mbar_init(&run_done, 1);
-    mbar_init(&fin_bar, 1);
+    mbar_init(&fin_bar[0], 1);
+    mbar_init(&fin_bar[1], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -268,13 +282,13 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         int page_before = 0, page_k = 0, page_next = page_of(0);   // of the last two K tiles, and the next one's
         for (int i = 0; i < 2 * s.n; ++i) {
           int j;
-          const bool is_v = ta_item(i, s.n, &j);
+          const bool is_v = ta_item<Sh::SPLIT>(i, s.n, &j);
           if (!is_v) {
             page_before = page_k;
             page_k = page_next;
             page_next = page_of(j + 1);
           }
-          int page = is_v && i != 2 * s.n - 1 ? page_before : page_k;
+          int page = !Sh::SPLIT && is_v && i != 2 * s.n - 1 ? page_before : page_k;
           ok = ta_wait(&op_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
           if (!ok) break;
           const int t0 = (s.tile0 + j) * TA_TILE;
@@ -316,13 +330,13 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         int page_before = 0, page_k = 0, page_next = page_of(0);   // of the last two K tiles, and the next one's
         for (int i = 0; i < 2 * s.n; ++i) {
           int j;
-          const bool is_v = ta_item(i, s.n, &j);
+          const bool is_v = ta_item<Sh::SPLIT>(i, s.n, &j);
           if (!is_v) {
             page_before = page_k;
             page_k = page_next;
             page_next = page_of(j + 1);
           }
-          int page = is_v && i != 2 * s.n - 1 ? page_before : page_k;
+          int page = !Sh::SPLIT && is_v && i != 2 * s.n - 1 ? page_before : page_k;
           ok = ta_wait(&piece_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
           if (!ok) break;
           const int t0 = (s.tile0 + j) * TA_TILE, t = t0 + 16 * lane;
@@ -352,11 +366,12 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         ring.next();
       }
     }
-  } else if (warp == Sh::MMA) {
+  } else if (warp >= Sh::MMA) {
     // ============================================================ MMA issue
     // The whole warp runs the loop and one lane issues, so that descriptors and addresses live in uniform registers.
     {
       TaRing<Sh::OPS> ring;
+      if (Sh::SPLIT && warp == Sh::MMA2) ring.next();   // V's slots are the odd ones
       uint32_t n_q = 0, n_s = 0, n_p = 0;               // phases seen of each barrier
       bool ok = true;
       const bool issuer = elect_one();
@@ -378,52 +393,82 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         const int N = (rows + 15) & ~15;
         const uint32_t id_s = f16_idesc_ex(TA_TILE, N, RAW16, false, false), id_o = f16_idesc_ex(TA_TILE, N, RAW16, true, true),
                        id_l = f16_idesc_ex(TA_TILE, N, RAW16, false, true);
-        ok = ta_wait(&q_full, n_q++ & 1, abort_v, ERR_TIMEOUT_FULL);
-        for (int i = 0; i < 2 * n && ok; ++i) {
-          const bool is_v = i == 2 * n - 1 || (i > 0 && !(i & 1));
-          ok = ta_wait(&op_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
-          if (ok && is_v) ok = ta_wait(&p_full[n_p & 1], (n_p >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
-          if (!ok) break;
-          tc05_fence_after();
-          const uint32_t base = ops0 + ring.slot * (Sh::OP >> 4);
-          if (!is_v) {
-            // S buffer of tile n_s: P of tile n_s - 2 was handed over before the product issued last, so S has been read
-            const uint32_t d = tm + TA_S + 128 * (n_s & 1), lo = base | LO_K, qlo = q0 | LO_K;
-            if (issuer) {
+        // S = K Q^T of tile n_s
+        auto scores = [&](uint32_t base) {
+          const uint32_t d = tm + TA_S + NB * (n_s % Sh::SB), lo = base | LO_K, qlo = q0 | LO_K;
+          if (issuer) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                tc05_mma_f16_lohi(d, lo + (kk >> 2) * (TA_TILE * 128 >> 4) + (kk & 3) * 2, HI,
-                                  qlo + (kk >> 2) * (NB * 128 >> 4) + (kk & 3) * 2, HI, id_s, kk > 0);
-              tc05_commit(&s_full[n_s & 1]);
-              tc05_commit(&op_empty[ring.slot]);
-            }
-            ++n_s;
-          } else {
-            const uint32_t lo = base | LO_V, plo = (p0 + (n_p & 1) * (Sh::P >> 4)) | LO_P, ones = ones0 | LO_K;
-            const bool more = !(i < 3 && !(i == 1 && n > 1));   // V of the segment's first tile: item 2, or 1 of 2
-            if (issuer) {
-#pragma unroll
-              for (int kk = 0; kk < TA_TILE / 16; ++kk) {
-                tc05_mma_f16_lohi(tm + TA_O, lo + kk * (2048 >> 4), HI, plo + kk * (2048 >> 4), HI, id_o, more || kk > 0);
-                tc05_mma_f16_lohi(tm + TA_L, ones, HI_ONES, plo + kk * (2048 >> 4), HI, id_l, more || kk > 0);
-              }
-              tc05_commit(&pv_done[n_p & 1]);
-              if (i == 2 * n - 1) tc05_commit(&run_done);
-              tc05_commit(&op_empty[ring.slot]);
-            }
-            ++n_p;
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc05_mma_f16_lohi(d, lo + (kk >> 2) * (TA_TILE * 128 >> 4) + (kk & 3) * 2, HI,
+                                qlo + (kk >> 2) * (NB * 128 >> 4) + (kk & 3) * 2, HI, id_s, kk > 0);
+            tc05_commit(&s_full[n_s % Sh::SB]);
+            tc05_commit(&op_empty[ring.slot]);
           }
-          __syncwarp();
-          ring.next();
+          ++n_s;
+        };
+        // O += V^T P^T and L += 1 P^T of tile n_p
+        auto values = [&](uint32_t base, bool first, bool last) {
+          const uint32_t lo = base | LO_V, plo = (p0 + (n_p & 1) * (Sh::P >> 4)) | LO_P, ones = ones0 | LO_K;
+          if (issuer) {
+#pragma unroll
+            for (int kk = 0; kk < TA_TILE / 16; ++kk) {
+              tc05_mma_f16_lohi(tm + TA_O, lo + kk * (2048 >> 4), HI, plo + kk * (2048 >> 4), HI, id_o, !first || kk > 0);
+              tc05_mma_f16_lohi(tm + TA_L, ones, HI_ONES, plo + kk * (2048 >> 4), HI, id_l, !first || kk > 0);
+            }
+            tc05_commit(&pv_done[n_p & 1]);
+            tc05_commit(&op_empty[ring.slot]);
+            if (last) tc05_commit(&run_done);
+          }
+          ++n_p;
+        };
+        if constexpr (Sh::SPLIT) {
+          if (warp == Sh::MMA) {
+            ok = ta_wait(&q_full, n_q++ & 1, abort_v, ERR_TIMEOUT_FULL);
+            for (int j = 0; j < n && ok; ++j) {
+              if (n_s >= Sh::SB) ok = ta_wait(&s_free[n_s % Sh::SB], (n_s / Sh::SB - 1) & 1, abort_v, ERR_TIMEOUT_FULL);
+              if (ok) ok = ta_wait(&op_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
+              if (!ok) break;
+              tc05_fence_after();
+              scores(ops0 + ring.slot * (Sh::OP >> 4));
+              __syncwarp();
+              ring.next(2);
+            }
+          } else {
+            for (int j = 0; j < n && ok; ++j) {
+              ok = ta_wait(&op_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
+              if (ok) ok = ta_wait(&p_full[n_p & 1], (n_p >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
+              if (!ok) break;
+              tc05_fence_after();
+              values(ops0 + ring.slot * (Sh::OP >> 4), j == 0, j == n - 1);
+              __syncwarp();
+              ring.next(2);
+            }
+          }
+        } else {
+          ok = ta_wait(&q_full, n_q++ & 1, abort_v, ERR_TIMEOUT_FULL);
+          for (int i = 0; i < 2 * n && ok; ++i) {
+            int j;
+            const bool is_v = ta_item<false>(i, n, &j);
+            ok = ta_wait(&op_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
+            if (ok && is_v) ok = ta_wait(&p_full[n_p & 1], (n_p >> 1) & 1, abort_v, ERR_TIMEOUT_FULL);
+            if (ok && !is_v && n_s >= Sh::SB) ok = ta_wait(&s_free[n_s % Sh::SB], (n_s / Sh::SB - 1) & 1, abort_v, ERR_TIMEOUT_FULL);
+            if (!ok) break;
+            tc05_fence_after();
+            if (is_v) values(ops0 + ring.slot * (Sh::OP >> 4), j == 0, j == n - 1);
+            else scores(ops0 + ring.slot * (Sh::OP >> 4));
+            __syncwarp();
+            ring.next();
+          }
         }
         u += n;
       }
       // no MMA may still be running when the tensor memory is freed: this wait
       // ignores the abort flag and ends only on completion or the time limit
       if (issuer) {
-        tc05_commit(&fin_bar);
+        uint64_t* const mine = &fin_bar[warp - Sh::MMA];
+        tc05_commit(mine);
         volatile int never = 0;
-        mbar_wait_bounded(&fin_bar, 0, &never);
+        mbar_wait_bounded(mine, 0, &never);
       }
       __syncwarp();
     }
@@ -439,7 +484,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         const TaSeg s = ta_segment(p, plan, u, u0, u1);
         for (int i = 0; i < 2 * s.n; ++i, ring.next()) {
           int j;
-          const bool is_v = ta_item(i, s.n, &j);
+          const bool is_v = ta_item<Sh::SPLIT>(i, s.n, &j);
           ok = ta_wait(&load_full[ring.slot], ring.phase, abort_v, ERR_TIMEOUT_FULL);
           if (!ok) break;
           const int pos = (s.tile0 + j) * TA_TILE + t;
@@ -681,10 +726,10 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       // ---------------------------------------------------------- tiles
       for (int j = (group ^ n0) & 1; j < s.n; j += 2) {
         const uint32_t n_tile = n0 + j, turn = n_tile >> 1;
-        const uint32_t sbuf = tmem + TA_S + 128 * group + lanes, pbuf = smem_u32(s_p) + group * Sh::P;
+        const uint32_t sbuf = tmem + TA_S + NB * (n_tile % Sh::SB) + lanes, pbuf = smem_u32(s_p) + group * Sh::P;
         const int t0 = (s.tile0 + j) * TA_TILE, back = t0 + t - s.len;   // the token's place among the drafts
         const bool masked = t0 + TA_TILE > s.len;
-        ok = ta_wait(&s_full[group], turn & 1, abort_v, ERR_TIMEOUT_FULL);
+        ok = ta_wait(&s_full[n_tile % Sh::SB], (n_tile / Sh::SB) & 1, abort_v, ERR_TIMEOUT_FULL);
         if (ok && turn > 0) ok = ta_wait(&pv_done[group], (turn - 1) & 1, abort_v, ERR_TIMEOUT_FULL);   // P is free
         tc05_fence_after();
         // Does row r see this token?  Without branches, here and below: a branch per row would keep the rows' chains of
@@ -812,6 +857,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
         }
         if (t == 0) {
           mbar_arrive(&p_full[group]);
+          mbar_arrive(&s_free[n_tile % Sh::SB]);
           mbar_arrive(&checked[group]);
         }
       }
