@@ -8,7 +8,7 @@
 
 namespace sv {
 
-constexpr int TA_MAX_BLOCK = 128;
+constexpr int TA_MAX_BLOCK = 128, TA_NARROW_ROWS = 32;
 
 // Joins the partial sums of items that spanned CTAs, in CTA order; a warp per (row, query head).
 template <int D>
@@ -142,14 +142,15 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
     if (m * p.group > rows) rows = m * p.group;
   }
   // Items of up to 64 rows leave more shared memory to the ring of operand tiles; wider requests take items of 128.
-  p.block = rows <= 64 ? 64 : TA_MAX_BLOCK;
+  const bool narrow = rows <= TA_NARROW_ROWS;
+  p.block = narrow ? (rows <= 16 ? 16 : 32) : (rows <= 64 ? 64 : TA_MAX_BLOCK);
   // the lengths are on the device: size the grid for the longest the table allows
   const long long most_units = (((long long)table_pages << p.c.page_shift) + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
   long long most = 0;
   for (int b = 0; b < B; ++b)
     most += (long long)p.c.heads * ta_blocks((p.map.offs[b + 1] - p.map.offs[b]) * p.group, p.block) * most_units;
   p.grid = most < sms ? (int)most : sms;
-  if (p.c.bits == 16) {
+  if (p.c.bits == 16 && !narrow) {
     const uint64_t slabs = (uint64_t)p.c.n_pages * p.c.heads, page = 1ull << p.c.page_shift;
     const uint32_t box = page < 128 ? (uint32_t)page : 128u;
     st = encode_tiled_3d_sw128(&p.tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.c.p.k, p.c.dim, page, slabs, 2, 64, box);
@@ -157,7 +158,7 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
     if (st) return st;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_tree_attn(p, s);
+  cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn(p, s);
   if (e == cudaSuccess && most_units > 1) e = p.c.dim == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "tree attention launch");
 }

@@ -1,0 +1,618 @@
+// Tree attention of few rows (drafted rows x query heads per key head), with warp-level matrix instructions.
+//
+//   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q . k_t - max)
+//
+// Bound by memory: with 16 rows a cached byte meets 16 to 64 multiply-adds, far below what warp-level MMA gives, so the
+// point is to keep loads in flight and instructions per cached byte few.  A warp works alone: it owns every W-th step of
+// 16 tokens of the CTA's run, with its own ring of cp.async stages in shared memory, its own running maximum, weight and
+// sums in registers, and no barrier until the run ends, where the warps' sums are joined in warp order.
+//
+// Codes become MMA operands in registers, without a second trip through shared memory.  S = Q K^T: the contraction may run
+// over a head's elements in any order, so the lane that holds column q of a token's k-slices takes whole 16-byte pieces of
+// its codes and Q is laid out to match.  O += P V: P's accumulator layout is the A operand's; V's pairs (two tokens, one
+// element) come from byte shuffles of the two tokens' words, and the output's columns are numbered so that a lane owns a
+// contiguous piece of a V row.  fp16 s * c + b with the exact code (half an fp16 step); Q enters as fp16 scaled by a power of
+// two per row; 16-bit caches go through bf16 MMA as they are.
+//
+// MT row tiles of 16 per warp; RG row groups of warps read the same steps for different rows.
+#include <type_traits>
+
+#include "tree_attn.cuh"
+
+namespace sv {
+
+constexpr int TN_STEP = 16;  // tokens per warp step
+
+template <int D, int BITS, int MT, int RG>
+struct TnShape {
+  static constexpr int W = MT == 1 && BITS != 16 ? 16 : 8, WS = W / RG;        // warps; warps per row group
+  static constexpr int THREADS = 32 * W, BLOCK = 16 * MT * RG;
+  static constexpr int ROWB = D * BITS / 8, G = D / GROUP;
+  static constexpr int SIDE = BITS == 16 ? 0 : TN_STEP * G * 2;                 // one array of scales or biases
+  static constexpr int STAGE = 2 * TN_STEP * ROWB + 4 * SIDE;
+  static constexpr int QBYTES = RG * MT * (D / 16) * 512;
+  static constexpr int LD = D == 128 ? 144 : 72;                                // floats per row of a joined tile (conflict-free)
+  static constexpr int TILE = 16 * LD * 4, JOIN = 8 * TILE;
+  static constexpr int BUDGET = 218 * 1024 - QBYTES;
+  static constexpr int FIT = BUDGET / (W * STAGE);
+  static constexpr int NST = FIT > 8 ? 8 : FIT;
+  static constexpr int RING = W * NST * STAGE;
+  static constexpr int SMEM = QBYTES + (RING > JOIN ? RING : JOIN);             // the join's tiles lie in the drained ring
+  static_assert(NST >= 2, "stages");
+  // as in the kernel for many rows: room for a score to outgrow its row's reference, in the weights' 16-bit type
+  static constexpr float BIAS = BITS == 16 ? 0.f : 5.f, GROW = BITS == 16 ? 60.f : 15.f;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <bool BF16>
+__device__ __forceinline__ void tn_mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t tn_fma(uint32_t biased, uint32_t s2, uint32_t b2) {  // (biased - 1024) * s + b
+  const __half2 k1024 = __half2half2(__ushort_as_half((unsigned short)0x6400));
+  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&s2), __hsub2(*reinterpret_cast<const __half2*>(&biased), k1024),
+                            *reinterpret_cast<const __half2*>(&b2));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], int at, const uint8_t* p) {
+  if constexpr (N >= 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[at] = v.x; w[at + 1] = v.y; w[at + 2] = v.z; w[at + 3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+__device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint32_t lds16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+
+// Which of the lane's elements are the four of k-slice kk: (b0 low, b0 high, b1 low, b1 high).
+template <int BITS>
+__device__ __forceinline__ int tn_k_pick(int kk, int i) {
+  if (BITS != 4) return 4 * kk + i;
+  return 8 * (kk / 2) + 2 * (kk & 1) + (i >> 1) + 4 * (i & 1);
+}
+// Element of output column `col` of n-tile nt: a lane's share of a V row is contiguous.
+template <int D, int BITS>
+__device__ __forceinline__ int tn_v_elem(int nt, int col) {
+  if (D == 128 && BITS == 16) return (nt >> 3) * 64 + 8 * col + (nt & 7);
+  return (D / 8) * col + nt;
+}
+
+template <int D, int BITS, int MT, int RG>
+__global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_attn_narrow_kernel(const __grid_constant__ TreeAttnParams p) {
+  using Sh = TnShape<D, BITS, MT, RG>;
+  constexpr bool RAW16 = BITS == 16;
+  constexpr int ROWB = Sh::ROWB, CPR = ROWB / 16, G = Sh::G, NST = Sh::NST, KK = D / 16, NT = D / 8;
+  constexpr int KW = D * BITS / 128, VW = D * BITS / 256;   // 32-bit words of a lane's share of a K row, of a V row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ TaPlan plan;
+  __shared__ float s_f[Sh::BLOCK], s_max[Sh::W][16 * MT], s_sum[Sh::W][16 * MT];
+  __shared__ long long s_out[Sh::BLOCK];                   // where each row of the block is written (elements)
+  __shared__ int s_odd;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int rg = warp % RG, ws = warp / RG;
+  uint4* const qf = reinterpret_cast<uint4*>(smem);         // [RG * MT][KK][32]
+  uint8_t* const ring = smem + Sh::QBYTES + warp * NST * Sh::STAGE;
+  const uint32_t ring_a = smem_u32(ring);
+  float* const tiles = reinterpret_cast<float*>(smem + Sh::QBYTES);
+
+  pdl_trigger();
+  pdl_wait();
+  if (warp == 0) ta_plan(p, &plan, blockIdx.x == 0);
+  __syncthreads();
+  const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
+  const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
+  const int pm = (1 << p.c.page_shift) - 1;
+
+  for (long long u = u0; u < u1;) {
+    const TaSeg s = ta_segment(p, plan, u, u0, u1);
+    u += s.n;
+    // ------------------------------------------------------------ the ring's first copies
+    const int r0 = rg * 16 * MT;                                            // this warp's first row of the block
+    const int mts = s.rows <= r0 ? 0 : (s.rows - r0 > 16 ? MT : 1);         // its row tiles with rows
+    const int first = s.tile0 << (TA_UNIT_SHIFT - 4), all = (s.total + TN_STEP - 1) / TN_STEP;   // in steps
+    const int mine = (all - first < s.n << (TA_UNIT_SHIFT - 4) ? all - first : s.n << (TA_UNIT_SHIFT - 4)) - ws;
+    const int steps = mts && mine > 0 ? (mine + Sh::WS - 1) / Sh::WS : 0;
+    int pages = 0;                                                          // lane i: the page of step (base + i)
+    auto load_pages = [&](int base) {
+      const int k = base + lane;
+      pages = 0;
+      if (k < steps) {
+        const int t = (first + ws + k * Sh::WS) * TN_STEP;
+        pages = p.table[(size_t)s.b * p.table_pages + (t >> p.c.page_shift)];
+      }
+    };
+    load_pages(0);
+    auto issue = [&](int k) {
+      if (k < steps) {
+        if (k && !(k & 31)) load_pages(k);
+        int page = __shfl_sync(0xffffffffu, pages, k & 31);
+        if ((unsigned)page >= (unsigned)p.c.n_pages) {
+          raise_error(ERR_BAD_INPUT);
+          page = 0;                                                          // stay inside the arrays: the result is undefined
+        }
+        const int t = (first + ws + k * Sh::WS) * TN_STEP;
+        const size_t tok = kv_token(p.c, page, s.h, t & pm);
+        const uint32_t st = ring_a + (k % NST) * Sh::STAGE;
+        const uint8_t *ks = p.c.p.k + tok * ROWB, *vs = p.c.p.v + tok * ROWB;
+#pragma unroll
+        for (int i = 0; i < CPR / 2; ++i) {
+          // chunk c of token r; the place of a chunk in its row keeps the lanes that read together on different banks
+          const int id = i * 32 + lane, r = id / CPR, c = id % CPR;
+          const int fk = CPR >= 8 ? (r & 1) << 2 : 0;
+          const int fv = CPR >= 8 ? ((r >> 1) & 3) << 1 : (CPR == 4 ? (r >> 1) & 3 : 0);
+          cp_async16(st + r * ROWB + ((c ^ fk) << 4), ks + id * 16);
+          cp_async16(st + TN_STEP * ROWB + r * ROWB + ((c ^ fv) << 4), vs + id * 16);
+        }
+        if constexpr (!RAW16) {
+          constexpr int SC = Sh::SIDE / 16;                                  // chunks of one array
+          if (lane < 4 * SC) {
+            const int a = lane / SC, c = lane % SC;
+            const __half* src = (a == 0 ? p.c.p.ks : (a == 1 ? p.c.p.kb : (a == 2 ? p.c.p.vs : p.c.p.vb))) + tok * G;
+            cp_async16(st + 2 * TN_STEP * ROWB + lane * 16, reinterpret_cast<const uint8_t*>(src) + c * 16);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < NST - 1; ++k) issue(k);
+    // ------------------------------------------------------------ Q, as A operands
+    if (threadIdx.x == 0) s_odd = 0;
+    const bool minus = p.scale < 0.f;                                       // the sign goes into q
+    for (int t = warp; t < RG * MT; t += Sh::W) {
+      // this lane's share of two rows: the elements that its share of a K row meets
+      constexpr int PE = D * BITS >= 512 ? 128 / BITS : D / 4, NP = D / 4 / PE;
+      uint4 raw[2][D / 32];
+      bool real[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = 16 * t + 8 * i + g;
+        real[i] = k < s.rows;
+        const int r = s.rb * p.block + k, di = real[i] ? r / p.group : 0, hg = real[i] ? r - di * p.group : 0;
+        const __nv_bfloat16* src = p.q + (size_t)(s.row0 + di) * p.ldq + (s.h * p.group + hg) * D;
+#pragma unroll
+        for (int c = 0; c < NP; ++c)
+#pragma unroll
+          for (int y = 0; y < PE / 8; ++y)
+            raw[i][c * (PE / 8) + y] = real[i] ? *reinterpret_cast<const uint4*>(src + (4 * c + q) * PE + 8 * y) : make_uint4(0, 0, 0, 0);
+      }
+      float up[2] = {minus ? -1.f : 1.f, minus ? -1.f : 1.f};
+      float f[2];
+      f[0] = f[1] = fabsf(p.scale) * 1.4426950408889634f;
+      auto elem = [&](int i, int e) -> float {           // the e-th of the share
+        const uint4 v = raw[i][e / 8];
+        const uint32_t w = (e / 2) % 4 == 0 ? v.x : ((e / 2) % 4 == 1 ? v.y : ((e / 2) % 4 == 2 ? v.z : v.w));
+        return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+      };
+      if constexpr (!RAW16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = 0.f;
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) mx = fmaxf(mx, fabsf(elem(i, e)));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int ex = scale_exponent(mx);
+          up[i] *= pow2_exact(ex);
+          f[i] *= pow2_exact(-ex);
+        }
+      }
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        float x[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = elem(i, tn_k_pick<BITS>(kk, e)) * up[i];
+        qf[(t * KK + kk) * 32 + lane] = make_uint4(ta_pack(x[0][0], x[0][1], RAW16), ta_pack(x[1][0], x[1][1], RAW16),
+                                                   ta_pack(x[0][2], x[0][3], RAW16), ta_pack(x[1][2], x[1][3], RAW16));
+      }
+      if (q < 2) {
+        const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = r / p.group;
+        s_f[k] = f[q];
+        s_out[k] = s.n == s.nt ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
+                               : (long long)(ta_slot(s) * p.block + k) * D;
+      }
+    }
+    __syncthreads();
+    // ------------------------------------------------------------ this warp's rows
+    float o[MT][NT][4], f[MT][2], nref[MT][2], lim[MT][2], sum[MT][2];   // nref: minus the reference, lim: how far a score may outgrow it
+    uint64_t bits[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[m][n][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = r0 + 16 * m + 8 * i + g, r = s.rb * p.block + k;
+        f[m][i] = s_f[k];
+        nref[m][i] = 0.f;
+        lim[m][i] = -INFINITY;                           // no reference yet
+        sum[m][i] = 0.f;
+        const int di = k < s.rows ? r / p.group : 0;
+        bits[m][i] = k < s.rows ? ta_mask(p, s.row0 + di, di, s.m) : 0;
+      }
+    }
+    const uint4* const qw = qf + (rg * MT) * KK * 32 + lane;
+    // One step.  Whether it is masked and how many row tiles it has are fixed at compile time: branches inside would keep the
+    // independent chains of conversions and products from overlapping.
+    auto step = [&](const uint8_t* st, int t0, auto is_masked, auto row_tiles) {
+      constexpr bool masked = decltype(is_masked)::value;
+      constexpr int MS = decltype(row_tiles)::value;
+      {
+        // ---------------------------------------------------------- S = Q K^T
+        float sc[MS][2][4];
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.f;
+        {
+          uint32_t w[2][KW], s2[2][2], b2[2][2];                             // [token half][group of the piece]
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int r = 8 * n + g;
+            const uint8_t* row = st + r * ROWB;
+            if constexpr (KW >= 4) {
+#pragma unroll
+              for (int c = 0; c < KW / 4; ++c) lds_words(w[n], 4 * c, row + (((4 * c + q) ^ (CPR >= 8 ? (r & 1) << 2 : 0)) << 4));
+            } else {
+              lds_words(w[n], 0, row + q * 8);
+            }
+            if constexpr (!RAW16) {
+              const uint8_t* side = st + 2 * TN_STEP * ROWB + r * (2 * G);
+              if constexpr (G == 2) {
+                const uint32_t a = lds32(side), b = lds32(side + Sh::SIDE);
+                if constexpr (KW == 8) {                                     // piece 0 is group 0, piece 1 group 1
+                  s2[n][0] = __byte_perm(a, 0, 0x1010); s2[n][1] = __byte_perm(a, 0, 0x3232);
+                  b2[n][0] = __byte_perm(b, 0, 0x1010); b2[n][1] = __byte_perm(b, 0, 0x3232);
+                } else {                                                     // one piece: group q / 2
+                  s2[n][0] = s2[n][1] = __byte_perm(a, 0, q & 2 ? 0x3232 : 0x1010);
+                  b2[n][0] = b2[n][1] = __byte_perm(b, 0, q & 2 ? 0x3232 : 0x1010);
+                }
+              } else {
+                s2[n][0] = s2[n][1] = __byte_perm(lds16(side), 0, 0x1010);
+                b2[n][0] = b2[n][1] = __byte_perm(lds16(side + Sh::SIDE), 0, 0x1010);
+              }
+            }
+          }
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) {
+            uint4 a[MS];
+#pragma unroll
+            for (int m = 0; m < MS; ++m) a[m] = qw[(m * KK + kk) * 32];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              uint32_t b0, b1;
+              if constexpr (RAW16) {
+                b0 = w[n][2 * kk];
+                b1 = w[n][2 * kk + 1];
+              } else {
+                const int gp = KW == 8 ? kk / 4 : 0;
+                if constexpr (BITS == 8) {
+                  b0 = __byte_perm(w[n][kk], 0x64646464u, 0x4140);
+                  b1 = __byte_perm(w[n][kk], 0x64646464u, 0x4342);
+                } else {
+                  const uint32_t x = w[n][kk / 2] >> (8 * (kk & 1));
+                  b0 = (x & 0x000f000fu) | 0x64006400u;
+                  b1 = ((x >> 4) & 0x000f000fu) | 0x64006400u;
+                }
+                b0 = tn_fma(b0, s2[n][gp], b2[n][gp]);
+                b1 = tn_fma(b1, s2[n][gp], b2[n][gp]);
+              }
+#pragma unroll
+              for (int m = 0; m < MS; ++m)
+                tn_mma<RAW16>(sc[m][n], a[m], b0, b1);
+            }
+          }
+        }
+        // ---------------------------------------------------------- weights
+        uint4 pa[MS];
+#pragma unroll
+        for (int m = 0; m < MS; ++m) {
+          uint32_t see[2] = {0xffffu, 0xffffu};                              // visible tokens of the step, per row half
+          if constexpr (masked) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int d = t0 - s.len;                                      // drafted index of the step's first token
+              see[i] = d <= -32 ? 0xffffu : (d < 0 ? ((1u << -d) - 1) | (uint32_t)(bits[m][i] << -d)
+                                                   : (d < 64 ? (uint32_t)(bits[m][i] >> d) : 0u));
+            }
+          }
+          auto shown = [&](int n, int e) { return see[e >> 1] >> (8 * n + 2 * q + (e & 1)) & 1; };
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], !masked || shown(n, e) ? sc[m][n][e] : -INFINITY);
+          bool grown = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            top[i] = top[i] == -INFINITY ? top[i] : top[i] * f[m][i];
+            grown |= top[i] + nref[m][i] > lim[m][i];                        // (nothing visible: never)
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+              const bool move = top[i] + nref[m][i] > lim[m][i];             // alike in the row's four lanes
+              const float now = move ? Sh::BIAS - top[i] : nref[m][i];
+              const float fix = lim[m][i] == -INFINITY ? 1.f : ta_exp2(now - nref[m][i]);   // no weight so far: nothing to rescale
+              lim[m][i] = move ? Sh::GROW : lim[m][i];
+              nref[m][i] = now;
+              sum[m][i] *= fix;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                o[m][n][2 * i] *= fix;
+                o[m][n][2 * i + 1] *= fix;
+              }
+            }
+          }
+          float w[2][4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = e >> 1;
+              const float x = ta_exp2(fmaf(sc[m][n][e], f[m][i], nref[m][i]));
+              w[n][e] = !masked || shown(n, e) ? x : 0.f;
+              sum[m][i] += w[n][e];
+            }
+          pa[m] = make_uint4(ta_pack(w[0][0], w[0][1], RAW16), ta_pack(w[0][2], w[0][3], RAW16), ta_pack(w[1][0], w[1][1], RAW16),
+                             ta_pack(w[1][2], w[1][3], RAW16));
+        }
+        // ---------------------------------------------------------- O += P V
+        {
+          uint32_t w[4][VW], s2[2], b2[2];                                   // tokens 2q, 2q + 1, 2q + 8, 2q + 9
+          const int valid = s.total - t0, drafted = s.len - t0;
+          bool odd = false;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 2 * q + (x & 1) + 8 * (x >> 1);
+            const uint8_t* row = st + TN_STEP * ROWB + r * ROWB;
+            const int fv = CPR >= 8 ? ((r >> 1) & 3) << 1 : (CPR == 4 ? (r >> 1) & 3 : 0);
+            if constexpr (VW >= 4) {
+#pragma unroll
+              for (int c = 0; c < VW / 4; ++c) lds_words(w[x], 4 * c, row + (((8 * c + g) ^ fv) << 4));
+            } else if constexpr (VW == 2) {
+              lds_words(w[x], 0, row + (((g >> 1) ^ fv) << 4) + (g & 1) * 8);
+            } else {
+              lds_words(w[x], 0, row + (g >> 2) * 16 + (g & 3) * 4);
+            }
+            if constexpr (RAW16 && masked) {
+              // Rows past the end are zeroed (their weight is 0, and 0 * NaN would not be); so are a drafted row's
+              // infinities and NaN, which only rows that see it may get (added in when the run is written).
+#pragma unroll
+              for (int y = 0; y < VW; ++y) {
+                if (r >= valid) {
+                  w[x][y] = 0;
+                } else if (r >= drafted) {
+                  if ((w[x][y] & 0x7f80u) == 0x7f80u) { w[x][y] &= 0xffff0000u; odd = true; }
+                  if ((w[x][y] & 0x7f800000u) == 0x7f800000u) { w[x][y] &= 0x0000ffffu; odd = true; }
+                }
+              }
+            }
+          }
+          if constexpr (!RAW16) {
+            const uint8_t* side = st + 2 * TN_STEP * ROWB + 2 * Sh::SIDE;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {                                    // token pairs
+              uint32_t a[2], b[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int r = 2 * q + z + 8 * y;
+                const uint8_t* at = side + r * (2 * G) + (G == 2 ? (g >> 2) * 2 : 0);
+                a[z] = lds16(at);
+                b[z] = lds16(at + Sh::SIDE);
+                if constexpr (masked) {                                      // as above, a group at a time
+                  const bool wild = ta_half_bad(a[z]) | ta_half_bad(b[z]), off = (r >= valid) | ((r >= drafted) & wild);
+                  odd |= off & (r < valid);
+                  a[z] = off ? 0 : a[z];
+                  b[z] = off ? 0 : b[z];
+                }
+              }
+              s2[y] = a[0] | a[1] << 16;
+              b2[y] = b[0] | b[1] << 16;
+            }
+          }
+          if constexpr (masked) {
+            if (odd) s_odd = 1;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint32_t b[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t *A = w[2 * y], *B = w[2 * y + 1];
+              if constexpr (RAW16) {
+                b[y] = __byte_perm(A[n / 2], B[n / 2], n & 1 ? 0x7632 : 0x5410);
+              } else if constexpr (BITS == 8) {
+                const uint32_t x = __byte_perm(A[n / 4], B[n / 4], n & 2 ? 0x7362 : 0x5140);
+                b[y] = tn_fma(__byte_perm(x, 0x64646464u, n & 1 ? 0x4342 : 0x4140), s2[y], b2[y]);
+              } else {
+                const uint32_t x = __byte_perm(A[n / 8], B[n / 8], n & 4 ? 0x7632 : 0x5410);
+                b[y] = tn_fma(((x >> (4 * (n & 3))) & 0x000f000fu) | 0x64006400u, s2[y], b2[y]);
+              }
+            }
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+              tn_mma<RAW16>(o[m][n], pa[m], b[0], b[1]);
+          }
+        }
+      }
+    };
+    for (int k = 0; k < steps; ++k) {
+      cp_async_wait<NST - 2>();
+      __syncwarp();                                                          // every lane's copies of this stage have landed
+      const uint8_t* st = ring + (k % NST) * Sh::STAGE;
+      const int t0 = (first + ws + k * Sh::WS) * TN_STEP;
+      if (t0 + TN_STEP > s.len) {
+        if (mts == 1) step(st, t0, std::true_type{}, std::integral_constant<int, 1>{});
+        else step(st, t0, std::true_type{}, std::integral_constant<int, MT>{});
+      } else {
+        if (mts == 1) step(st, t0, std::false_type{}, std::integral_constant<int, 1>{});
+        else step(st, t0, std::false_type{}, std::integral_constant<int, MT>{});
+      }
+      __syncwarp();                                                          // the stage may be overwritten
+      issue(k + NST - 1);
+    }
+    // ------------------------------------------------------------ the warps' sums meet
+    cp_async_wait<0>();
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = sum[m][i];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (q == 0) {
+          s_max[warp][16 * m + 8 * i + g] = lim[m][i] == -INFINITY ? -INFINITY : -nref[m][i];
+          s_sum[warp][16 * m + 8 * i + g] = x;
+        }
+      }
+    __syncthreads();
+    const bool whole = s.n == s.nt, odd = s_odd != 0;
+    const size_t slot = ta_slot(s);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = 16 * m + 8 * i + g;
+        float most = -INFINITY, weight = 0.f;
+        for (int x = 0; x < Sh::WS; ++x) most = fmaxf(most, s_max[x * RG + rg][k]);
+        const float base = most == -INFINITY ? 0.f : most;
+        for (int x = 0; x < Sh::WS; ++x) weight += s_sum[x * RG + rg][k] * ta_exp2(s_max[x * RG + rg][k] - base);
+        const float own = ta_exp2(s_max[warp][k] - base), factor = whole ? (weight == 0.f ? 0.f : own / weight) : own;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[m][n][2 * i] *= factor;
+          o[m][n][2 * i + 1] *= factor;
+        }
+        if (!whole && ws == 0 && q == 0) {
+          p.stats[(2 * slot) * p.block + r0 + k] = most;
+          p.stats[(2 * slot + 1) * p.block + r0 + k] = weight;
+        }
+      }
+    constexpr int LD = Sh::LD;
+    // a lane's sums of one row tile, in element order
+    auto put = [&](int m, float* tile, bool add) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int n = 0; n < NT; n += 4) {
+            const int d = tn_v_elem<D, BITS>(n, 2 * q + e);
+            float4* at = reinterpret_cast<float4*>(tile + (8 * i + g) * LD + d + (d >> 5) * 4);
+            const int c = 2 * i + e;
+            if (add) {
+              const float4 t = *at;
+              o[m][n][c] += t.x; o[m][n + 1][c] += t.y; o[m][n + 2][c] += t.z; o[m][n + 3][c] += t.w;
+            } else {
+              *at = make_float4(o[m][n][c], o[m][n + 1][c], o[m][n + 2][c], o[m][n + 3][c]);
+            }
+          }
+    };
+    if constexpr (Sh::W == 16) {                                             // 16 warps: the upper half goes to the lower first
+      if (warp >= 8) put(0, tiles + (warp - 8) * (Sh::TILE / 4), false);
+      __syncthreads();
+      if (warp < 8) {
+        put(0, tiles + warp * (Sh::TILE / 4), true);
+        put(0, tiles + warp * (Sh::TILE / 4), false);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if constexpr (Sh::W == 8) {
+        put(m, tiles + warp * (Sh::TILE / 4), false);
+        __syncthreads();
+      }
+      constexpr int QUADS = D / 4;
+      for (int idx = threadIdx.x; idx < RG * 16 * QUADS; idx += Sh::THREADS) {
+        const int x = idx / (16 * QUADS), row = (idx / QUADS) % 16, d0 = 4 * (idx % QUADS);
+        const int k = x * 16 * MT + 16 * m + row;
+        if (k >= s.rows) continue;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < 8 / RG; ++y) {
+          const float4 t = *reinterpret_cast<const float4*>(tiles + (y * RG + x) * (Sh::TILE / 4) + row * LD + d0 + (d0 >> 5) * 4);
+          a.x += t.x; a.y += t.y; a.z += t.z; a.w += t.w;
+        }
+        if (odd) {
+          // V held infinities or NaN in drafted tokens, which were left out of the products: the rows that see one get it
+          const int r = s.rb * p.block + k, di = r / p.group;
+          const uint64_t see = ta_mask(p, s.row0 + di, di, s.m);
+          float* e = reinterpret_cast<float*>(&a);
+#pragma unroll 1
+          for (int i = 0; i < 4 * s.m; ++i) {
+            const int pos = s.len + i / 4;
+            if (!(see >> (i / 4) & 1) || pos < s.tile0 << TA_UNIT_SHIFT || pos >= (s.tile0 + s.n) << TA_UNIT_SHIFT) continue;
+            const int page = p.table[(size_t)s.b * p.table_pages + (pos >> p.c.page_shift)];
+            if ((unsigned)page >= (unsigned)p.c.n_pages) continue;
+            const float v = ta_cache_value<BITS>(p.c.p.v, p.c.p.vs, p.c.p.vb, kv_token(p.c, page, s.h, pos & pm), D, d0 + i % 4);
+            if (!isfinite(v)) e[i % 4] += v;
+          }
+        }
+        if (whole) {
+          __nv_bfloat162 o2[2] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w)};
+          *reinterpret_cast<uint2*>(p.out + s_out[k] + d0) = *reinterpret_cast<uint2*>(o2);
+        } else {
+          *reinterpret_cast<float4*>(p.partial + s_out[k] + d0) = a;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int D, int BITS, int MT, int RG>
+static cudaError_t launch_narrow(const TreeAttnParams& p, cudaStream_t s) {
+  using Sh = TnShape<D, BITS, MT, RG>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(tree_attn_narrow_kernel<D, BITS, MT, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(p.grid), dim3(Sh::THREADS), Sh::SMEM, s, attr);
+  return cudaLaunchKernelEx(&cfg, tree_attn_narrow_kernel<D, BITS, MT, RG>, p);
+}
+template <int D, int BITS>
+static cudaError_t launch_narrow_rows(const TreeAttnParams& p, cudaStream_t s) {
+  return p.block == 16 ? launch_narrow<D, BITS, 1, 1>(p, s) : launch_narrow<D, BITS, 2, 1>(p, s);
+}
+
+cudaError_t launch_tree_attn_narrow(const TreeAttnParams& p, cudaStream_t s) {
+  if (p.c.dim == 128)
+    return p.c.bits == 16 ? launch_narrow_rows<128, 16>(p, s)
+                          : (p.c.bits == 8 ? launch_narrow_rows<128, 8>(p, s) : launch_narrow_rows<128, 4>(p, s));
+  return p.c.bits == 16 ? launch_narrow_rows<64, 16>(p, s)
+                        : (p.c.bits == 8 ? launch_narrow_rows<64, 8>(p, s) : launch_narrow_rows<64, 4>(p, s));
+}
+
+}  // namespace sv
