@@ -10,57 +10,89 @@ namespace sv {
 
 constexpr int TA_MAX_BLOCK = 128, TA_NARROW_ROWS = 32;
 
-// Joins the partial sums of items that spanned CTAs, in CTA order; a warp per (row, query head).
+// Joins the partial sums of items that spanned CTAs, in CTA order.  A CTA per (row, query head): its four warps take every
+// fourth part, so that all parts are on their way at once, and meet in shared memory in warp order.
 template <int D>
-__global__ void __launch_bounds__(256) tree_attn_join_kernel(const __grid_constant__ TreeAttnParams p) {
+__global__ void __launch_bounds__(128) tree_attn_join_kernel(const __grid_constant__ TreeAttnParams p) {
   __shared__ TaPlan plan;
-  pdl_trigger();
-  pdl_wait();
+  __shared__ float s_acc[4][D], s_most[4], s_weight[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The kernel before lets this one start only after its own wait, so what came before it is there already.
   if (warp == 0) ta_plan(p, &plan, false);
   __syncthreads();
   const int heads = p.c.heads * p.group;
-  const long long id = (long long)blockIdx.x * 8 + warp;
-  const int row = (int)(id / heads), hq = (int)(id - (long long)row * heads);
-  if (row >= p.map.offs[p.map.B]) return;
+  const int row = blockIdx.x / heads, hq = blockIdx.x - row * heads;
   const int b = request_of(p.map, row), i = row - p.map.offs[b], m = p.map.offs[b + 1] - p.map.offs[b];
   const int h = hq / p.group, r = i * p.group + (hq - h * p.group), rb = r / p.block, k = r - rb * p.block;
   const int nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
   const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
-  const long long a0 = plan.pre[b] + ((long long)h * ta_blocks(m * p.group, p.block) + rb) * nt;
-  const int c0 = (int)(a0 / per), c1 = (int)((a0 + nt - 1) / per);
+  const long long a0 = plan.pre[b] + ((long long)h * ta_blocks(m * p.group, p.block) + rb) * (nt + p.begin_cost);
+  // the CTAs that have units of this item, and whose parts they are: a CTA's first one if its share begins in the item
+  int c0 = (int)((a0 + p.begin_cost) / per);
+  const int c1 = (int)((a0 + p.begin_cost + nt - 1) / per);
+  pdl_wait();
+  pdl_trigger();
   if (c0 == c1) return;                                // one CTA had the whole item and wrote the output
-  // CTA c's run of this item is its first one unless the item began inside the CTA's range
-  auto slot_of = [&](int c) -> size_t { return 2 * (size_t)c + (c == c0 && a0 > (long long)c * per ? 1 : 0); };
-  float most = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) most = fmaxf(most, p.stats[2 * slot_of(c) * p.block + k]);
-#pragma unroll
-  for (int off = 16; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-  const float base = most == -INFINITY ? 0.f : most;
+  auto slot_of = [&](int c) -> size_t { return 2 * (size_t)c + (a0 > (long long)c * per ? 1 : 0); };
   constexpr int E = D / 32;
-  float acc[E] = {}, weight = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t slot = slot_of(c);
-    const float w = ta_exp2(p.stats[2 * slot * p.block + k] - base);
-    weight += p.stats[(2 * slot + 1) * p.block + k] * w;
-    const float* src = p.partial + (slot * p.block + k) * D + lane * E;
-    float x[E];
-    if constexpr (E == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(src);
-      x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(src);
-      x[0] = t.x; x[1] = t.y;
+  float acc[E] = {}, weight = 0.f, most = -INFINITY;
+  for (int c8 = c0 + warp; c8 <= c1; c8 += 32) {       // eight parts of this warp at a time
+    float x[8][E], st[8], wt[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const int c = c8 + 4 * y;
+      st[y] = -INFINITY;
+      wt[y] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[y][e] = 0.f;
+      if (c <= c1) {
+        const size_t slot = slot_of(c);
+        st[y] = p.stats[2 * slot * p.block + k];
+        wt[y] = p.stats[(2 * slot + 1) * p.block + k];
+        const float* src = p.partial + (slot * p.block + k) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[y][0] = v.x; x[y][1] = v.y; x[y][2] = v.z; x[y][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[y][0] = v.x; x[y][1] = v.y;
+        }
+      }
     }
+    float top = most;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += x[e] * w;
+    for (int y = 0; y < 8; ++y) top = fmaxf(top, st[y]);
+    const float base = top == -INFINITY ? 0.f : top, fix = ta_exp2(most - base);
+    weight *= fix;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= fix;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const float w = ta_exp2(st[y] - base);
+      weight += wt[y] * w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += x[y][e] * w;
+    }
+    most = top;
   }
-  __nv_bfloat16* dst = p.out + (size_t)row * p.ldo + hq * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + e) =
-        weight == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc[e] / weight, acc[e + 1] / weight);
+  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+  if (lane == 0) {
+    s_most[warp] = most;
+    s_weight[warp] = weight;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+  const float base = most == -INFINITY ? 0.f : most;
+  float sum = 0.f, all = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = ta_exp2(s_most[w] - base);
+    sum += s_acc[w][threadIdx.x] * f;
+    all += s_weight[w] * f;
+  }
+  p.out[(size_t)row * p.ldo + hq * D + threadIdx.x] = __float2bfloat16_rn(all == 0.f ? 0.f : sum / all);
 }
 
 // ------------------------------------------------------------------ host side
@@ -84,7 +116,7 @@ template <int D>
 static cudaError_t launch_join(const TreeAttnParams& p, cudaStream_t s) {
   const long long pairs = (long long)p.map.offs[p.map.B] * p.c.heads * p.group;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((pairs + 7) / 8)), dim3(256), 0, s, attr);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)pairs), dim3(128), 0, s, attr);
   return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D>, p);
 }
 
@@ -144,6 +176,8 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   // Items of up to 64 rows leave more shared memory to the ring of operand tiles; wider requests take items of 128.
   const bool narrow = rows <= TA_NARROW_ROWS;
   p.block = narrow ? (rows <= 16 ? 16 : 32) : (rows <= 64 ? 64 : TA_MAX_BLOCK);
+  // Measured: beginning an item takes a narrow CTA some 7 us, a wide one 4, against 1.2 and 1.7 a unit.
+  p.begin_cost = narrow ? 4 : 2;
   // the lengths are on the device: size the grid for the longest the table allows
   const long long most_units = (((long long)table_pages << p.c.page_shift) + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
   long long most = 0;

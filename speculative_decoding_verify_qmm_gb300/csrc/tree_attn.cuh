@@ -1,10 +1,12 @@
 // Shared by the kernel of tree attention and the join: their parameters, how the work is dealt, and how a finished run of an item is
 // written.
 //
-// Every (request, key head, block of rows) is an item of ceil(tokens / unit) units; the units of all items, in order, are
-// dealt to the CTAs in equal contiguous runs, so ragged lengths balance and one long sequence fills the GPU.  A CTA that has
-// an item whole writes the output; parts of an item leave fp32 sums (with their maximum and weight) in the workspace, and a
-// second kernel joins them in CTA order.  Each CTA has at most two such parts: its first run and its last.
+// Every (request, key head, block of rows) is an item of ceil(tokens / 128) units.  Beginning an item costs a CTA as much as
+// some units (its rows to load, the pipeline to fill, the sums to write), so an item counts as its units plus that many; the
+// items, in order, are dealt to the CTAs in equal contiguous shares of that count.  Ragged lengths balance, and one long
+// sequence fills the GPU.  A CTA that has an item whole writes the output; parts of an item leave fp32 sums (with their
+// maximum and weight) in the workspace, and a second kernel joins them in CTA order.  Each CTA has at most two such parts:
+// of the item that its share begins in, and of the one that it ends in.
 #pragma once
 
 #include "sv_kv.cuh"
@@ -28,11 +30,12 @@ struct TreeAttnParams {
   float* stats;              // [2 * grid][2][block]: their maximum (as an exponent of 2) and weight
   int grid;
   int block;                 // rows (drafted row x query head of the group) per item
+  int begin_cost;            // what beginning an item costs, in units
 };
 
 // What every CTA derives from the lengths: prefix sums of units.
 struct TaPlan {
-  long long pre[MAX_BATCH + 1];   // units of the requests before b
+  long long pre[MAX_BATCH + 1];   // count of the requests before b
   int len[MAX_BATCH];             // committed tokens, brought into the table's range
 };
 
@@ -55,7 +58,7 @@ __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, b
         len = len < 0 ? 0 : cap - m;
       }
       plan->len[b] = (int)len;
-      if (m) units = (long long)p.c.heads * ta_blocks(m * p.group, p.block) * ((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT);
+      if (m) units = (long long)p.c.heads * ta_blocks(m * p.group, p.block) * (((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT) + p.begin_cost);
     }
     long long inc = units;
 #pragma unroll
@@ -69,11 +72,18 @@ __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, b
   if (lane == 0) plan->pre[0] = 0;
 }
 
+// Of an item that counts from a0 on and has nt units: the units before position x of the count.
+__device__ __forceinline__ int ta_units_before(long long x, long long a0, int nt, int begin_cost) {
+  const long long n = x - a0 - begin_cost;
+  return n <= 0 ? 0 : (n < nt ? (int)n : nt);
+}
+
 // A run of units of one item in one CTA.
 struct TaSeg {
   int b, h, rb, m, row0, rows;   // request, key head, row block; drafted rows, first row, rows of the block
   int tile0, n, nt, len, total;  // first unit, units, the item's units; committed and all tokens
-  bool first;                    // starts at the CTA's first unit
+  long long next;                // where the count goes on
+  bool first;                    // of the item that the CTA's share begins in
 };
 __device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPlan& plan, long long u, long long u0, long long u1) {
   int lo = 0, hi = p.map.B;
@@ -88,18 +98,29 @@ __device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPla
   s.len = plan.len[lo];
   s.total = s.len + s.m;
   s.nt = (s.total + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
-  const unsigned long long local = (unsigned long long)(u - plan.pre[lo]);
-  const int item = (int)(local / (unsigned)s.nt);
-  s.tile0 = (int)(local - (unsigned long long)item * (unsigned)s.nt);
+  const int count = s.nt + p.begin_cost;
+  const long long local = u - plan.pre[lo];
+  const int item = local <= 0x7fffffff ? (int)((unsigned)local / (unsigned)count) : (int)(local / count);
+  const long long a0 = plan.pre[lo] + (long long)item * count;
   const int nrb = ta_blocks(s.m * p.group, p.block);
   s.h = item / nrb;
   s.rb = item - s.h * nrb;
   const int left = s.m * p.group - s.rb * p.block;
   s.rows = left < p.block ? left : p.block;
-  const long long can = u1 - u;
-  s.n = s.nt - s.tile0 < can ? s.nt - s.tile0 : (int)can;
+  s.next = a0 + count < u1 ? a0 + count : u1;
+  s.tile0 = ta_units_before(u, a0, s.nt, p.begin_cost);
+  s.n = ta_units_before(s.next, a0, s.nt, p.begin_cost) - s.tile0;
   s.first = u == u0;
   return s;
+}
+// The CTA's next run that has units, from position u on; false: there is none.
+__device__ __forceinline__ bool ta_next(const TreeAttnParams& p, const TaPlan& plan, long long* u, long long u0, long long u1, TaSeg* s) {
+  while (*u < u1) {
+    *s = ta_segment(p, plan, *u, u0, u1);
+    *u = s->next;
+    if (s->n > 0) return true;
+  }
+  return false;
 }
 
 // Drafted tokens a row sees, as bits 0 .. m - 1.

@@ -38,7 +38,7 @@ struct TnShape {
   static constexpr int NST = FIT > 8 ? 8 : FIT;
   static constexpr int RING = W * NST * STAGE;
   static constexpr int SMEM = QBYTES + (RING > JOIN ? RING : JOIN);             // the join's tiles lie in the drained ring
-  static_assert(NST >= 2, "stages");
+  static_assert(NST >= 2 && RG * MT <= W, "stages, and a warp for each row tile of Q");
   // as in the kernel for many rows: room for a score to outgrow its row's reference, in the weights' 16-bit type
   static constexpr float BIAS = BITS == 16 ? 0.f : 5.f, GROW = BITS == 16 ? 60.f : 15.f;
 };
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_att
   __shared__ TaPlan plan;
   __shared__ float s_f[Sh::BLOCK], s_max[Sh::W][16 * MT], s_sum[Sh::W][16 * MT];
   __shared__ long long s_out[Sh::BLOCK];                   // where each row of the block is written (elements)
+  __shared__ uint64_t s_mask[Sh::BLOCK];
   __shared__ int s_odd;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int rg = warp % RG, ws = warp / RG;
@@ -117,17 +118,16 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_att
   const uint32_t ring_a = smem_u32(ring);
   float* const tiles = reinterpret_cast<float*>(smem + Sh::QBYTES);
 
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();             // after the wait: the join may then read what this kernel's predecessors wrote before its own
   if (warp == 0) ta_plan(p, &plan, blockIdx.x == 0);
   __syncthreads();
   const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
   const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
   const int pm = (1 << p.c.page_shift) - 1;
 
-  for (long long u = u0; u < u1;) {
-    const TaSeg s = ta_segment(p, plan, u, u0, u1);
-    u += s.n;
+  TaSeg s;
+  for (long long u = u0; ta_next(p, plan, &u, u0, u1, &s);) {
     // ------------------------------------------------------------ the ring's first copies
     const int r0 = rg * 16 * MT;                                            // this warp's first row of the block
     const int mts = s.rows <= r0 ? 0 : (s.rows - r0 > 16 ? MT : 1);         // its row tiles with rows
@@ -176,28 +176,36 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_att
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int k = 0; k < NST - 1; ++k) issue(k);
     // ------------------------------------------------------------ Q, as A operands
     if (threadIdx.x == 0) s_odd = 0;
     const bool minus = p.scale < 0.f;                                       // the sign goes into q
-    for (int t = warp; t < RG * MT; t += Sh::W) {
-      // this lane's share of two rows: the elements that its share of a K row meets
-      constexpr int PE = D * BITS >= 512 ? 128 / BITS : D / 4, NP = D / 4 / PE;
-      uint4 raw[2][D / 32];
-      bool real[2];
+    const int t = warp;                                                     // a warp a row tile
+    const bool has_q = t < RG * MT;
+    // this lane's share of two rows: the elements that its share of a K row meets
+    constexpr int PE = D * BITS >= 512 ? 128 / BITS : D / 4, NP = D / 4 / PE;
+    uint4 raw[2][D / 32];
+    bool real[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = 16 * t + 8 * i + g;
-        real[i] = k < s.rows;
-        const int r = s.rb * p.block + k, di = real[i] ? r / p.group : 0, hg = real[i] ? r - di * p.group : 0;
-        const __nv_bfloat16* src = p.q + (size_t)(s.row0 + di) * p.ldq + (s.h * p.group + hg) * D;
+    for (int i = 0; i < 2; ++i) {
+      const int k = 16 * t + 8 * i + g;
+      real[i] = has_q && k < s.rows;
+      const int r = s.rb * p.block + k, di = real[i] ? r / p.group : 0, hg = real[i] ? r - di * p.group : 0;
+      const __nv_bfloat16* src = p.q + (size_t)(s.row0 + di) * p.ldq + (s.h * p.group + hg) * D;
 #pragma unroll
-        for (int c = 0; c < NP; ++c)
+      for (int c = 0; c < NP; ++c)
 #pragma unroll
-          for (int y = 0; y < PE / 8; ++y)
-            raw[i][c * (PE / 8) + y] = real[i] ? *reinterpret_cast<const uint4*>(src + (4 * c + q) * PE + 8 * y) : make_uint4(0, 0, 0, 0);
-      }
+        for (int y = 0; y < PE / 8; ++y)
+          raw[i][c * (PE / 8) + y] = real[i] ? *reinterpret_cast<const uint4*>(src + (4 * c + q) * PE + 8 * y) : make_uint4(0, 0, 0, 0);
+    }
+    uint64_t mask = 0;                                 // of row 16 t + 8 q + g, kept by the lanes with q < 2
+    if (has_q && q < 2 && 16 * t + 8 * q + g < s.rows) {
+      const int di = (s.rb * p.block + 16 * t + 8 * q + g) / p.group;
+      mask = ta_mask(p, s.row0 + di, di, s.m);
+    }
+    // (asked for before the ring's copies, which would hold these loads up)
+#pragma unroll
+    for (int k = 0; k < NST - 1; ++k) issue(k);
+    if (has_q) {
       float up[2] = {minus ? -1.f : 1.f, minus ? -1.f : 1.f};
       float f[2];
       f[0] = f[1] = fabsf(p.scale) * 1.4426950408889634f;
@@ -231,7 +239,8 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_att
       }
       if (q < 2) {
         const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = r / p.group;
-        s_f[k] = f[q];
+        s_f[k] = q ? f[1] : f[0];
+        s_mask[k] = mask;
         s_out[k] = s.n == s.nt ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
                                : (long long)(ta_slot(s) * p.block + k) * D;
       }
@@ -248,13 +257,12 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_att
         for (int e = 0; e < 4; ++e) o[m][n][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k = r0 + 16 * m + 8 * i + g, r = s.rb * p.block + k;
+        const int k = r0 + 16 * m + 8 * i + g;
         f[m][i] = s_f[k];
         nref[m][i] = 0.f;
         lim[m][i] = -INFINITY;                           // no reference yet
         sum[m][i] = 0.f;
-        const int di = k < s.rows ? r / p.group : 0;
-        bits[m][i] = k < s.rows ? ta_mask(p, s.row0 + di, di, s.m) : 0;
+        bits[m][i] = s_mask[k];
       }
     }
     const uint4* const qw = qf + (rg * MT) * KK * 32 + lane;

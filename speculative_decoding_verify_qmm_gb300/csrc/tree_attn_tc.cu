@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
   volatile int* abort_v = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::OPS; ++i) {
       mbar_init(&load_full[i], 1);
@@ -254,6 +253,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
     tmem_relinquish();
   }
   pdl_wait();
+  pdl_trigger();             // after the wait: the join may then read what this kernel's predecessors wrote before its own
   if (warp == 0) ta_plan(p, &plan, blockIdx.x == 0);
   tc05_fence_before();
   __syncthreads();
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       const int my_chunk = lane / PER, part = lane - my_chunk * PER;
       TaRing<Sh::OPS> ring;
       bool ok = true;
-      for (long long u = u0; u < u1 && ok;) {
-        const TaSeg s = ta_segment(p, plan, u, u0, u1);
+      TaSeg s;
+      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s);) {
         // the table's entry for this lane's chunk of tile j, checked when it is used: the load is a tile ahead
         auto page_of = [&](int j) -> int {
           const int t = (s.tile0 + j) * TA_TILE + (my_chunk << shift);
@@ -307,7 +307,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
           }
           ring.next();
         }
-        u += s.n;
       }
       // every copy is waited for by its reader; after a failure, give those in flight time to land
       if (!ok || *abort_v) {
@@ -320,8 +319,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       const int pm = (1 << p.c.page_shift) - 1;
       int n_seg = 0;
       bool ok = true;
-      for (long long u = u0; u < u1 && ok; ++n_seg) {
-        const TaSeg s = ta_segment(p, plan, u, u0, u1);
+      TaSeg s;
+      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s); ++n_seg) {
         auto page_of = [&](int j) -> int {             // of 16-token piece `lane` of tile j; checked when it is used
           const int t = (s.tile0 + j) * TA_TILE + 16 * lane;
           if (j >= s.n || lane >= TA_TILE / 16 || t >= s.total) return 0;
@@ -353,7 +352,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
           if (lane == 0) mbar_arrive(&piece_full[ring.slot]);
           ring.next();
         }
-        u += s.n;
       }
       // the end: one descriptor for each team
       for (int e = 0; e < Sh::TEAMS && ok; ++e) {
@@ -383,10 +381,10 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29), HI_ONES = (1u << 14) | (2u << 29);
       constexpr uint32_t LO_K = 1u << 16, LO_V = (D == 128 ? (uint32_t)(TA_TILE * 128 >> 4) : 0u) << 16,
                          LO_P = (uint32_t)(TA_TILE * 128 >> 4) << 16;
-      for (long long u = u0; u < u1 && ok;) {
+      TaSeg s;
+      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s);) {
         int n, rows;
         {
-          const TaSeg s = ta_segment(p, plan, u, u0, u1);
           n = __shfl_sync(0xffffffffu, s.n, 0);
           rows = __shfl_sync(0xffffffffu, s.rows, 0);
         }
@@ -460,7 +458,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
             ring.next();
           }
         }
-        u += n;
       }
       // no MMA may still be running when the tensor memory is freed: this wait
       // ignores the abort flag and ends only on completion or the time limit
@@ -480,8 +477,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
       TaRing<Sh::OPS> ring;
       int n_seg = 0;
       bool ok = true;
-      for (long long u = u0; u < u1 && ok; ++n_seg) {
-        const TaSeg s = ta_segment(p, plan, u, u0, u1);
+      TaSeg s;
+      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s); ++n_seg) {
         for (int i = 0; i < 2 * s.n; ++i, ring.next()) {
           int j;
           const bool is_v = ta_item<Sh::SPLIT>(i, s.n, &j);
@@ -518,7 +515,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
           __syncwarp();
           if (lane == 0) mbar_arrive(&op_full[ring.slot]);
         }
-        u += s.n;
       }
     } else {
       // ========================================================== codes -> fp16 operands
@@ -651,9 +647,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS, NB>::THREADS, 1) tree_attn_ke
     const uint32_t lanes = (uint32_t)(32 * gw) << 16;
     uint32_t n0 = 0;                                    // tiles of the runs before: a tile's number gives group and phases
     int n_seg = 0;
-    for (long long u = u0; u < u1; ++n_seg) {
-      const TaSeg s = ta_segment(p, plan, u, u0, u1);
-      u += s.n;
+    TaSeg s;
+    for (long long u = u0; ta_next(p, plan, &u, u0, u1, &s); ++n_seg) {
       const bool whole = s.n == s.nt;
       const size_t slot = ta_slot(s);
       const int N = (s.rows + 15) & ~15;
