@@ -1,5 +1,5 @@
 // Attention of the drafted rows over the paged cache: the entry point, and the join of items that spanned CTAs (the kernel
-// itself is tree_attn_tc.cu).
+// itself is tree_attn_narrow.cu up to 32 rows and tree_attn_wide.cu above).
 #include <cmath>
 #include <cstddef>
 #include <cstring>
@@ -173,9 +173,8 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
       return fail(SV_EINVAL, "request %d has more rows than block_table has places", b);
     if (m * p.group > rows) rows = m * p.group;
   }
-  // Items of up to 64 rows leave more shared memory to the ring of operand tiles; wider requests take items of 128.
   const bool narrow = rows <= TA_NARROW_ROWS;
-  p.block = narrow ? (rows <= 16 ? 16 : 32) : (rows <= 64 ? 64 : TA_MAX_BLOCK);
+  p.block = narrow ? (rows <= 16 ? 16 : 32) : TA_MAX_BLOCK;
   // Measured: beginning an item takes a narrow CTA some 7 us, a wide one 4, against 1.2 and 1.7 a unit.
   p.begin_cost = narrow ? 4 : 2;
   // the lengths are on the device: size the grid for the longest the table allows
@@ -192,7 +191,7 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
     if (st) return st;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn(p, s);
+  cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn_wide(p, s);
   if (e == cudaSuccess && most_units > 1) e = p.c.dim == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "tree attention launch");
 }

@@ -153,7 +153,7 @@ __device__ __forceinline__ bool ta_half_bad(uint32_t h) { return (h & 0x7c00u) =
 // Where a CTA's run of an item leaves its partial sums.
 __device__ __forceinline__ size_t ta_slot(const TaSeg& s) { return 2 * (size_t)blockIdx.x + (s.first ? 0 : 1); }
 
-cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t s);          // blocks of 64 or 128 rows
+cudaError_t launch_tree_attn_wide(const TreeAttnParams& p, cudaStream_t s);     // blocks of 128 rows
 cudaError_t launch_tree_attn_narrow(const TreeAttnParams& p, cudaStream_t s);   // of 16 or 32
 
 }  // namespace sv
