@@ -10,89 +10,106 @@ namespace sv {
 
 constexpr int TA_MAX_BLOCK = 128, TA_NARROW_ROWS = 32;
 
-// Joins the partial sums of items that spanned CTAs, in CTA order.  A CTA per (row, query head): its four warps take every
-// fourth part, so that all parts are on their way at once, and meet in shared memory in warp order.
-template <int D>
-__global__ void __launch_bounds__(128) tree_attn_join_kernel(const __grid_constant__ TreeAttnParams p) {
+// Joins the partial sums of items that spanned CTAs, in CTA order.  WPP warps per (row, query head) take every WPP-th part,
+// eight parts on their way at once, and meet in shared memory in warp order.  One CTA per SM: it comes in when the kernel
+// before leaves the SM, with its plan made while it waited.
+constexpr int TJ_WARPS = 16;
+template <int D, int WPP>
+__global__ void __launch_bounds__(32 * TJ_WARPS, 1) tree_attn_join_kernel(const __grid_constant__ TreeAttnParams p) {
+  constexpr int PAIRS = TJ_WARPS / WPP, E = D / 32;
   __shared__ TaPlan plan;
-  __shared__ float s_acc[4][D], s_most[4], s_weight[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float s_acc[PAIRS][WPP][WPP > 1 ? D : 1], s_most[PAIRS][WPP], s_weight[PAIRS][WPP];
+  const int lane = threadIdx.x & 31, pair = (threadIdx.x >> 5) / WPP, warp = (threadIdx.x >> 5) % WPP;
   // The kernel before lets this one start only after its own wait, so what came before it is there already.
-  if (warp == 0) ta_plan(p, &plan, false);
+  if (threadIdx.x < 32) ta_plan(p, &plan, false);
   __syncthreads();
+  const long long all = plan.pre[p.map.B], per = (all + p.grid - 1) / p.grid;
   const int heads = p.c.heads * p.group;
-  const int row = blockIdx.x / heads, hq = blockIdx.x - row * heads;
-  const int b = request_of(p.map, row), i = row - p.map.offs[b], m = p.map.offs[b + 1] - p.map.offs[b];
-  const int h = hq / p.group, r = i * p.group + (hq - h * p.group), rb = r / p.block, k = r - rb * p.block;
-  const int nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
-  const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
-  const long long a0 = plan.pre[b] + ((long long)h * ta_blocks(m * p.group, p.block) + rb) * (nt + p.begin_cost);
-  // the CTAs that have units of this item, and whose parts they are: a CTA's first one if its share begins in the item
-  int c0 = (int)((a0 + p.begin_cost) / per);
-  const int c1 = (int)((a0 + p.begin_cost + nt - 1) / per);
+  const long long pairs = (long long)p.map.offs[p.map.B] * heads;
   pdl_wait();
   pdl_trigger();
-  if (c0 == c1) return;                                // one CTA had the whole item and wrote the output
-  auto slot_of = [&](int c) -> size_t { return 2 * (size_t)c + (a0 > (long long)c * per ? 1 : 0); };
-  constexpr int E = D / 32;
-  float acc[E] = {}, weight = 0.f, most = -INFINITY;
-  for (int c8 = c0 + warp; c8 <= c1; c8 += 32) {       // eight parts of this warp at a time
-    float x[8][E], st[8], wt[8];
+  for (long long id = (long long)blockIdx.x * PAIRS + pair; id < pairs; id += (long long)gridDim.x * PAIRS) {
+    const int row = (int)(id / heads), hq = (int)(id - (long long)row * heads);
+    const int b = request_of(p.map, row), i = row - p.map.offs[b], m = p.map.offs[b + 1] - p.map.offs[b];
+    const int h = hq / p.group, r = i * p.group + (hq - h * p.group), rb = r / p.block, k = r - rb * p.block;
+    const int nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT, cost = ta_cost(p, m);
+    const long long span = (long long)nt * cost;
+    const long long a0 = plan.pre[b] + ((long long)h * ta_blocks(m * p.group, p.block) + rb) * (span + plan.begin);
+    // the first and the last CTA with units of this item (one between them may have none where shares are small)
+    const int c0 = (int)((a0 + plan.begin + cost - 1) / per), c1 = (int)((a0 + plan.begin + span - 1) / per);
+    if (c0 == c1) continue;                            // one CTA had the whole item and wrote the output
+    float acc[E] = {}, weight = 0.f, most = -INFINITY;
+    for (int c8 = c0 + warp; c8 <= c1; c8 += 8 * WPP) {
+      float x[8][E], st[8], wt[8];
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const int c = c8 + 4 * y;
-      st[y] = -INFINITY;
-      wt[y] = 0.f;
+      for (int y = 0; y < 8; ++y) {
+        const int c = c8 + WPP * y;
+        const long long lo = (long long)c * per;
+        st[y] = -INFINITY;
+        wt[y] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[y][e] = 0.f;
-      if (c <= c1) {
-        const size_t slot = slot_of(c);
-        st[y] = p.stats[2 * slot * p.block + k];
-        wt[y] = p.stats[(2 * slot + 1) * p.block + k];
-        const float* src = p.partial + (slot * p.block + k) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          x[y][0] = v.x; x[y][1] = v.y; x[y][2] = v.z; x[y][3] = v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          x[y][0] = v.x; x[y][1] = v.y;
+        for (int e = 0; e < E; ++e) x[y][e] = 0.f;
+        if (c <= c1 && ta_units_before(lo + per, a0, nt, cost, plan.begin) > ta_units_before(lo, a0, nt, cost, plan.begin)) {
+          const size_t slot = 2 * (size_t)c + (a0 > lo ? 1 : 0);   // the CTA's first item if its share begins in it
+          st[y] = p.stats[2 * slot * p.block + k];
+          wt[y] = p.stats[(2 * slot + 1) * p.block + k];
+          const float* src = p.partial + (slot * p.block + k) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[y][0] = v.x; x[y][1] = v.y; x[y][2] = v.z; x[y][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[y][0] = v.x; x[y][1] = v.y;
+          }
         }
       }
+      float top = most;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) top = fmaxf(top, st[y]);
+      const float base = top == -INFINITY ? 0.f : top, fix = ta_exp2(most - base);
+      weight *= fix;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= fix;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = ta_exp2(st[y] - base);
+        weight += wt[y] * w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += x[y][e] * w;
+      }
+      most = top;
     }
-    float top = most;
+    if constexpr (WPP > 1) {
 #pragma unroll
-    for (int y = 0; y < 8; ++y) top = fmaxf(top, st[y]);
-    const float base = top == -INFINITY ? 0.f : top, fix = ta_exp2(most - base);
-    weight *= fix;
+      for (int e = 0; e < E; ++e) s_acc[pair][warp][lane * E + e] = acc[e];
+      if (lane == 0) {
+        s_most[pair][warp] = most;
+        s_weight[pair][warp] = weight;
+      }
+      named_bar_sync(1 + pair, 32 * WPP);
+      if (warp == 0) {
+        for (int w = 0; w < WPP; ++w) most = fmaxf(most, s_most[pair][w]);
+        const float base = most == -INFINITY ? 0.f : most;
+        weight = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= fix;
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const float w = ta_exp2(st[y] - base);
-      weight += wt[y] * w;
+        for (int w = 0; w < WPP; ++w) {
+          const float f = ta_exp2(s_most[pair][w] - base);
+          weight += s_weight[pair][w] * f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += x[y][e] * w;
+          for (int e = 0; e < E; ++e) acc[e] += s_acc[pair][w][lane * E + e] * f;
+        }
+      }
+      named_bar_sync(1 + pair, 32 * WPP);
+      if (warp) continue;
     }
-    most = top;
-  }
+    __nv_bfloat16* dst = p.out + (size_t)row * p.ldo + hq * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    s_most[warp] = most;
-    s_weight[warp] = weight;
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+          weight == 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc[e] / weight, acc[e + 1] / weight);
   }
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
-  const float base = most == -INFINITY ? 0.f : most;
-  float sum = 0.f, all = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ta_exp2(s_most[w] - base);
-    sum += s_acc[w][threadIdx.x] * f;
-    all += s_weight[w] * f;
-  }
-  p.out[(size_t)row * p.ldo + hq * D + threadIdx.x] = __float2bfloat16_rn(all == 0.f ? 0.f : sum / all);
 }
 
 // ------------------------------------------------------------------ host side
@@ -112,12 +129,18 @@ static int ta_sms() {
 static size_t ta_partial_bytes(int grid, int dim) { return (size_t)2 * grid * TA_MAX_BLOCK * dim * sizeof(float); }
 static size_t ta_stats_bytes(int grid) { return (size_t)4 * grid * TA_MAX_BLOCK * sizeof(float); }
 
-template <int D>
-static cudaError_t launch_join(const TreeAttnParams& p, cudaStream_t s) {
-  const long long pairs = (long long)p.map.offs[p.map.B] * p.c.heads * p.group;
+template <int D, int WPP>
+static cudaError_t launch_join_w(const TreeAttnParams& p, int sms, cudaStream_t s) {
+  const long long pairs = (long long)p.map.offs[p.map.B] * p.c.heads * p.group, ctas = (pairs + TJ_WARPS / WPP - 1) / (TJ_WARPS / WPP);
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)pairs), dim3(128), 0, s, attr);
-  return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D>, p);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(ctas < sms ? ctas : sms)), dim3(32 * TJ_WARPS), 0, s, attr);
+  return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, WPP>, p);
+}
+// Four warps a pair while that takes the GPU one round.
+template <int D>
+static cudaError_t launch_join(const TreeAttnParams& p, int sms, cudaStream_t s) {
+  const long long pairs = (long long)p.map.offs[p.map.B] * p.c.heads * p.group;
+  return pairs <= (long long)sms * TJ_WARPS / 4 ? launch_join_w<D, 4>(p, sms, s) : launch_join_w<D, 1>(p, sms, s);
 }
 
 }  // namespace sv
@@ -175,8 +198,12 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   }
   const bool narrow = rows <= TA_NARROW_ROWS;
   p.block = narrow ? (rows <= 16 ? 16 : 32) : TA_MAX_BLOCK;
-  // Measured: beginning an item takes a narrow CTA some 7 us, a wide one 4, against 1.2 and 1.7 a unit.
-  p.begin_cost = narrow ? 4 : 2;
+  // Measured (in fifths of the time that a narrow unit with one row tile takes): a second row tile adds two, beginning an
+  // item costs some 7 us against 1.2 a unit in the narrow kernel, 10 against 1.6 in the wide one.
+  p.many = narrow ? 16 : 64;
+  p.cost[0] = 5;
+  p.cost[1] = narrow ? 7 : 5;
+  p.begin_cost = narrow ? 25 : 30;
   // the lengths are on the device: size the grid for the longest the table allows
   const long long most_units = (((long long)table_pages << p.c.page_shift) + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
   long long most = 0;
@@ -192,7 +219,7 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn_wide(p, s);
-  if (e == cudaSuccess && most_units > 1) e = p.c.dim == 128 ? launch_join<128>(p, s) : launch_join<64>(p, s);
+  if (e == cudaSuccess && most_units > 1) e = p.c.dim == 128 ? launch_join<128>(p, sms, s) : launch_join<64>(p, sms, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "tree attention launch");
 }
 

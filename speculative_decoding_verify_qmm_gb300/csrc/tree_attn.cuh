@@ -1,12 +1,12 @@
 // Shared by the kernel of tree attention and the join: their parameters, how the work is dealt, and how a finished run of an item is
 // written.
 //
-// Every (request, key head, block of rows) is an item of ceil(tokens / 128) units.  Beginning an item costs a CTA as much as
-// some units (its rows to load, the pipeline to fill, the sums to write), so an item counts as its units plus that many; the
-// items, in order, are dealt to the CTAs in equal contiguous shares of that count.  Ragged lengths balance, and one long
-// sequence fills the GPU.  A CTA that has an item whole writes the output; parts of an item leave fp32 sums (with their
-// maximum and weight) in the workspace, and a second kernel joins them in CTA order.  Each CTA has at most two such parts:
-// of the item that its share begins in, and of the one that it ends in.
+// Every (request, key head, block of rows) is an item of ceil(tokens / 128) units.  A unit's cost depends on the rows, and
+// beginning an item costs a CTA as much as some units (its rows to load, the pipeline to fill, the sums to write); the items,
+// in order, are dealt to the CTAs in equal contiguous shares of that cost.  Ragged lengths balance, and one long sequence
+// fills the GPU.  A CTA that has an item whole writes the output; parts of an item leave fp32 sums (with their maximum and
+// weight) in the workspace, and a second kernel joins them in CTA order.  Each CTA has at most two such parts: of the item
+// that its share begins in, and of the one that it ends in.
 #pragma once
 
 #include "sv_kv.cuh"
@@ -30,37 +30,50 @@ struct TreeAttnParams {
   float* stats;              // [2 * grid][2][block]: their maximum (as an exponent of 2) and weight
   int grid;
   int block;                 // rows (drafted row x query head of the group) per item
-  int begin_cost;            // what beginning an item costs, in units
+  int cost[2], many;         // of a unit with up to `many` rows, and with more
+  int begin_cost;            // of beginning an item
 };
 
 // What every CTA derives from the lengths: prefix sums of units.
 struct TaPlan {
-  long long pre[MAX_BATCH + 1];   // count of the requests before b
+  long long pre[MAX_BATCH + 1];   // cost of the requests before b
   int len[MAX_BATCH];             // committed tokens, brought into the table's range
+  int begin;                      // p.begin_cost, or nothing where the shares are too small to hold a second beginning
 };
 
 __host__ __device__ __forceinline__ int ta_blocks(int rows, int block) { return (rows + block - 1) / block; }
+
+__device__ __forceinline__ int ta_cost(const TreeAttnParams& p, int m) { return p.cost[m * p.group > p.many]; }
 
 // By one warp.
 __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool report) {
   const int lane = threadIdx.x & 31;
   const RowMap& map = p.map;
   const long long cap = (long long)p.table_pages << p.c.page_shift;   // at least every request's rows (checked by the host)
+  long long all = 0;
+  for (int b = lane; b < map.B; b += 32) {
+    const int m = map.offs[b + 1] - map.offs[b];
+    long long len = p.kv_len[b];
+    if (m && (len < 0 || len + m > cap)) {
+      if (report) raise_error(ERR_BAD_INPUT);
+      len = len < 0 ? 0 : cap - m;
+    }
+    plan->len[b] = (int)len;
+    if (m) all += (long long)p.c.heads * ta_blocks(m * p.group, p.block) * ((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT) * ta_cost(p, m);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+  const int begin = all / p.grid >= 4 * p.cost[0] ? p.begin_cost : 0;
   long long run = 0;
   for (int b0 = 0; b0 < map.B; b0 += 32) {
     const int b = b0 + lane;
-    long long units = 0;
+    long long cost = 0;
     if (b < map.B) {
       const int m = map.offs[b + 1] - map.offs[b];
-      long long len = p.kv_len[b];
-      if (m && (len < 0 || len + m > cap)) {
-        if (report) raise_error(ERR_BAD_INPUT);
-        len = len < 0 ? 0 : cap - m;
-      }
-      plan->len[b] = (int)len;
-      if (m) units = (long long)p.c.heads * ta_blocks(m * p.group, p.block) * (((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT) + p.begin_cost);
+      const long long nt = ((long long)plan->len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
+      if (m) cost = (long long)p.c.heads * ta_blocks(m * p.group, p.block) * (nt * ta_cost(p, m) + begin);
     }
-    long long inc = units;
+    long long inc = cost;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long up = __shfl_up_sync(0xffffffffu, inc, off);
@@ -69,13 +82,17 @@ __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, b
     if (b < map.B) plan->pre[b + 1] = run + inc;
     run += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (lane == 0) plan->pre[0] = 0;
+  if (lane == 0) {
+    plan->pre[0] = 0;
+    plan->begin = begin;
+  }
 }
 
-// Of an item that counts from a0 on and has nt units: the units before position x of the count.
-__device__ __forceinline__ int ta_units_before(long long x, long long a0, int nt, int begin_cost) {
-  const long long n = x - a0 - begin_cost;
-  return n <= 0 ? 0 : (n < nt ? (int)n : nt);
+// Of an item whose cost counts from a0 on and that has nt units: the units before position x of the count.
+__device__ __forceinline__ int ta_units_before(long long x, long long a0, int nt, int cost, int begin) {
+  const long long n = x - a0 - begin;
+  if (n <= 0) return 0;
+  return n < (long long)nt * cost ? (int)((unsigned)n / (unsigned)cost) : nt;
 }
 
 // A run of units of one item in one CTA.
@@ -98,8 +115,8 @@ __device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPla
   s.len = plan.len[lo];
   s.total = s.len + s.m;
   s.nt = (s.total + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
-  const int count = s.nt + p.begin_cost;
-  const long long local = u - plan.pre[lo];
+  const int cost = ta_cost(p, s.m);
+  const long long count = (long long)s.nt * cost + plan.begin, local = u - plan.pre[lo];
   const int item = local <= 0x7fffffff ? (int)((unsigned)local / (unsigned)count) : (int)(local / count);
   const long long a0 = plan.pre[lo] + (long long)item * count;
   const int nrb = ta_blocks(s.m * p.group, p.block);
@@ -108,8 +125,8 @@ __device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPla
   const int left = s.m * p.group - s.rb * p.block;
   s.rows = left < p.block ? left : p.block;
   s.next = a0 + count < u1 ? a0 + count : u1;
-  s.tile0 = ta_units_before(u, a0, s.nt, p.begin_cost);
-  s.n = ta_units_before(s.next, a0, s.nt, p.begin_cost) - s.tile0;
+  s.tile0 = ta_units_before(u, a0, s.nt, cost, plan.begin);
+  s.n = ta_units_before(s.next, a0, s.nt, cost, plan.begin) - s.tile0;
   s.first = u == u0;
   return s;
 }
