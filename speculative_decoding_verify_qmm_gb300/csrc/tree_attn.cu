@@ -23,20 +23,32 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, 1) tree_attn_join_kernel(const 
   // The kernel before lets this one start only after its own wait, so what came before it is there already.
   if (threadIdx.x < 32) ta_plan(p, &plan, false);
   __syncthreads();
-  const long long all = plan.pre[p.map.B], per = (all + p.grid - 1) / p.grid;
+  const long long all = plan.pre[p.map.B], per = ta_div(all + p.grid - 1, p.grid);
   const int heads = p.c.heads * p.group;
   const long long pairs = (long long)p.map.offs[p.map.B] * heads;
+  int row, hq, k, c0, c1, nt, cost;
+  long long a0;
+  auto locate = [&](long long id) {
+    row = (int)ta_div(id, heads);
+    hq = (int)(id - (long long)row * heads);
+    const int b = request_of(p.map, row), i = row - p.map.offs[b], m = p.map.offs[b + 1] - p.map.offs[b];
+    const int h = hq / p.group, r = i * p.group + (hq - h * p.group), rb = r / p.block;
+    k = r - rb * p.block;
+    nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
+    cost = ta_cost(p, m);
+    const long long span = (long long)nt * cost;
+    a0 = plan.pre[b] + ((long long)h * ta_blocks(m * p.group, p.block) + rb) * (span + plan.begin);
+    // the first and the last CTA with units of this item (one between them may have none where shares are small)
+    c0 = (int)ta_div(a0 + plan.begin + cost - 1, per);
+    c1 = (int)ta_div(a0 + plan.begin + span - 1, per);
+  };
+  const long long first = (long long)blockIdx.x * PAIRS + pair, step = (long long)gridDim.x * PAIRS;
+  if (first < pairs) locate(first);                    // before the wait: all that does not read the parts
+  const bool dense = per >= 12;                        // more than any unit costs: every CTA of a share has units
   pdl_wait();
   pdl_trigger();
-  for (long long id = (long long)blockIdx.x * PAIRS + pair; id < pairs; id += (long long)gridDim.x * PAIRS) {
-    const int row = (int)(id / heads), hq = (int)(id - (long long)row * heads);
-    const int b = request_of(p.map, row), i = row - p.map.offs[b], m = p.map.offs[b + 1] - p.map.offs[b];
-    const int h = hq / p.group, r = i * p.group + (hq - h * p.group), rb = r / p.block, k = r - rb * p.block;
-    const int nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT, cost = ta_cost(p, m);
-    const long long span = (long long)nt * cost;
-    const long long a0 = plan.pre[b] + ((long long)h * ta_blocks(m * p.group, p.block) + rb) * (span + plan.begin);
-    // the first and the last CTA with units of this item (one between them may have none where shares are small)
-    const int c0 = (int)((a0 + plan.begin + cost - 1) / per), c1 = (int)((a0 + plan.begin + span - 1) / per);
+  for (long long id = first; id < pairs; id += step) {
+    if (id != first) locate(id);
     if (c0 == c1) continue;                            // one CTA had the whole item and wrote the output
     float acc[E] = {}, weight = 0.f, most = -INFINITY;
     for (int c8 = c0 + warp; c8 <= c1; c8 += 8 * WPP) {
@@ -49,7 +61,7 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, 1) tree_attn_join_kernel(const 
         wt[y] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) x[y][e] = 0.f;
-        if (c <= c1 && ta_units_before(lo + per, a0, nt, cost, plan.begin) > ta_units_before(lo, a0, nt, cost, plan.begin)) {
+        if (c <= c1 && (dense || ta_units_before(lo + per, a0, nt, cost, plan.begin) > ta_units_before(lo, a0, nt, cost, plan.begin))) {
           const size_t slot = 2 * (size_t)c + (a0 > lo ? 1 : 0);   // the CTA's first item if its share begins in it
           st[y] = p.stats[2 * slot * p.block + k];
           wt[y] = p.stats[(2 * slot + 1) * p.block + k];
@@ -136,11 +148,13 @@ static cudaError_t launch_join_w(const TreeAttnParams& p, int sms, cudaStream_t 
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(ctas < sms ? ctas : sms)), dim3(32 * TJ_WARPS), 0, s, attr);
   return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, WPP>, p);
 }
-// Four warps a pair while that takes the GPU one round.
+// As many warps a pair, up to four, as one round of the GPU has.
 template <int D>
 static cudaError_t launch_join(const TreeAttnParams& p, int sms, cudaStream_t s) {
   const long long pairs = (long long)p.map.offs[p.map.B] * p.c.heads * p.group;
-  return pairs <= (long long)sms * TJ_WARPS / 4 ? launch_join_w<D, 4>(p, sms, s) : launch_join_w<D, 1>(p, sms, s);
+  const long long slots = (long long)sms * TJ_WARPS;
+  if (pairs * 4 <= slots) return launch_join_w<D, 4>(p, sms, s);
+  return pairs * 2 <= slots ? launch_join_w<D, 2>(p, sms, s) : launch_join_w<D, 1>(p, sms, s);
 }
 
 }  // namespace sv

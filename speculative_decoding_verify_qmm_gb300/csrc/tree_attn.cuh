@@ -88,6 +88,11 @@ __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, b
   }
 }
 
+// a / b for 0 <= a, 0 < b, in 32 bits where they fit (a 64-bit division takes hundreds of cycles).
+__device__ __forceinline__ long long ta_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // Of an item whose cost counts from a0 on and that has nt units: the units before position x of the count.
 __device__ __forceinline__ int ta_units_before(long long x, long long a0, int nt, int cost, int begin) {
   const long long n = x - a0 - begin;
@@ -117,7 +122,7 @@ __device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPla
   s.nt = (s.total + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
   const int cost = ta_cost(p, s.m);
   const long long count = (long long)s.nt * cost + plan.begin, local = u - plan.pre[lo];
-  const int item = local <= 0x7fffffff ? (int)((unsigned)local / (unsigned)count) : (int)(local / count);
+  const int item = (int)ta_div(local, count);
   const long long a0 = plan.pre[lo] + (long long)item * count;
   const int nrb = ta_blocks(s.m * p.group, p.block);
   s.h = item / nrb;

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT, RG>::THREADS, 1) tree_att
   pdl_trigger();             // after the wait: the join may then read what this kernel's predecessors wrote before its own
   if (warp == 0) ta_plan(p, &plan, blockIdx.x == 0);
   __syncthreads();
-  const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
+  const long long units = plan.pre[p.map.B], per = ta_div(units + p.grid - 1, p.grid);
   const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
   const int pm = (1 << p.c.page_shift) - 1;
 

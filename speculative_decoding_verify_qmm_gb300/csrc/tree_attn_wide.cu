@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
   __syncthreads();
   tc05_fence_after();
   const uint32_t tmem = s_tmem;
-  const long long units = plan.pre[p.map.B], per = (units + p.grid - 1) / p.grid;
+  const long long units = plan.pre[p.map.B], per = ta_div(units + p.grid - 1, p.grid);
   const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
 
   if (warp == Sh::PROD) {
@@ -749,47 +749,63 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
         p.stats[(2 * slot) * p.block + rr] = most;
         p.stats[(2 * slot + 1) * p.block + rr] = weight;
       }
+      // natural element y of a chunk's columns (codes of 4 bits stand at another position inside each 8 elements)
+      auto col = [](int d) { return BITS == 4 ? (d & ~7) + 2 * (d & 3) + ((d >> 2) & 1) : d; };
+      if (split == 1) {
+        // a lane has its row: straight from its registers
+        const long long at = real ? s_out[rr] : 0;
+        auto put = [&](auto is_whole) {
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tmem + TA_O + lanes + 32 * c, o);
-        float* dst = scratch + L * TA_PAD;
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + TA_O + lanes + 32 * c, o);
+            float e[32];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          float4 q4;
-          float* q = reinterpret_cast<float*>(&q4);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int d = 4 * x + y;                    // natural element; codes of 4 bits sit at another position
-            const int at = BITS == 4 ? (d & ~7) + 2 * (d & 3) + ((d >> 2) & 1) : d;
-            q[y] = __uint_as_float(o[at]) * factor;
-          }
-          *reinterpret_cast<float4*>(dst + 4 * x) = q4;
-        }
-        named_bar_sync(1, TA_SOFT * 32);
-        const int d0 = 4 * (L & 7);
-        auto put = [&](auto is_whole, auto is_split) {
-#pragma unroll 2
-          for (int k = L >> 3; k < s.rows; k += 16) {
-            float4 a = *reinterpret_cast<const float4*>(scratch + k * TA_PAD + d0);
-            if constexpr (decltype(is_split)::value) {
-              const float4 b = *reinterpret_cast<const float4*>(scratch + (64 + k) * TA_PAD + d0);
-              a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-            }
+            for (int x = 0; x < 32; ++x) e[x] = __uint_as_float(o[col(x)]) * factor;
+            if (!real) continue;
             if constexpr (decltype(is_whole)::value) {
-              __nv_bfloat162 o2[2] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w)};
-              *reinterpret_cast<uint2*>(p.out + s_out[k] + 32 * c + d0) = *reinterpret_cast<uint2*>(o2);
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) {
+                const uint4 w = make_uint4(ta_pack(e[x], e[x + 1], true), ta_pack(e[x + 2], e[x + 3], true),
+                                           ta_pack(e[x + 4], e[x + 5], true), ta_pack(e[x + 6], e[x + 7], true));
+                *reinterpret_cast<uint4*>(p.out + at + 32 * c + x) = w;
+              }
             } else {
-              *reinterpret_cast<float4*>(p.partial + s_out[k] + 32 * c + d0) = a;
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(p.partial + at + 32 * c + x) = make_float4(e[x], e[x + 1], e[x + 2], e[x + 3]);
             }
           }
         };
-        if (whole) {
-          if (split > 1) put(std::true_type{}, std::true_type{}); else put(std::true_type{}, std::false_type{});
-        } else {
-          if (split > 1) put(std::false_type{}, std::true_type{}); else put(std::false_type{}, std::false_type{});
-        }
+        if (whole) put(std::true_type{}); else put(std::false_type{});
         named_bar_sync(1, TA_SOFT * 32);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + TA_O + lanes + 32 * c, o);
+          float* dst = scratch + L * TA_PAD;
+#pragma unroll
+          for (int x = 0; x < 32; x += 4)
+            *reinterpret_cast<float4*>(dst + x) = make_float4(__uint_as_float(o[col(x)]) * factor, __uint_as_float(o[col(x + 1)]) * factor,
+                                                              __uint_as_float(o[col(x + 2)]) * factor, __uint_as_float(o[col(x + 3)]) * factor);
+          named_bar_sync(1, TA_SOFT * 32);
+          const int d0 = 4 * (L & 7);
+          auto put = [&](auto is_whole) {
+#pragma unroll 2
+            for (int k = L >> 3; k < s.rows; k += 16) {
+              float4 a = *reinterpret_cast<const float4*>(scratch + k * TA_PAD + d0);
+              const float4 b = *reinterpret_cast<const float4*>(scratch + (64 + k) * TA_PAD + d0);
+              a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+              if constexpr (decltype(is_whole)::value) {
+                *reinterpret_cast<uint2*>(p.out + s_out[k] + 32 * c + d0) = make_uint2(ta_pack(a.x, a.y, true), ta_pack(a.z, a.w, true));
+              } else {
+                *reinterpret_cast<float4*>(p.partial + s_out[k] + 32 * c + d0) = a;
+              }
+            }
+          };
+          if (whole) put(std::true_type{}); else put(std::false_type{});
+          named_bar_sync(1, TA_SOFT * 32);
+        }
       }
       if (s_bad[n_seg % TA_FLAGS] && L < D) {
         // V held infinities or NaN in drafted tokens, which were left out of the products: the rows that see one get it here
