@@ -62,8 +62,8 @@ class KVCache:
     def __init__(self, view, tensors):
         self.view, self.tensors, self.ref = view, tensors, ctypes.byref(view)
         self.k, self.v = tensors[0], tensors[1]
-        self.device = self.k.device
-        self.width = view.n_kv_heads * view.head_dim
+        self.device, self.index = self.k.device, self.k.get_device()
+        self.head_dim, self.width = view.head_dim, view.n_kv_heads * view.head_dim
 
 
 class KVLayers:
@@ -74,7 +74,7 @@ class KVLayers:
         if not self.caches or any(c.device != self.caches[0].device for c in self.caches):
             raise SVError(SV_EINVAL, "the layers' caches must be on one device, and at least one")
         self.array = (KVCacheView * len(self.caches))(*[c.view for c in self.caches])
-        self.device = self.caches[0].device
+        self.device, self.index = self.caches[0].device, self.caches[0].index
 
 SV_CAP_MAX = 31
 
@@ -259,28 +259,35 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _tensors(device, dtype, *tensors):
-    """Refuse tensors that the C side would read as something else."""
-    for t in tensors:
-        if t.dtype != dtype or t.device != device:
-            raise SVError(SV_EINVAL, "expected a %s tensor on %s, got %s on %s" % (dtype, device, t.dtype, t.device))
+# Checks of the attention-side calls.  They run on every call of a latency-bound step, so each asks a tensor for as little
+# as it can: dtypes by identity, devices by index.
+
+def _refuse(what, t):
+    raise SVError(SV_EINVAL, "%s, got %s %s with strides %s on %s" % (what, t.dtype, tuple(t.shape), t.stride(), t.device))
 
 
-def _rows(name, t, rows, width):
-    """Refuse anything but a [>= rows, >= width] matrix with adjacent elements; returns its row stride."""
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width or (t.stride(1) != 1 and width > 1):
-        raise SVError(SV_EINVAL, "%s must be a [%d, %d] matrix with unit inner stride, got %s with strides %s"
-                      % (name, rows, width, tuple(t.shape), t.stride()))
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+def _matrix(name, t, dtype, dev, rows, width):
+    """Row stride of a [>= rows, >= width] matrix on device `dev` with adjacent elements; anything else is refused."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] < rows or shape[1] < width \
+            or (strides[1] != 1 and width > 1):
+        _refuse("%s must be a %s [%d, %d] matrix on cuda:%d with unit inner stride" % (name, dtype, rows, width, dev), t)
+    return strides[0] if shape[0] > 1 else max(strides[0], width)
 
 
-def _launch_stream(stream, device):
-    """Raw handle of the stream to launch on; the tensors' device must be the current one."""
-    import torch
-    here = torch.cuda.current_device()
-    if device.type != "cuda" or device.index != here:
-        raise SVError(SV_EINVAL, "tensors on %s, current device cuda:%d" % (device, here))
-    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+def _vector(name, t, dtype, dev, n):
+    """Data pointer of a contiguous tensor of at least n elements on device `dev`; anything else is refused."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        _refuse("%s must be a contiguous %s tensor of %d elements on cuda:%d" % (name, dtype, n, dev), t)
+    return t.data_ptr()
+
+
+def _table(t, dtype, dev, B):
+    """(data pointer, width) of a block table."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] < B or not t.is_contiguous():
+        _refuse("block_table must be a contiguous %s [%d, pages] tensor on cuda:%d" % (dtype, B, dev), t)
+    return t.data_ptr(), shape[1]
 
 
 class Library:
@@ -288,6 +295,7 @@ class Library:
 
     def __init__(self, path=LIB_PATH):
         self.lib = load_library(path)
+        self._torch = None
 
     # -------------------------------------------------------------- plumbing
     def check(self, status):
@@ -576,18 +584,14 @@ class Library:
         if k.dim() != 4 or k.shape != v.shape or k.device.type != "cuda" or len(side) not in (0, 4):
             raise SVError(SV_EINVAL, "k and v must be equal 4-d CUDA tensors, scales and biases all given or none")
         pages, heads, page, last = k.shape
+        dim, bits = (side[0].shape[-1] * 64, 0) if side else (last, 16)
         if side:
-            _tensors(k.device, torch.int32, k, v)
-            _tensors(k.device, torch.float16, *side)
-            dim = side[0].shape[-1] * 64
             bits = last * 32 // dim if dim else 0
             if any(tuple(t.shape) != (pages, heads, page, dim // 64) for t in side) or last * 32 != dim * bits:
                 raise SVError(SV_EINVAL, "scales and biases must be [pages, heads, page, dim / 64]")
-        else:
-            _tensors(k.device, torch.bfloat16, k, v)
-            dim, bits = last, 16
-        if not all(t.is_contiguous() for t in [k, v] + side):
-            raise SVError(SV_EINVAL, "cache tensors must be contiguous")
+        for t, want in [(t, torch.int32 if side else torch.bfloat16) for t in (k, v)] + [(t, torch.float16) for t in side]:
+            if t.dtype is not want or t.device != k.device or not t.is_contiguous():
+                _refuse("cache tensors must be contiguous, on one device, and %s" % want, t)
         ptrs = [t.data_ptr() for t in side] or [None] * 4
         return KVCache(KVCacheView(k.data_ptr(), v.data_ptr(), *ptrs, pages, page, heads, dim, bits), [k, v] + side)
 
@@ -605,80 +609,79 @@ class Library:
     def kv_layers(caches):
         return KVLayers(caches)
 
+    def _launch_stream(self, stream, dev):
+        """Raw handle of the stream to launch on; the tensors' device must be the current one."""
+        if self._torch is None:
+            import torch
+            self._torch = torch
+        if dev < 0 or self._torch._C._cuda_getDevice() != dev:
+            raise SVError(SV_EINVAL, "tensors on cuda:%d (-1: the host), which is not the current device" % dev)
+        return self._torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
     def qk_norm_rope(self, q, k, head_dim, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
                      norm=True, interleaved=False, q_out=None, k_out=None, stream=None):
         """(q_out, k_out).  q [rows, q_heads * head_dim], k [rows, kv_heads * head_dim] or None; the
         rotary width is 2 * len(inv_freq) (no rotation without it); q_out = q works in place."""
         import torch
-        rows, dev = q.shape[0], q.device
+        bf16, dev = torch.bfloat16, q.get_device()
+        handle = self._launch_stream(stream, dev)
+        (rows, qw), kw = q.shape, 0
         if q_out is None:
-            q_out = torch.empty((rows, q.shape[1]), dtype=q.dtype, device=dev)
-        mats = [("q", q), ("q_out", q_out)]
+            q_out = torch.empty((rows, qw), dtype=bf16, device=q.device)
+        ldq, ldqo, ldk, ldko = _matrix("q", q, bf16, dev, rows, qw), _matrix("q_out", q_out, bf16, dev, rows, qw), 0, 0
+        kp = kop = qwp = kwp = pos = inv = None
         if k is not None:
+            kw = k.shape[-1]
             if k_out is None:
-                k_out = torch.empty((rows, k.shape[1]), dtype=k.dtype, device=dev)
-            mats += [("k", k), ("k_out", k_out)]
-        _tensors(dev, torch.bfloat16, *[m for _, m in mats], *[w for w in (q_weight, k_weight) if w is not None])
-        for w in (q_weight, k_weight):
-            if w is not None and (w.numel() != head_dim or not w.is_contiguous()):
-                raise SVError(SV_EINVAL, "a norm weight must be a contiguous [%d] tensor" % head_dim)
-        ld = [_rows(name, m, rows, (k if name[0] == "k" else q).shape[1]) for name, m in mats] + [0, 0]
+                k_out = torch.empty((rows, kw), dtype=bf16, device=q.device)
+            ldk, ldko = _matrix("k", k, bf16, dev, rows, kw), _matrix("k_out", k_out, bf16, dev, rows, kw)
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+        if head_dim < 1 or qw % head_dim or kw % head_dim:
+            raise SVError(SV_EINVAL, "q and k widths must be multiples of head_dim")
+        if q_weight is not None:
+            qwp = _vector("q_weight", q_weight, bf16, dev, head_dim)
+        if k_weight is not None:
+            kwp = _vector("k_weight", k_weight, bf16, dev, head_dim)
         rot = 0
         if inv_freq is not None:
             rot = 2 * inv_freq.numel()
-            _tensors(dev, torch.float32, inv_freq)
-            _tensors(dev, torch.int32, positions)
-            if positions.numel() < rows or not positions.is_contiguous() or not inv_freq.is_contiguous():
-                raise SVError(SV_EINVAL, "positions must be a contiguous [rows] tensor, inv_freq contiguous")
-        if head_dim < 1 or q.shape[1] % head_dim or (k is not None and k.shape[1] % head_dim):
-            raise SVError(SV_EINVAL, "q and k widths must be multiples of head_dim")
-        opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            inv = _vector("inv_freq", inv_freq, torch.float32, dev, rot // 2)
+            if rot:
+                pos = _vector("positions", positions, torch.int32, dev, rows)
         if rows:
-            self.check(self.lib.sv_qk_norm_rope(
-                q.data_ptr(), ld[0], opt(k), ld[2], rows, q.shape[1] // head_dim,
-                0 if k is None else k.shape[1] // head_dim, head_dim, 1 if norm else 0, opt(q_weight), opt(k_weight), eps,
-                positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, rot,
-                1 if interleaved else 0, q_out.data_ptr(), ld[1], opt(k_out), ld[3], _launch_stream(stream, dev)))
+            status = self.lib.sv_qk_norm_rope(q.data_ptr(), ldq, kp, ldk, rows, qw // head_dim, kw // head_dim, head_dim, norm,
+                                              qwp, kwp, eps, pos, inv if rot else None, rot, interleaved, q_out.data_ptr(), ldqo,
+                                              kop, ldko, handle)
+            if status:
+                self.check(status)
         return q_out, k_out
 
-    @staticmethod
-    def _sequences(device, offs, lens, table):
-        """Checks of the arrays that place requests in the cache; returns (B, rows, table width)."""
+    def _kv_rows(self, call, cache, row_offsets, first, block_table, k, v, stream):
         import torch
+        i32, bf16, dev, width = torch.int32, torch.bfloat16, cache.index, cache.width
+        offs = row_offsets if isinstance(row_offsets, ctypes.Array) else self.row_offsets(row_offsets)
         B = len(offs) - 1
-        _tensors(device, torch.int32, lens, table)
-        if table.dim() != 2 or table.shape[0] < B or lens.numel() < B or not table.is_contiguous() \
-                or not lens.is_contiguous():
-            raise SVError(SV_EINVAL, "block_table must be a contiguous [B, pages] tensor and the lengths [B], B = %d" % B)
-        return B, offs[B], table.shape[1]
+        rows = offs[B]
+        lens, (table, pages) = _vector("the lengths", first, i32, dev, B), _table(block_table, i32, dev, B)
+        ldk, ldv = _matrix("k", k, bf16, dev, rows, width), _matrix("v", v, bf16, dev, rows, width)
+        handle = self._launch_stream(stream, dev)
+        if rows:
+            status = call(cache.ref, B, offs, lens, table, pages, k.data_ptr(), ldk, v.data_ptr(), ldv, handle)
+            if status:
+                self.check(status)
 
     def kv_append(self, cache, row_offsets, kv_len, block_table, k, v, stream=None):
         """Rows of k and v [rows, kv_heads * head_dim] into the cache at kv_len[b], kv_len[b] + 1, ..."""
-        import torch
-        offs = self.row_offsets(row_offsets)
-        B, rows, pages = self._sequences(cache.device, offs, kv_len, block_table)
-        _tensors(cache.device, torch.bfloat16, k, v)
-        if rows:
-            self.check(self.lib.sv_kv_append(
-                cache.ref, B, offs, kv_len.data_ptr(), block_table.data_ptr(), pages, k.data_ptr(),
-                _rows("k", k, rows, cache.width), v.data_ptr(), _rows("v", v, rows, cache.width),
-                _launch_stream(stream, cache.device)))
+        self._kv_rows(self.lib.sv_kv_append, cache, row_offsets, kv_len, block_table, k, v, stream)
 
     def kv_read(self, cache, row_offsets, first, block_table, k=None, v=None, stream=None):
         """(k, v) bf16 [rows, kv_heads * head_dim]: row i of request b from position first[b] + i."""
-        import torch
-        offs = self.row_offsets(row_offsets)
-        B, rows, pages = self._sequences(cache.device, offs, first, block_table)
-        if k is None:
-            k = torch.empty((rows, cache.width), dtype=torch.bfloat16, device=cache.device)
-        if v is None:
-            v = torch.empty((rows, cache.width), dtype=torch.bfloat16, device=cache.device)
-        _tensors(cache.device, torch.bfloat16, k, v)
-        if rows:
-            self.check(self.lib.sv_kv_read(
-                cache.ref, B, offs, first.data_ptr(), block_table.data_ptr(), pages, k.data_ptr(),
-                _rows("k", k, rows, cache.width), v.data_ptr(), _rows("v", v, rows, cache.width),
-                _launch_stream(stream, cache.device)))
+        if k is None or v is None:
+            import torch
+            shape = (row_offsets[len(row_offsets) - 1], cache.width)
+            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+            v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+        self._kv_rows(self.lib.sv_kv_read, cache, row_offsets, first, block_table, k, v, stream)
         return k, v
 
     def tree_attention_workspace_bytes(self, cache, row_offsets, n_q_heads):
@@ -690,31 +693,29 @@ class Library:
         """out bf16 [rows, q_heads * head_dim]; tree_mask int64 [rows] (bit j: the row sees the request's
         drafted row j), None for a chain; scale defaults to head_dim ** -0.5."""
         import torch
-        offs = self.row_offsets(row_offsets)
-        dev = cache.device
-        B, rows, pages = self._sequences(dev, offs, kv_len, block_table)
-        width = n_q_heads * cache.view.head_dim
+        i32, bf16, dev, dim = torch.int32, torch.bfloat16, cache.index, cache.head_dim
+        offs = row_offsets if isinstance(row_offsets, ctypes.Array) else self.row_offsets(row_offsets)
+        B, width = len(offs) - 1, n_q_heads * dim
+        rows = offs[B]
+        lens, (table, pages) = _vector("kv_len", kv_len, i32, dev, B), _table(block_table, i32, dev, B)
+        mask = None if tree_mask is None else _vector("tree_mask", tree_mask, torch.int64, dev, rows)
         if out is None:
-            out = torch.empty((q.shape[0], width), dtype=torch.bfloat16, device=dev)
-        _tensors(dev, torch.bfloat16, q, out)
-        if tree_mask is not None:
-            _tensors(dev, torch.int64, tree_mask)
-            if tree_mask.numel() < rows or not tree_mask.is_contiguous():
-                raise SVError(SV_EINVAL, "tree_mask must be a contiguous [rows] tensor")
-        ldq, ldo = _rows("q", q, rows, width), _rows("out", out, rows, width)
+            out = torch.empty((q.shape[0], width), dtype=bf16, device=cache.device)
+        ldq, ldo = _matrix("q", q, bf16, dev, rows, width), _matrix("out", out, bf16, dev, rows, width)
+        handle = self._launch_stream(stream, dev)
         if workspace is None:
             workspace = torch.empty(max(256, self.tree_attention_workspace_bytes(cache, offs, n_q_heads)),
-                                    dtype=torch.uint8, device=dev)
+                                    dtype=torch.uint8, device=cache.device)
             if stream is not None:
                 workspace.record_stream(stream)  # the call outlives this tensor on that stream
-        elif workspace.device != dev:
-            raise SVError(SV_EINVAL, "workspace on %s, cache on %s" % (workspace.device, dev))
+        elif workspace.get_device() != dev:
+            _refuse("the workspace must be on cuda:%d" % dev, workspace)
         if rows:
-            self.check(self.lib.sv_tree_attention(
-                cache.ref, B, offs, kv_len.data_ptr(), block_table.data_ptr(), pages, q.data_ptr(), ldq, n_q_heads,
-                cache.view.head_dim ** -0.5 if scale is None else scale,
-                None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(), ldo, workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), _launch_stream(stream, dev)))
+            status = self.lib.sv_tree_attention(cache.ref, B, offs, lens, table, pages, q.data_ptr(), ldq, n_q_heads,
+                                                dim ** -0.5 if scale is None else scale, mask, out.data_ptr(), ldo,
+                                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+            if status:
+                self.check(status)
         return out
 
     def kv_commit(self, caches, kv_len, block_table, path, path_len, stream=None):
@@ -722,16 +723,15 @@ class Library:
         every cache of `caches` (a list of KVCache, or kv_layers() of one)."""
         import torch
         layers = caches if isinstance(caches, KVLayers) else KVLayers(caches)
-        dev = layers.device
-        _tensors(dev, torch.int32, kv_len, block_table, path, path_len)
-        B = kv_len.numel()
-        if block_table.dim() != 2 or path.dim() != 2 or block_table.shape[0] < B or path.shape[0] < B \
-                or path_len.numel() < B or not (block_table.is_contiguous() and path.is_contiguous()
-                                                and kv_len.is_contiguous() and path_len.is_contiguous()):
-            raise SVError(SV_EINVAL, "block_table [B, pages], path [B, n] and path_len [B] must be contiguous, B = %d" % B)
-        self.check(self.lib.sv_kv_commit(
-            layers.array, len(layers.array), B, kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-            path.data_ptr(), path.shape[1], path_len.data_ptr(), _launch_stream(stream, dev)))
+        i32, dev, B = torch.int32, layers.index, kv_len.numel()
+        lens, (table, pages) = _vector("kv_len", kv_len, i32, dev, B), _table(block_table, i32, dev, B)
+        if path.dim() != 2 or path.shape[0] < B:
+            _refuse("path must be an int32 [%d, n] tensor" % B, path)
+        status = self.lib.sv_kv_commit(layers.array, len(layers.array), B, lens, table, pages,
+                                       _vector("path", path, i32, dev, 0), path.shape[1],
+                                       _vector("path_len", path_len, i32, dev, B), self._launch_stream(stream, dev))
+        if status:
+            self.check(status)
 
     def residual_add(self, h, t, stream=None):
         self.check(self.lib.sv_residual_add(_ptr(h), h.stride(0), _ptr(t), t.stride(0), h.shape[0], h.shape[1],

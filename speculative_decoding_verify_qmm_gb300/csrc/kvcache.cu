@@ -5,15 +5,23 @@
 // codes are in the weight format: affine, group 64, fp16 scale and bias).
 //
 // All three are bound by memory, or by launch latency for a drafted block.
-// A thread owns 8 adjacent values of a head (16 bytes of bf16, 8 or 4 bytes of
-// codes); a quantization group is 8 adjacent lanes, whose extremes meet by three
-// shuffles, so a value is read once and never staged.
+//
+// Rows.  A thread owns 8 adjacent values of a head (16 bytes of bf16, 8 or 4
+// bytes of codes), and the same ones of every row it works on, so that its heads,
+// pointers and strides are set up once; a quantization group is 8 adjacent lanes.
+// A value is read once and never staged.  A CTA takes tiles of consecutive rows; a
+// row's request, page and place are looked up by one thread - the next tile's
+// while the present one is worked on - and handed over in shared memory, for a
+// lookup by every thread is three dependent loads against one load of data.
 #include "sv_kv.cuh"
 
 namespace sv {
 
 constexpr float KV_FAR = 65280.f;  // bf16; with it scale * code + bias <= 65344 stays finite in fp16
-constexpr int KV_THREADS = 256;
+constexpr int KV_THREADS = 256;    // at most
+constexpr int KV_AHEAD = 4;        // chunks a thread has in flight when rows are many
+constexpr int KV_STEPS = 2;        // times that many rows of a thread per tile
+constexpr int KV_CTAS = 5;         // CTAs per SM of a long call
 
 struct KvRows {
   KvCache c;
@@ -24,6 +32,8 @@ struct KvRows {
   uint16_t *k, *v;          // bf16 rows (read by append, written by read)
   int ldk, ldv;
   bool vec_k, vec_v;
+  int cols, step;           // chunks of a row (K's, then V's); rows that a CTA's threads cover at once
+  int tile, tiles;          // rows of a tile
 };
 
 __device__ __forceinline__ uint4 load8(const uint16_t* u, bool vec) {
@@ -44,135 +54,259 @@ __device__ __forceinline__ void store8(uint16_t* u, const uint4& x, bool vec) {
   }
 }
 
-// A thread's place: row, K or V, head, chunk of 8 values; false past the last row.
-struct KvItem {
-  int row, head, chunk, b;
-  bool is_v, live;
-  long long page;   // -1: bad input
-  int place;
-};
-__device__ __forceinline__ KvItem kv_item(const KvRows& a) {
-  const int chunks = a.c.dim / 8, per_row = 2 * a.c.heads * chunks;
-  const long long idx = (long long)blockIdx.x * KV_THREADS + threadIdx.x;
-  KvItem it;
-  it.live = idx < (long long)a.map.offs[a.map.B] * per_row;
-  it.row = it.live ? (int)(idx / per_row) : 0;
-  const int r = it.live ? (int)(idx - (long long)it.row * per_row) : 0;
-  it.is_v = r >= a.c.heads * chunks;
-  const int hc = it.is_v ? r - a.c.heads * chunks : r;
-  it.head = hc / chunks;
-  it.chunk = hc - it.head * chunks;
-  it.page = -1;
-  it.place = 0;
-  if (it.live) {
-    it.b = request_of(a.map, it.row);
-    const long long first = a.first[it.b];
-    const long long pos = first + (it.row - a.map.offs[it.b]);
-    if (first >= 0) it.page = kv_page_of(a.c, a.table, a.table_pages, it.b, pos);
-    it.place = (int)(pos & ((1ll << a.c.page_shift) - 1));
-    if (it.page < 0) raise_error(ERR_BAD_INPUT);
+// Byte offset of a row's values in head 0; negative for bad input.
+template <int BITS>
+__device__ __forceinline__ long long kv_row_bytes(const KvRows& a, int row) {
+  const int b = request_of(a.map, row);
+  const int first = a.first[b];
+  const long long pos = (long long)first + (row - a.map.offs[b]);
+  const long long page = first < 0 ? -1 : kv_page_of(a.c, a.table, a.table_pages, b, pos);
+  if (page < 0) {
+    raise_error(ERR_BAD_INPUT);
+    return -1;
   }
-  return it;
+  return (long long)(kv_token(a.c, (int)page, 0, (int)(pos & ((1ll << a.c.page_shift) - 1))) * (a.c.dim * BITS / 8));
 }
 
+// What a thread owns of every row.
+struct KvColumn {
+  bool live, vec;
+  int row, chunk;        // of the tile's rows, the first; chunk of the head
+  uint8_t* data;         // its values in token 0
+  __half *scale, *bias;
+  uint16_t* rows;        // its values in row 0 of the caller's
+  size_t ld;
+};
 template <int BITS>
+__device__ __forceinline__ KvColumn kv_column(const KvRows& a) {
+  KvColumn m;
+  const int wide = min(a.cols, KV_THREADS);   // columns of a CTA
+  m.row = threadIdx.x / wide;
+  const int col = blockIdx.y * KV_THREADS + threadIdx.x - m.row * wide;
+  m.live = m.row < a.step && col < a.cols;
+  const int half = a.cols >> 1, chunks = a.c.dim / 8;
+  const bool is_v = col >= half;
+  const int hc = is_v ? col - half : col, head = hc / chunks;
+  m.chunk = hc - head * chunks;
+  const size_t tok = (size_t)head << a.c.page_shift;
+  m.data = (is_v ? a.c.p.v : a.c.p.k) + tok * (a.c.dim * BITS / 8) + m.chunk * BITS;
+  m.scale = (is_v ? a.c.p.vs : a.c.p.ks) + tok * (a.c.dim / GROUP) + m.chunk / 8;
+  m.bias = (is_v ? a.c.p.vb : a.c.p.kb) + tok * (a.c.dim / GROUP) + m.chunk / 8;
+  m.rows = (is_v ? a.v : a.k) + head * a.c.dim + m.chunk * 8;
+  m.ld = is_v ? a.ldv : a.ldk;
+  m.vec = is_v ? a.vec_v : a.vec_k;
+  return m;
+}
+// A row's scales lie at 1 / (4 * BITS) of its codes' byte offset: 2 bytes for 64 codes.
+template <int BITS>
+__device__ __forceinline__ __half* kv_side(__half* base, long long bytes) {
+  return reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(base) + (bytes >> (BITS == 8 ? 5 : 4)));
+}
+
+// The loop both kernels share.  work(rows, look) handles AHEAD rows at once: it calls look(offsets) for
+// their byte offsets - after it has asked for the caller's rows, where it reads those - and the first look of a
+// tile also looks the CTA's next tile up.  All threads of a CTA make the same steps: work may shuffle.
+template <int BITS, int AHEAD, typename Work>
+__device__ __forceinline__ void kv_tiles(const KvRows& a, const KvColumn& m, Work work) {
+  __shared__ long long s_at[2][KV_THREADS];
+  const int tid = threadIdx.x, rows = a.map.offs[a.map.B];
+  bool first = true;
+  int buf = 0;
+  for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, buf ^= 1) {
+    const int base = t * a.tile, n = min(a.tile, rows - base);
+    for (int r0 = 0; r0 < a.tile; r0 += AHEAD * a.step) {
+      int r[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) r[i] = r0 + m.row + i * a.step;
+      work(base, r, n, [&](long long (&at)[AHEAD]) {
+        if (first) {
+          if (tid < n) s_at[0][tid] = kv_row_bytes<BITS>(a, base + tid);
+          __syncthreads();
+          first = false;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) at[i] = m.live && r[i] < n ? s_at[buf][r[i]] : -1;
+      });
+      if (r0 == 0) {
+        const int next = (t + (int)gridDim.x) * a.tile + tid;
+        if (tid < a.tile && t + (int)gridDim.x < a.tiles && next < rows) s_at[buf ^ 1][tid] = kv_row_bytes<BITS>(a, next);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// bf16 number e of a chunk.
+__device__ __forceinline__ float chunk_value(const uint4& r, int e) {
+  const uint32_t u = e < 2 ? r.x : (e < 4 ? r.y : (e < 6 ? r.z : r.w));
+  return __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
+}
+
+template <int BITS, int AHEAD>
 __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const __grid_constant__ KvRows a) {
   pdl_trigger();
   pdl_wait();
-  const KvItem it = kv_item(a);
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (it.live) {
-    const uint16_t* src = it.is_v ? a.v + (size_t)it.row * a.ldv : a.k + (size_t)it.row * a.ldk;
-    raw = load8(src + it.head * a.c.dim + it.chunk * 8, it.is_v ? a.vec_v : a.vec_k);
-  }
-  const bool ok = it.live && it.page >= 0;
-  const size_t tok = ok ? kv_token(a.c, (int)it.page, it.head, it.place) : 0;
-  if constexpr (BITS == 16) {
-    if (ok) {
-      uint8_t* base = it.is_v ? a.c.p.v : a.c.p.k;
-      *reinterpret_cast<uint4*>(base + (tok * a.c.dim + it.chunk * 8) * 2) = raw;
-    }
-  } else {
-    float x[8];
-    const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&raw);
-    float lo = INFINITY, hi = -INFINITY;
-    int nan = 0;
+  const KvColumn m = kv_column<BITS>(a);
+  const int lane = threadIdx.x & 31;
+  kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int n, auto look) {
+    uint4 raw[AHEAD];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float f = e & 1 ? __bfloat162float(r2[e / 2].y) : __bfloat162float(r2[e / 2].x);
-      nan |= f != f;
-      x[e] = fminf(fmaxf(f, -KV_FAR), KV_FAR);
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
+    for (int i = 0; i < AHEAD; ++i) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (m.live && r[i] < n) raw[i] = load8(m.rows + (size_t)(base + r[i]) * m.ld, m.vec);
     }
+    long long at[AHEAD];
+    look(at);
+    if constexpr (BITS == 16) {
 #pragma unroll
-    for (int off = 4; off; off >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-      nan |= __shfl_xor_sync(0xffffffffu, nan, off);
-    }
-    constexpr int TOP = (1 << BITS) - 1;
-    // the format's own roundings, each IEEE: a host or torch program gets the same codes
-    const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), (float)TOP));
-    const __half b16 = __float2half_rn(lo);
-    const float s = __half2float(s16), b = __half2float(b16);
-    uint32_t w[2] = {0, 0};
-    if (s > 0.f && !nan) {
+      for (int i = 0; i < AHEAD; ++i)
+        if (at[i] >= 0) *reinterpret_cast<uint4*>(m.data + at[i]) = raw[i];
+    } else {
+      constexpr int TOP = (1 << BITS) - 1;
+      // Each group's extremes, as bf16 (exact) in pairs: (max, max of the negated).  A NaN stays.
+      __nv_bfloat162 ends[AHEAD];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], b), s)), 0.f), (float)TOP);
-        const uint32_t code = (uint32_t)c;
-        if constexpr (BITS == 8) w[e / 4] |= code << (8 * (e % 4));
-        else w[0] |= code << (4 * e);
+      for (int i = 0; i < AHEAD; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        auto pair = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+        const __nv_bfloat162 hi = __hmax2_nan(__hmax2_nan(pair(w[0]), pair(w[1])), __hmax2_nan(pair(w[2]), pair(w[3])));
+        const __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(pair(w[0]), pair(w[1])), __hmin2_nan(pair(w[2]), pair(w[3])));
+        ends[i] = __hmax2_nan(__halves2bfloat162(hi.x, __hneg(lo.x)), __halves2bfloat162(hi.y, __hneg(lo.y)));
+      }
+      // Over the 8 lanes of a group.  Of 4 groups a lane ends up with number lane % 4, so that the group's own
+      // arithmetic is done once for the four: each exchange halves the groups a lane still reduces.
+      auto other = [](__nv_bfloat162 x, int off) { return __hmax2_nan(x, __shfl_xor_sync(0xffffffffu, x, off)); };
+      __nv_bfloat162 mine;
+      if constexpr (AHEAD == 4) {
+        const bool b0 = lane & 1, b1 = lane & 2;
+        const __nv_bfloat162 s0 = __shfl_xor_sync(0xffffffffu, b0 ? ends[0] : ends[1], 1);
+        const __nv_bfloat162 s1 = __shfl_xor_sync(0xffffffffu, b0 ? ends[2] : ends[3], 1);
+        const __nv_bfloat162 p0 = __hmax2_nan(b0 ? ends[1] : ends[0], s0), p1 = __hmax2_nan(b0 ? ends[3] : ends[2], s1);
+        const __nv_bfloat162 s2 = __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
+        mine = other(__hmax2_nan(b1 ? p1 : p0, s2), 4);
+      } else {
+        static_assert(AHEAD == 1, "one group, or four");
+        mine = other(other(other(ends[0], 1), 2), 4);
+      }
+      const float top = __bfloat162float(mine.x), bottom = -__bfloat162float(mine.y);
+      const bool nan = top != top;
+      const float hi = fminf(fmaxf(top, -KV_FAR), KV_FAR), lo = fminf(fmaxf(bottom, -KV_FAR), KV_FAR);
+      // The format's own roundings, each IEEE: a host or torch program gets the same codes.
+      const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), (float)TOP)), b16 = __float2half_rn(lo);
+      const float s_mine = __half2float(s16);
+      // A code is rint((x - b) / s) clamped to [0, TOP], the difference and the quotient each rounded.  Here
+      // the quotient comes from a product with 1 / (s * TOP), off by less than TOP * (2^-23 + 2^-24) < 5e-5:
+      // where it lies further than that from a half, rint is the same, and the few threads with a closer
+      // one divide.  The saturation is the clamp: x beyond KV_FAR gives an end of the range, as lo and hi are
+      // clamped to it.  A group without a range, or with a NaN, has codes 0.
+      const float inv_mine = s_mine > 0.f && !nan ? __fdiv_rn(1.f, s_mine * (float)TOP) : 0.f;
+      const uint32_t side_mine = nan ? 0x7fff7fffu : __half_as_ushort(s16) | ((uint32_t)__half_as_ushort(b16) << 16);
+      constexpr float MAGIC = 8388608.f;  // 2^23: its sum with a small value rounds that to an integer, in the low bits
+      uint32_t word[AHEAD][BITS / 4], side[AHEAD];
+      float far = 0.f;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float inv = AHEAD == 1 ? inv_mine : __shfl_sync(0xffffffffu, inv_mine, (lane & 24) + i);
+        side[i] = AHEAD == 1 ? side_mine : __shfl_sync(0xffffffffu, side_mine, (lane & 24) + i);
+        const float b = __half2float(__ushort_as_half((unsigned short)(side[i] >> 16)));
+        uint32_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float unit = __saturatef(__fsub_rn(chunk_value(raw[i], e), b) * inv);
+          const float sum = fmaf(unit, (float)TOP, MAGIC);
+          q[e] = __float_as_uint(sum);
+          far = fmaxf(far, fabsf(fmaf(unit, (float)TOP, MAGIC - sum)));
+        }
+        if constexpr (BITS == 8) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            word[i][e] = __byte_perm(__byte_perm(q[4 * e], q[4 * e + 1], 0x0040), __byte_perm(q[4 * e + 2], q[4 * e + 3], 0x0040), 0x5410);
+        } else {  // the low 16 bits of each sum: MAGIC's own bits lie above them
+          const uint32_t u = q[0] + 16u * q[1] + 256u * q[2] + 4096u * q[3], v = q[4] + 16u * q[5] + 256u * q[6] + 4096u * q[7];
+          word[i][0] = __byte_perm(u, v, 0x5410);
+        }
+      }
+      if (far > 0.49995f) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const float s = __half2float(__ushort_as_half((unsigned short)side[i]));
+          const float b = __half2float(__ushort_as_half((unsigned short)(side[i] >> 16)));
+          if (!(s > 0.f)) continue;  // no range, or NaN
+#pragma unroll
+          for (int e = 0; e < BITS / 4; ++e) word[i][e] = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float c = rintf(__fdiv_rn(__fsub_rn(chunk_value(raw[i], e), b), s));
+            word[i][e * BITS / 32] |= (uint32_t)fminf(fmaxf(c, 0.f), (float)TOP) << (e * BITS % 32);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (at[i] < 0) continue;
+        if constexpr (BITS == 8) *reinterpret_cast<uint2*>(m.data + at[i]) = make_uint2(word[i][0], word[i][1]);
+        else *reinterpret_cast<uint32_t*>(m.data + at[i]) = word[i][0];
+        if ((m.chunk & 7) == 0) {
+          *kv_side<BITS>(m.scale, at[i]) = __ushort_as_half((unsigned short)side[i]);
+          *kv_side<BITS>(m.bias, at[i]) = __ushort_as_half((unsigned short)(side[i] >> 16));
+        }
       }
     }
-    if (ok) {
-      uint8_t* dst = (it.is_v ? a.c.p.v : a.c.p.k) + tok * (a.c.dim * BITS / 8) + it.chunk * BITS;
-      if constexpr (BITS == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = w[0];
-      if ((it.chunk & 7) == 0) {
-        const size_t g = tok * (a.c.dim / GROUP) + it.chunk / 8;
-        const __half q16 = __ushort_as_half((unsigned short)0x7fff);
-        (it.is_v ? a.c.p.vs : a.c.p.ks)[g] = nan ? q16 : s16;
-        (it.is_v ? a.c.p.vb : a.c.p.kb)[g] = nan ? q16 : b16;
-      }
-    }
-  }
+  });
 }
 
-template <int BITS>
+template <int BITS, int AHEAD>
 __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const __grid_constant__ KvRows a) {
   pdl_trigger();
   pdl_wait();
-  const KvItem it = kv_item(a);
-  if (!it.live || it.page < 0) return;
-  const size_t tok = kv_token(a.c, (int)it.page, it.head, it.place);
-  const uint8_t* base = it.is_v ? a.c.p.v : a.c.p.k;
-  uint4 out;
-  if constexpr (BITS == 16) {
-    out = *reinterpret_cast<const uint4*>(base + (tok * a.c.dim + it.chunk * 8) * 2);
-  } else {
-    const uint8_t* src = base + tok * (a.c.dim * BITS / 8) + it.chunk * BITS;
-    uint32_t w[2] = {0, 0};
-    if constexpr (BITS == 8) {
-      const uint2 t = *reinterpret_cast<const uint2*>(src);
-      w[0] = t.x;
-      w[1] = t.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(src);
-    }
-    const size_t g = tok * (a.c.dim / GROUP) + it.chunk / 8;
-    const float s = __half2float((it.is_v ? a.c.p.vs : a.c.p.ks)[g]);
-    const float b = __half2float((it.is_v ? a.c.p.vb : a.c.p.kb)[g]);
-    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(&out);
+  const KvColumn m = kv_column<BITS>(a);
+  kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int, auto look) {
+    long long at[AHEAD];
+    look(at);
+    uint4 raw[AHEAD];             // bf16, or codes in x (and y)
+    __half scale[AHEAD], bias[AHEAD];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t code = BITS == 8 ? (w[e / 4] >> (8 * (e % 4))) & 255u : (w[0] >> (4 * e)) & 15u;
-      o[e] = __float2bfloat16_rn(fmaf(s, (float)code, b));
+    for (int i = 0; i < AHEAD; ++i) {
+      if (at[i] < 0) continue;
+      if constexpr (BITS == 16) {
+        raw[i] = *reinterpret_cast<const uint4*>(m.data + at[i]);
+      } else {
+        if constexpr (BITS == 8) {
+          const uint2 t = *reinterpret_cast<const uint2*>(m.data + at[i]);
+          raw[i].x = t.x;
+          raw[i].y = t.y;
+        } else {
+          raw[i].x = *reinterpret_cast<const uint32_t*>(m.data + at[i]);
+        }
+        scale[i] = *kv_side<BITS>(m.scale, at[i]);
+        bias[i] = *kv_side<BITS>(m.bias, at[i]);
+      }
     }
-  }
-  uint16_t* dst = it.is_v ? a.v + (size_t)it.row * a.ldv : a.k + (size_t)it.row * a.ldk;
-  store8(dst + it.head * a.c.dim + it.chunk * 8, out, it.is_v ? a.vec_v : a.vec_k);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if constexpr (BITS != 16) {
+        const float s = __half2float(scale[i]), b = __half2float(bias[i]);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // a code in the low bits of 2^23 is that number plus 2^23
+          uint32_t u;
+          if constexpr (BITS == 8) u = __byte_perm(e < 4 ? raw[i].x : raw[i].y, 0x4b000000u, 0x7550 + e % 4);
+          else u = ((raw[i].x >> (4 * e)) & 15u) | 0x4b000000u;
+          x[e] = fmaf(s, __uint_as_float(u) - 8388608.f, b);
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (at[i] >= 0) store8(m.rows + (size_t)(base + r[i]) * m.ld, raw[i], m.vec);
+  });
 }
 
 // Commit.  Destination j never lies behind source j, and no destination j is the
@@ -336,19 +470,30 @@ static int kv_rows_call(bool append, const sv_kv_cache* cache, int B, const int3
   a.ldv = ldv;
   a.vec_k = aligned(k, 16) && ldk % 8 == 0;
   a.vec_v = aligned(v, 16) && ldv % 8 == 0;
-  const long long items = (long long)a.map.offs[B] * 2 * a.c.heads * (a.c.dim / 8);
-  const long long blocks = (items + KV_THREADS - 1) / KV_THREADS;
-  if (blocks > 0x7fffffffll) return fail(SV_EUNSUPPORTED, "too many values in one call");
+  const int sms = device_sm_count();
+  if (sms <= 0) return fail(SV_ECUDA, "no CUDA device");
+  const int rows = a.map.offs[B];
+  a.cols = 2 * a.c.heads * (a.c.dim / 8);
+  a.step = a.cols < KV_THREADS ? KV_THREADS / a.cols : 1;
+  const int threads = a.cols < KV_THREADS ? (a.step * a.cols + 31) / 32 * 32 : KV_THREADS;
+  const int wide = (a.cols + KV_THREADS - 1) / KV_THREADS;   // CTAs across a row
+  // Few rows: a chunk per thread, for parallelism.  Many: KV_AHEAD of them at once, for bytes in flight.
+  const bool many = (long long)rows * a.cols >= (long long)KV_AHEAD * KV_THREADS * sms;
+  a.tile = a.step * (many ? KV_AHEAD * KV_STEPS : 1);
+  a.tiles = (rows + a.tile - 1) / a.tile;
+  const int most = (sms * KV_CTAS + wide - 1) / wide;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(KV_THREADS), 0, static_cast<cudaStream_t>(stream), attr);
-  const int bits = a.c.bits;
-  cudaError_t e;
-  if (append)
-    e = bits == 16 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<16>, a)
-                   : (bits == 8 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<8>, a) : cudaLaunchKernelEx(&cfg, kv_append_kernel<4>, a));
-  else
-    e = bits == 16 ? cudaLaunchKernelEx(&cfg, kv_read_kernel<16>, a)
-                   : (bits == 8 ? cudaLaunchKernelEx(&cfg, kv_read_kernel<8>, a) : cudaLaunchKernelEx(&cfg, kv_read_kernel<4>, a));
+  cudaLaunchConfig_t cfg = pdl_config(dim3(a.tiles < most ? a.tiles : most, wide), dim3(threads), 0,
+                                      static_cast<cudaStream_t>(stream), attr);
+  using Kernel = void (*)(KvRows);
+  static constexpr Kernel kernels[2][3][2] = {
+      {{kv_read_kernel<4, 1>, kv_read_kernel<4, KV_AHEAD>},
+       {kv_read_kernel<8, 1>, kv_read_kernel<8, KV_AHEAD>},
+       {kv_read_kernel<16, 1>, kv_read_kernel<16, KV_AHEAD>}},
+      {{kv_append_kernel<4, 1>, kv_append_kernel<4, KV_AHEAD>},
+       {kv_append_kernel<8, 1>, kv_append_kernel<8, KV_AHEAD>},
+       {kv_append_kernel<16, 1>, kv_append_kernel<16, KV_AHEAD>}}};
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[append][a.c.bits == 4 ? 0 : (a.c.bits == 8 ? 1 : 2)][many], a);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, append ? "cache append launch" : "cache read launch");
 }
 

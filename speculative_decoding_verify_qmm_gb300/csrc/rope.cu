@@ -5,17 +5,22 @@
 //   x <- x / sqrt(mean(x^2) + eps) * w,   (x_i, x_j) <- (x_i cos a - x_j sin a, x_j cos a + x_i sin a)
 //
 // Bound by memory for prompts and by launch latency for a drafted block: each
-// q and k element is read once and written once.  A thread owns 8 adjacent
+// q and k element is read once and written once.  A lane owns 8 adjacent
 // elements of a head (one 16-byte access each way), a head is D / 8 adjacent
 // lanes of a warp (rounded up to a power of two), the mean is a shuffle tree,
 // and the rotation's partner chunk - rotary_dim / 2 elements away - comes from
-// another lane by shuffle, so a head's values never leave registers.  The
-// sines and cosines of a row are made once per CTA, in shared memory, while the
-// first loads are in flight.
+// another lane by shuffle, so a head's values never leave registers.
 //
-// Angles: position * inv_freq reaches 1e6 radians, where one fp32 ulp is 0.06
-// rad.  It is formed in fp64 in units of turns, its whole turns are dropped, and
-// the rest (at most half a turn, error 2^-25 turns) goes to sincospif.
+// A warp is on its own: it takes some heads of one row, makes the row's sines and
+// cosines while its first loads are in flight (each lane a few frequencies, handed
+// over through the warp's piece of shared memory) and holds those of its chunk in
+// registers over all its heads.  No barrier joins warps.
+//
+// Angles.  position * inv_freq reaches 1e6 radians, where one fp32 ulp is 0.06
+// rad, and fp64 is slow here.  In units of 2^-64 turns the product is one of integers,
+// and whole turns fall off at the top: 64 bits of inv_freq / 2 pi times the position,
+// mod 2^64, off by at most |position| * 2^-63 turns.  Its upper 32 bits, as a float
+// (2^-26 turns), go to sincospif.
 #include "sv_kv.cuh"
 
 namespace sv {
@@ -25,16 +30,20 @@ struct RopeParams {
   __nv_bfloat16* out[2];
   const __nv_bfloat16* w[2];
   int ld_in[2], ld_out[2], heads[2];
-  bool vec_in[2], vec_out[2];   // 16-byte accesses allowed
   int dim, half, lanes;         // half = rotary_dim / 2; lanes per head
-  bool norm, interleaved;
-  float eps;
+  int rows, split, batches[2];  // warps of a row; batches of AHEAD passes of 32 / lanes heads
+  float eps, mean;              // mean = 1 / dim
   const int32_t* positions;
   const float* inv_freq;
 };
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_AHEAD = 4;  // chunks a thread loads before it computes
+constexpr int ROPE_WARPS = 4;
+constexpr int ROPE_MAX_HALF = 128;
+constexpr int ROPE_AHEAD = 4;  // chunks a lane has in flight
+constexpr int ROPE_FILL = 64;  // warps per SM that a call asks for
+
+// Pairs that rotate together.
+enum RopePairs { ROPE_NONE, ROPE_HALVES, ROPE_ADJACENT };
 
 __device__ __forceinline__ uint4 load_chunk(const __nv_bfloat16* p, bool vec) {
   if (vec) return *reinterpret_cast<const uint4*>(p);
@@ -47,101 +56,144 @@ __device__ __forceinline__ uint4 load_chunk(const __nv_bfloat16* p, bool vec) {
   return r;
 }
 
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 s_cs[128];
+// 2^64 / 2 pi, to the unit: a turn's part that one radian is.
+constexpr unsigned long long TURN_PER_RADIAN = 2935890503282001226ull;
+
+// (cos, sin) of position * f.  f = m * 2^(e - 23) with a 24-bit m; from 2^24 on (and for
+// infinity and NaN) no phase is left in it and the result is NaN.
+__device__ __forceinline__ float2 rope_turn(int position, float f) {
+  const uint32_t u = __float_as_uint(f);
+  const int e = (int)((u >> 23) & 255) - 127, shift = 23 - e;
+  const uint64_t m = (u & 0x7fffff) | (e > -127 ? 0x800000u : 0u);
+  const uint64_t lo = m * TURN_PER_RADIAN, hi = __umul64hi(m, TURN_PER_RADIAN);
+  uint64_t c = 0;               // the 128-bit product, shifted right by 0 to 150
+  if (shift <= 0) c = lo;
+  else if (shift < 64) c = (lo >> shift) | (hi << (64 - shift));
+  else if (shift < 128) c = hi >> (shift - 64);
+  const uint64_t turns = (u >> 31 ? 0 - c : c) * (uint64_t)(int64_t)position;
+  float sn, cs;
+  sincospif((float)(int32_t)(turns >> 32) * (shift < 0 ? __int_as_float(0x7fffffff) : 4.656612873077393e-10f), &sn, &cs);
+  return make_float2(cs, sn);
+}
+
+// Batches are q's, then k's: none has heads of both, so one weight and one pair of pointers serve a batch.
+template <int PAIRS, bool NORM, bool VEC, int AHEAD>
+__global__ void __launch_bounds__(32 * ROPE_WARPS) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ __align__(16) float s_cos[ROPE_WARPS][ROPE_MAX_HALF], s_sin[ROPE_WARPS][ROPE_MAX_HALF];
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const int L = p.lanes, j = tid & (L - 1);              // chunk of the head
-  const int per = ROPE_THREADS / L, slots = per * gridDim.y;
-  const int total = p.heads[0] + p.heads[1];
-  const bool live = j * 8 < p.dim;
-  // every thread of the CTA makes the same number of passes (the shuffles are warp-wide)
-  for (int base = blockIdx.y * per; base < total; base += slots * ROPE_AHEAD) {
-    uint4 raw[ROPE_AHEAD];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int task = blockIdx.x * ROPE_WARPS + warp;
+  const int row = (int)((uint32_t)task / (uint32_t)p.split), part = task - row * p.split;
+  if (row >= p.rows) return;    // whole warps: what follows is warp-wide
+  const int L = p.lanes, j = lane & (L - 1), per = 32 / L;  // j: chunk of the head
+  const int batches = p.batches[0] + p.batches[1];
+  const int first = (int)((uint32_t)(part * batches) / (uint32_t)p.split);
+  const int end = (int)((uint32_t)((part + 1) * batches) / (uint32_t)p.split);
+  const bool in_head = j * 8 < p.dim;
+  const int hc = p.half / 8;
+  const bool low = j < hc, turned = j * 8 < 2 * p.half;
+  float c[8], s[8];             // of this lane's chunk; adjacent pairs use 4
+  float w[8];
+  for (int batch = first; batch < end; ++batch) {
+    const int t = batch >= p.batches[0], heads = p.heads[t];
+    const int h0 = (batch - (t ? p.batches[0] : 0)) * AHEAD * per + lane / L;
+    const __nv_bfloat16* src = p.in[t] + (size_t)row * p.ld_in[t] + h0 * p.dim + j * 8;
+    __nv_bfloat16* dst = p.out[t] + (size_t)row * p.ld_out[t] + h0 * p.dim + j * 8;
+    const int hop = per * p.dim;
+    uint4 raw[AHEAD];
 #pragma unroll
-    for (int i = 0; i < ROPE_AHEAD; ++i) {
-      const int h = base + i * slots + tid / L;
+    for (int i = 0; i < AHEAD; ++i) {
       raw[i] = make_uint4(0, 0, 0, 0);
-      if (live && h < total) {
-        const int t = h >= p.heads[0], hh = t ? h - p.heads[0] : h;
-        raw[i] = load_chunk(p.in[t] + (size_t)row * p.ld_in[t] + hh * p.dim + j * 8, p.vec_in[t]);
+      if (in_head && h0 + i * per < heads) raw[i] = load_chunk(src + i * hop, VEC);
+    }
+    if (NORM && (batch == first || batch == p.batches[0])) {
+      uint4 w4 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // ones
+      if (p.w[t] && in_head) w4 = load_chunk(p.w[t] + j * 8, VEC);
+      const uint32_t u[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+    }
+    if (PAIRS != ROPE_NONE && batch == first) {
+      const int position = p.positions[row];
+      for (int f = lane; f < p.half; f += 64) {  // two at a time: their latencies overlap
+        const int g = f + 32 < p.half ? f + 32 : f;
+        const float ff = p.inv_freq[f], fg = p.inv_freq[g];
+        const float2 cf = rope_turn(position, ff), cg = rope_turn(position, fg);
+        s_cos[warp][f] = cf.x;
+        s_sin[warp][f] = cf.y;
+        s_cos[warp][g] = cg.x;
+        s_sin[warp][g] = cg.y;
+      }
+      __syncwarp();
+      // adjacent: chunk j holds pairs 4j..; halves: chunk j of either half the frequencies 8j..
+      const int f0 = !turned ? 0 : (PAIRS == ROPE_ADJACENT ? 4 * j : 8 * (low ? j : j - hc));
+      const float sign = PAIRS == ROPE_HALVES && low ? -1.f : 1.f;
+#pragma unroll
+      for (int e = 0; e < (PAIRS == ROPE_ADJACENT ? 4 : 8); e += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(&s_cos[warp][f0 + e]);
+        const float4 b = *reinterpret_cast<const float4*>(&s_sin[warp][f0 + e]);
+        c[e] = a.x, c[e + 1] = a.y, c[e + 2] = a.z, c[e + 3] = a.w;
+        s[e] = sign * b.x, s[e + 1] = sign * b.y, s[e + 2] = sign * b.z, s[e + 3] = sign * b.w;
       }
     }
-    if (base == blockIdx.y * per) {
-      for (int f = tid; f < p.half; f += ROPE_THREADS) {
-        const double turns = (double)p.positions[row] * (double)p.inv_freq[f] * 0.15915494309189533577;
-        float sn, cs;
-        sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
-        s_cs[f] = make_float2(cs, sn);
+    float x[AHEAD][8], ss[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      ss[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[i][e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+        if (NORM) ss[i] = fmaf(x[i][e], x[i][e], ss[i]);
       }
-      __syncthreads();
+    }
+    if (NORM) {
+      for (int off = L / 2; off; off >>= 1) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], off);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float r = rsqrtf(fmaf(ss[i], p.mean, p.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * r * w[e];
+      }
+    }
+    if (PAIRS == ROPE_ADJACENT) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = x[i][2 * e], b = x[i][2 * e + 1];
+          x[i][2 * e] = turned ? a * c[e] - b * s[e] : a;
+          x[i][2 * e + 1] = turned ? b * c[e] + a * s[e] : b;
+        }
+      }
+    }
+    if (PAIRS == ROPE_HALVES) {
+      const int from = (lane & ~(L - 1)) + (low ? j + hc : (turned ? j - hc : j));
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, x[i][e], from);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = turned ? x[i][e] * c[e] + o[e] * s[e] : x[i][e];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < ROPE_AHEAD; ++i) {
-      if (base + i * slots >= total) break;              // uniform over the CTA
-      const int h = base + i * slots + tid / L;
-      const int t = h >= p.heads[0], hh = t ? h - p.heads[0] : h;
-      float x[8];
-      const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&raw[i]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __bfloat1622float2(r2[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-      }
-      if (p.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-        for (int off = L / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        const float r = rsqrtf(ss / (float)p.dim + p.eps);
-        const __nv_bfloat16* w = p.w[t];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= r;
-          if (w && live) x[e] *= __bfloat162float(w[j * 8 + e]);
-        }
-      }
-      if (p.half) {
-        if (p.interleaved) {
-          if (j * 8 < 2 * p.half) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 cs = s_cs[4 * j + e];
-              const float a = x[2 * e], b = x[2 * e + 1];
-              x[2 * e] = a * cs.x - b * cs.y;
-              x[2 * e + 1] = b * cs.x + a * cs.y;
-            }
-          }
-        } else {
-          const int hc = p.half / 8;                     // chunks of half the rotated part
-          const bool low = j < hc, turned = j < 2 * hc;
-          const int from = (tid & 31 & ~(L - 1)) + (low ? j + hc : (turned ? j - hc : j));
-          float o[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, x[e], from);
-          if (turned) {
-            const int f0 = 8 * (low ? j : j - hc);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 cs = s_cs[f0 + e];
-              x[e] = low ? x[e] * cs.x - o[e] * cs.y : x[e] * cs.x + o[e] * cs.y;
-            }
-          }
-        }
-      }
-      if (live && h < total) {
-        __nv_bfloat16* dst = p.out[t] + (size_t)row * p.ld_out[t] + hh * p.dim + j * 8;
-        if (p.vec_out[t]) {
+    for (int i = 0; i < AHEAD; ++i) {
+      if (in_head && h0 + i * per < heads) {
+        if (VEC) {
           uint4 o4;
           __nv_bfloat162* o2 = reinterpret_cast<__nv_bfloat162*>(&o4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o2[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-          *reinterpret_cast<uint4*>(dst) = o4;
+          for (int e = 0; e < 4; ++e) o2[e] = __floats2bfloat162_rn(x[i][2 * e], x[i][2 * e + 1]);
+          *reinterpret_cast<uint4*>(dst + i * hop) = o4;
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = __float2bfloat16_rn(x[e]);
+          for (int e = 0; e < 8; ++e) dst[i * hop + e] = __float2bfloat16_rn(x[i][e]);
         }
       }
     }
@@ -181,6 +233,7 @@ extern "C" int sv_qk_norm_rope(const uint16_t* q, int ldq, const uint16_t* k, in
   uint16_t* out[2] = {q_out, k_out};
   const uint16_t* w[2] = {q_weight, k_weight};
   const int li[2] = {ldq, ldk}, lo[2] = {ldqo, ldko}, hs[2] = {n_q_heads, n_kv_heads};
+  bool vec = true;              // 16-byte accesses allowed
   for (int t = 0; t < 2; ++t) {
     p.in[t] = reinterpret_cast<const __nv_bfloat16*>(in[t]);
     p.out[t] = reinterpret_cast<__nv_bfloat16*>(out[t]);
@@ -188,26 +241,40 @@ extern "C" int sv_qk_norm_rope(const uint16_t* q, int ldq, const uint16_t* k, in
     p.ld_in[t] = li[t];
     p.ld_out[t] = lo[t];
     p.heads[t] = hs[t];
-    p.vec_in[t] = aligned(in[t], 16) && li[t] % 8 == 0;
-    p.vec_out[t] = aligned(out[t], 16) && lo[t] % 8 == 0;
+    if (hs[t])
+      vec = vec && aligned(in[t], 16) && aligned(out[t], 16) && (!w[t] || aligned(w[t], 16)) && li[t] % 8 == 0 && lo[t] % 8 == 0;
   }
   p.dim = head_dim;
   p.half = rotary_dim / 2;
   p.lanes = 1;
   while (p.lanes * 8 < head_dim) p.lanes *= 2;
-  p.norm = norm != 0;
-  p.interleaved = interleaved != 0;
   p.eps = eps;
   p.positions = positions;
   p.inv_freq = inv_freq;
-  // Few rows: one pass of heads per CTA, for parallelism.  Many: one CTA a row, so
-  // that a row's sines and cosines (fp64, slow here) are made once.
-  const int per = ROPE_THREADS / p.lanes, passes = (n_q_heads + n_kv_heads + per - 1) / per;
+  p.rows = rows;
+  p.mean = 1.f / (float)head_dim;
   const int sms = device_sm_count();
   if (sms <= 0) return fail(SV_ECUDA, "no CUDA device");
-  const int split = rows >= 2 * sms ? 1 : passes;
+  // Few rows: one pass per warp, for parallelism.  Many: ROPE_AHEAD of them at once, for bytes in flight.
+  const int per = 32 / p.lanes, passes[2] = {(n_q_heads + per - 1) / per, (n_kv_heads + per - 1) / per};
+  const bool many = vec && passes[0] >= ROPE_AHEAD && (long long)rows * (passes[0] + passes[1]) >= ROPE_FILL * ROPE_AHEAD * sms;
+  const int ahead = many ? ROPE_AHEAD : 1;
+  for (int t = 0; t < 2; ++t) p.batches[t] = (passes[t] + ahead - 1) / ahead;
+  // Warps of a row: as many as give each SM ROPE_FILL of them, at most one a batch.
+  p.split = (ROPE_FILL * sms + rows - 1) / rows;
+  if (p.split > p.batches[0] + p.batches[1]) p.split = p.batches[0] + p.batches[1];
+  const long long tasks = (long long)rows * p.split;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3(rows, split), dim3(ROPE_THREADS), 0, static_cast<cudaStream_t>(stream), attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel, p);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((tasks + ROPE_WARPS - 1) / ROPE_WARPS)), dim3(32 * ROPE_WARPS), 0,
+                                      static_cast<cudaStream_t>(stream), attr);
+  using Kernel = void (*)(RopeParams);
+#define SV_ROPE(PAIRS, NORM) \
+  {rope_kernel<PAIRS, NORM, false, 1>, rope_kernel<PAIRS, NORM, true, 1>, rope_kernel<PAIRS, NORM, true, ROPE_AHEAD>}
+  static constexpr Kernel kernels[3][2][3] = {{SV_ROPE(ROPE_NONE, false), SV_ROPE(ROPE_NONE, true)},
+                                              {SV_ROPE(ROPE_HALVES, false), SV_ROPE(ROPE_HALVES, true)},
+                                              {SV_ROPE(ROPE_ADJACENT, false), SV_ROPE(ROPE_ADJACENT, true)}};
+#undef SV_ROPE
+  const int pairs = !rotary_dim ? ROPE_NONE : (interleaved ? ROPE_ADJACENT : ROPE_HALVES);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[pairs][norm != 0][many ? 2 : vec], p);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "norm and rotation launch");
 }
