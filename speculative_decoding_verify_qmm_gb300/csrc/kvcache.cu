@@ -21,7 +21,8 @@ constexpr float KV_FAR = 65280.f;  // bf16; with it scale * code + bias <= 65344
 constexpr int KV_THREADS = 256;    // at most
 constexpr int KV_AHEAD = 4;        // chunks a thread has in flight when rows are many
 constexpr int KV_STEPS = 2;        // times that many rows of a thread per tile
-constexpr int KV_CTAS = 5;         // CTAs per SM of a long call
+constexpr int KV_APPEND_CTAS = 4;  // CTAs per SM of a long call: what is resident at once
+constexpr int KV_READ_CTAS = 4;
 
 struct KvRows {
   KvCache c;
@@ -104,8 +105,9 @@ __device__ __forceinline__ __half* kv_side(__half* base, long long bytes) {
 }
 
 // The loop both kernels share.  work(rows, look) handles AHEAD rows at once: it calls look(offsets) for
-// their byte offsets - after it has asked for the caller's rows, where it reads those - and the first look of a
-// tile also looks the CTA's next tile up.  All threads of a CTA make the same steps: work may shuffle.
+// their byte offsets - after it has asked for the caller's rows, where it reads those - and ahead() once its
+// loads are on their way: the CTA's next tile is looked up meanwhile.  All threads of a CTA make the same steps:
+// work may shuffle.
 template <int BITS, int AHEAD, typename Work>
 __device__ __forceinline__ void kv_tiles(const KvRows& a, const KvColumn& m, Work work) {
   __shared__ long long s_at[2][KV_THREADS];
@@ -126,11 +128,11 @@ __device__ __forceinline__ void kv_tiles(const KvRows& a, const KvColumn& m, Wor
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) at[i] = m.live && r[i] < n ? s_at[buf][r[i]] : -1;
-      });
-      if (r0 == 0) {
+      }, [&] {
         const int next = (t + (int)gridDim.x) * a.tile + tid;
-        if (tid < a.tile && t + (int)gridDim.x < a.tiles && next < rows) s_at[buf ^ 1][tid] = kv_row_bytes<BITS>(a, next);
-      }
+        if (r0 == 0 && tid < a.tile && t + (int)gridDim.x < a.tiles && next < rows)
+          s_at[buf ^ 1][tid] = kv_row_bytes<BITS>(a, next);
+      });
     }
     __syncthreads();
   }
@@ -143,12 +145,12 @@ __device__ __forceinline__ float chunk_value(const uint4& r, int e) {
 }
 
 template <int BITS, int AHEAD>
-__global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const __grid_constant__ KvRows a) {
+__global__ void __launch_bounds__(KV_THREADS, KV_APPEND_CTAS) kv_append_kernel(const __grid_constant__ KvRows a) {
   pdl_trigger();
   pdl_wait();
   const KvColumn m = kv_column<BITS>(a);
   const int lane = threadIdx.x & 31;
-  kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int n, auto look) {
+  kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int n, auto look, auto ahead) {
     uint4 raw[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
@@ -157,6 +159,7 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const __grid_cons
     }
     long long at[AHEAD];
     look(at);
+    ahead();
     if constexpr (BITS == 16) {
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i)
@@ -194,28 +197,28 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const __grid_cons
       // The format's own roundings, each IEEE: a host or torch program gets the same codes.
       const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), (float)TOP)), b16 = __float2half_rn(lo);
       const float s_mine = __half2float(s16);
-      // A code is rint((x - b) / s) clamped to [0, TOP], the difference and the quotient each rounded.  Here
-      // the quotient comes from a product with 1 / (s * TOP), off by less than TOP * (2^-23 + 2^-24) < 5e-5:
-      // where it lies further than that from a half, rint is the same, and the few threads with a closer
-      // one divide.  The saturation is the clamp: x beyond KV_FAR gives an end of the range, as lo and hi are
-      // clamped to it.  A group without a range, or with a NaN, has codes 0.
-      const float inv_mine = s_mine > 0.f && !nan ? __fdiv_rn(1.f, s_mine * (float)TOP) : 0.f;
+      // A code is rint((x - b) / s) clamped to [0, TOP], the difference y and the quotient each rounded.  Ties
+      // are common (bf16 values over an 11-bit scale), so the quotient must be the rounded one: by Markstein's
+      // theorem (IBM J. Res. Dev. 34, 1990) t = y * inv, t + inv * (y - s * t) with two fused steps is that, for inv
+      // = 1 / s rounded and s not all ones.  y is clamped rather than the code, which is the same as both
+      // steps are monotonic, and lets infinities through.  A group without a range, or with a NaN, has codes 0.
+      const float inv_mine = s_mine > 0.f && !nan ? __fdiv_rn(1.f, s_mine) : 0.f;
       const uint32_t side_mine = nan ? 0x7fff7fffu : __half_as_ushort(s16) | ((uint32_t)__half_as_ushort(b16) << 16);
       constexpr float MAGIC = 8388608.f;  // 2^23: its sum with a small value rounds that to an integer, in the low bits
       uint32_t word[AHEAD][BITS / 4], side[AHEAD];
-      float far = 0.f;
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         const float inv = AHEAD == 1 ? inv_mine : __shfl_sync(0xffffffffu, inv_mine, (lane & 24) + i);
         side[i] = AHEAD == 1 ? side_mine : __shfl_sync(0xffffffffu, side_mine, (lane & 24) + i);
+        const float s = inv > 0.f ? __half2float(__ushort_as_half((unsigned short)side[i])) : 0.f;
         const float b = __half2float(__ushort_as_half((unsigned short)(side[i] >> 16)));
+        const float most = s * (float)TOP;  // exact: 11 bits times 8
         uint32_t q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float unit = __saturatef(__fsub_rn(chunk_value(raw[i], e), b) * inv);
-          const float sum = fmaf(unit, (float)TOP, MAGIC);
-          q[e] = __float_as_uint(sum);
-          far = fmaxf(far, fabsf(fmaf(unit, (float)TOP, MAGIC - sum)));
+          const float y = fminf(fmaxf(__fsub_rn(chunk_value(raw[i], e), b), 0.f), most);
+          const float t = __fmul_rn(y, inv);
+          q[e] = __float_as_uint(__fadd_rn(fmaf(inv, fmaf(-s, t, y), t), MAGIC));
         }
         if constexpr (BITS == 8) {
 #pragma unroll
@@ -224,21 +227,6 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const __grid_cons
         } else {  // the low 16 bits of each sum: MAGIC's own bits lie above them
           const uint32_t u = q[0] + 16u * q[1] + 256u * q[2] + 4096u * q[3], v = q[4] + 16u * q[5] + 256u * q[6] + 4096u * q[7];
           word[i][0] = __byte_perm(u, v, 0x5410);
-        }
-      }
-      if (far > 0.49995f) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          const float s = __half2float(__ushort_as_half((unsigned short)side[i]));
-          const float b = __half2float(__ushort_as_half((unsigned short)(side[i] >> 16)));
-          if (!(s > 0.f)) continue;  // no range, or NaN
-#pragma unroll
-          for (int e = 0; e < BITS / 4; ++e) word[i][e] = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float c = rintf(__fdiv_rn(__fsub_rn(chunk_value(raw[i], e), b), s));
-            word[i][e * BITS / 32] |= (uint32_t)fminf(fmaxf(c, 0.f), (float)TOP) << (e * BITS % 32);
-          }
         }
       }
 #pragma unroll
@@ -256,11 +244,11 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const __grid_cons
 }
 
 template <int BITS, int AHEAD>
-__global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const __grid_constant__ KvRows a) {
+__global__ void __launch_bounds__(KV_THREADS, KV_READ_CTAS) kv_read_kernel(const __grid_constant__ KvRows a) {
   pdl_trigger();
   pdl_wait();
   const KvColumn m = kv_column<BITS>(a);
-  kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int, auto look) {
+  kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int, auto look, auto ahead) {
     long long at[AHEAD];
     look(at);
     uint4 raw[AHEAD];             // bf16, or codes in x (and y)
@@ -282,6 +270,7 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const __grid_consta
         bias[i] = *kv_side<BITS>(m.bias, at[i]);
       }
     }
+    ahead();
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if constexpr (BITS != 16) {
@@ -481,7 +470,7 @@ static int kv_rows_call(bool append, const sv_kv_cache* cache, int B, const int3
   const bool many = (long long)rows * a.cols >= (long long)KV_AHEAD * KV_THREADS * sms;
   a.tile = a.step * (many ? KV_AHEAD * KV_STEPS : 1);
   a.tiles = (rows + a.tile - 1) / a.tile;
-  const int most = (sms * KV_CTAS + wide - 1) / wide;
+  const int most = (sms * (append ? KV_APPEND_CTAS : KV_READ_CTAS) + wide - 1) / wide;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pdl_config(dim3(a.tiles < most ? a.tiles : most, wide), dim3(threads), 0,
                                       static_cast<cudaStream_t>(stream), attr);

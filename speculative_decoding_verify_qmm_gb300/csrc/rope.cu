@@ -38,9 +38,10 @@ struct RopeParams {
 };
 
 constexpr int ROPE_WARPS = 4;
+constexpr int ROPE_CTAS = 8;   // per SM: 64 registers a thread
 constexpr int ROPE_MAX_HALF = 128;
 constexpr int ROPE_AHEAD = 4;  // chunks a lane has in flight
-constexpr int ROPE_FILL = 64;  // warps per SM that a call asks for
+constexpr int ROPE_FILL = 32;  // warps per SM that a call asks for
 
 // Pairs that rotate together.
 enum RopePairs { ROPE_NONE, ROPE_HALVES, ROPE_ADJACENT };
@@ -78,7 +79,7 @@ __device__ __forceinline__ float2 rope_turn(int position, float f) {
 
 // Batches are q's, then k's: none has heads of both, so one weight and one pair of pointers serve a batch.
 template <int PAIRS, bool NORM, bool VEC, int AHEAD>
-__global__ void __launch_bounds__(32 * ROPE_WARPS) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * ROPE_WARPS, ROPE_CTAS) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(16) float s_cos[ROPE_WARPS][ROPE_MAX_HALF], s_sin[ROPE_WARPS][ROPE_MAX_HALF];
   pdl_trigger();
   pdl_wait();
