@@ -15,6 +15,8 @@
 // lookup by every thread is three dependent loads against one load of data.
 #include "sv_kv.cuh"
 
+#include <type_traits>
+
 namespace sv {
 
 constexpr float KV_FAR = 65280.f;  // bf16; with it scale * code + bias <= 65344 stays finite in fp16
@@ -153,9 +155,15 @@ __global__ void __launch_bounds__(KV_THREADS, KV_APPEND_CTAS) kv_append_kernel(c
   kv_tiles<BITS, AHEAD>(a, m, [&](int base, const int (&r)[AHEAD], int n, auto look, auto ahead) {
     uint4 raw[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (m.live && r[i] < n) raw[i] = load8(m.rows + (size_t)(base + r[i]) * m.ld, m.vec);
+    for (int i = 0; i < AHEAD; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    if (m.vec) {  // one branch, so that the loads leave together
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (m.live && r[i] < n) raw[i] = load8(m.rows + (size_t)(base + r[i]) * m.ld, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (m.live && r[i] < n) raw[i] = load8(m.rows + (size_t)(base + r[i]) * m.ld, false);
     }
     long long at[AHEAD];
     look(at);
@@ -200,44 +208,57 @@ __global__ void __launch_bounds__(KV_THREADS, KV_APPEND_CTAS) kv_append_kernel(c
       // A code is rint((x - b) / s) clamped to [0, TOP], the difference y and the quotient each rounded.  Ties
       // are common (bf16 values over an 11-bit scale), so the quotient must be the rounded one: by Markstein's
       // theorem (IBM J. Res. Dev. 34, 1990) t = y * inv, t + inv * (y - s * t) with two fused steps is that, for inv
-      // = 1 / s rounded and s not all ones.  y is clamped rather than the code, which is the same as both
-      // steps are monotonic, and lets infinities through.  A group without a range, or with a NaN, has codes 0.
-      const float inv_mine = s_mine > 0.f && !nan ? __fdiv_rn(1.f, s_mine) : 0.f;
+      // = 1 / s rounded and s not all ones.  A group without a range, or with a NaN, has codes 0.
+      const bool flat = !(s_mine > 0.f) || nan;
+      const float inv_mine = flat ? 0.f : __fdiv_rn(1.f, s_mine);
       const uint32_t side_mine = nan ? 0x7fff7fffu : __half_as_ushort(s16) | ((uint32_t)__half_as_ushort(b16) << 16);
-      constexpr float MAGIC = 8388608.f;  // 2^23: its sum with a small value rounds that to an integer, in the low bits
-      uint32_t word[AHEAD][BITS / 4], side[AHEAD];
+      // Without the clamp no code leaves [0, TOP] if every value is within KV_FAR and s is a normal number: s is off by
+      // 2^-11 of itself, b by at most 2^-25.
+      const bool odd = nan || top > KV_FAR || bottom < -KV_FAR || (s_mine > 0.f && s_mine < 6.103515625e-5f);
+      const bool clamped = __any_sync(0xffffffffu, odd);
+      constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: its sum with a small value rounds that to an integer, in the low bits
+      uint32_t word[AHEAD][BITS / 4];
+      auto codes = [&](auto clamp) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const float inv = AHEAD == 1 ? inv_mine : __shfl_sync(0xffffffffu, inv_mine, (lane & 24) + i);
-        side[i] = AHEAD == 1 ? side_mine : __shfl_sync(0xffffffffu, side_mine, (lane & 24) + i);
-        const float s = inv > 0.f ? __half2float(__ushort_as_half((unsigned short)side[i])) : 0.f;
-        const float b = __half2float(__ushort_as_half((unsigned short)(side[i] >> 16)));
-        const float most = s * (float)TOP;  // exact: 11 bits times 8
-        uint32_t q[8];
+        for (int i = 0; i < AHEAD; ++i) {
+          const float inv = AHEAD == 1 ? inv_mine : __shfl_sync(0xffffffffu, inv_mine, (lane & 24) + i);
+          const uint32_t side = AHEAD == 1 ? side_mine : __shfl_sync(0xffffffffu, side_mine, (lane & 24) + i);
+          const float s = inv > 0.f ? __half2float(__ushort_as_half((unsigned short)side)) : 0.f;
+          const float b = __half2float(__ushort_as_half((unsigned short)(side >> 16)));
+          uint32_t q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = fminf(fmaxf(__fsub_rn(chunk_value(raw[i], e), b), 0.f), most);
-          const float t = __fmul_rn(y, inv);
-          q[e] = __float_as_uint(__fadd_rn(fmaf(inv, fmaf(-s, t, y), t), MAGIC));
+          for (int e = 0; e < 8; ++e) {
+            float y = __fsub_rn(chunk_value(raw[i], e), b);
+            // y instead of the code: both steps after it are monotonic.  s * TOP is exact (11 bits times 8)
+            if constexpr (decltype(clamp)::value) y = fminf(fmaxf(y, 0.f), s * (float)TOP);
+            const float t = __fmul_rn(y, inv);
+            q[e] = __float_as_uint(__fadd_rn(fmaf(inv, fmaf(-s, t, y), t), MAGIC));
+          }
+          if constexpr (BITS == 8) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              word[i][e] = __byte_perm(__byte_perm(q[4 * e], q[4 * e + 1], 0x0040), __byte_perm(q[4 * e + 2], q[4 * e + 3], 0x0040), 0x5410);
+          } else {  // the low 16 bits of each sum: MAGIC's own bits lie above them
+            const uint32_t u = q[0] + 16u * q[1] + 256u * q[2] + 4096u * q[3], v = q[4] + 16u * q[5] + 256u * q[6] + 4096u * q[7];
+            word[i][0] = __byte_perm(u, v, 0x5410);
+          }
         }
-        if constexpr (BITS == 8) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            word[i][e] = __byte_perm(__byte_perm(q[4 * e], q[4 * e + 1], 0x0040), __byte_perm(q[4 * e + 2], q[4 * e + 3], 0x0040), 0x5410);
-        } else {  // the low 16 bits of each sum: MAGIC's own bits lie above them
-          const uint32_t u = q[0] + 16u * q[1] + 256u * q[2] + 4096u * q[3], v = q[4] + 16u * q[5] + 256u * q[6] + 4096u * q[7];
-          word[i][0] = __byte_perm(u, v, 0x5410);
-        }
-      }
+      };
+      if (clamped) codes(std::true_type{});
+      else codes(std::false_type{});
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         if (at[i] < 0) continue;
         if constexpr (BITS == 8) *reinterpret_cast<uint2*>(m.data + at[i]) = make_uint2(word[i][0], word[i][1]);
         else *reinterpret_cast<uint32_t*>(m.data + at[i]) = word[i][0];
-        if ((m.chunk & 7) == 0) {
-          *kv_side<BITS>(m.scale, at[i]) = __ushort_as_half((unsigned short)side[i]);
-          *kv_side<BITS>(m.bias, at[i]) = __ushort_as_half((unsigned short)(side[i] >> 16));
-        }
+      }
+      // each of a group's first AHEAD lanes has the scale and bias of one row
+      const int own = lane & 7;
+      long long mine_at = at[0];
+      if constexpr (AHEAD == 4) mine_at = own & 2 ? (own & 1 ? at[3] : at[2]) : (own & 1 ? at[1] : at[0]);
+      if (own < AHEAD && mine_at >= 0) {
+        *kv_side<BITS>(m.scale, mine_at) = __ushort_as_half((unsigned short)side_mine);
+        *kv_side<BITS>(m.bias, mine_at) = __ushort_as_half((unsigned short)(side_mine >> 16));
       }
     }
   });
@@ -292,9 +313,15 @@ __global__ void __launch_bounds__(KV_THREADS, KV_READ_CTAS) kv_read_kernel(const
         raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+    if (m.vec) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (at[i] >= 0) store8(m.rows + (size_t)(base + r[i]) * m.ld, raw[i], m.vec);
+      for (int i = 0; i < AHEAD; ++i)
+        if (at[i] >= 0) store8(m.rows + (size_t)(base + r[i]) * m.ld, raw[i], true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (at[i] >= 0) store8(m.rows + (size_t)(base + r[i]) * m.ld, raw[i], false);
+    }
   });
 }
 
