@@ -204,19 +204,23 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   p.partial = static_cast<float*>(workspace);
   p.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + partial);
   int rows = 0;                // of the widest request, times the group
+  long long by16 = 0, by32 = 0;
   for (int b = 0; b < B; ++b) {
     const int m = p.map.offs[b + 1] - p.map.offs[b];
     if ((long long)m > ((long long)table_pages << p.c.page_shift))
       return fail(SV_EINVAL, "request %d has more rows than block_table has places", b);
     if (m * p.group > rows) rows = m * p.group;
+    by16 += 4 * ta_blocks(m * p.group, 16);
+    by32 += m ? (m * p.group > 16 ? 7 : 5) : 0;
   }
   const bool narrow = rows <= TA_NARROW_ROWS;
-  p.block = narrow ? (rows <= 16 ? 16 : 32) : TA_MAX_BLOCK;
-  // Measured (in fifths of the time that a narrow unit with one row tile takes): a second row tile adds two, beginning an
-  // item costs some 7 us against 1.2 a unit in the narrow kernel, 10 against 1.6 in the wide one.
-  p.many = narrow ? 16 : 64;
+  // In fifths of the time of a narrow unit of 32-row blocks with one row tile filled: two tiles filled take 7, a block of 16
+  // rows takes 4.  (One request of 32 rows over 16384 tokens: 22.7 us in a block of 32, 25.4 in two of 16; 48 requests of 4 to 20
+  // rows: 192.6 in blocks of 32, 165.5 in blocks of 16.)
+  p.block = narrow ? (by16 < by32 ? 16 : 32) : TA_MAX_BLOCK;
+  // Beginning an item costs some 7 us against 1.2 a unit in the narrow kernel, 10 against 1.6 in the wide one.
   p.cost[0] = 5;
-  p.cost[1] = narrow ? 7 : 5;
+  p.cost[1] = p.block == 32 ? 7 : 5;
   p.begin_cost = narrow ? 25 : 30;
   // the lengths are on the device: size the grid for the longest the table allows
   const long long most_units = (((long long)table_pages << p.c.page_shift) + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;

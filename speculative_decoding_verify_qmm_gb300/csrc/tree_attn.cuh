@@ -30,7 +30,7 @@ struct TreeAttnParams {
   float* stats;              // [2 * grid][2][block]: their maximum (as an exponent of 2) and weight
   int grid;
   int block;                 // rows (drafted row x query head of the group) per item
-  int cost[2], many;         // of a unit with up to `many` rows, and with more
+  int cost[2];               // of a unit with up to 16 rows, and with more
   int begin_cost;            // of beginning an item
 };
 
@@ -43,7 +43,7 @@ struct TaPlan {
 
 __host__ __device__ __forceinline__ int ta_blocks(int rows, int block) { return (rows + block - 1) / block; }
 
-__device__ __forceinline__ int ta_cost(const TreeAttnParams& p, int m) { return p.cost[m * p.group > p.many]; }
+__device__ __forceinline__ int ta_cost(const TreeAttnParams& p, int m) { return p.cost[m * p.group > 16]; }
 
 // By one warp.
 __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool report) {
