@@ -303,7 +303,8 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  *   a = positions[row] * inv_freq[p],  p = 0 .. rotary_dim/2 - 1,
  * with the pair (i, j) = (p, p + rotary_dim/2), or (2p, 2p + 1) when
  * interleaved != 0; elements from rotary_dim on are not rotated.  The angle is
- * formed in fp64 and reduced to one turn before its sine and cosine, the rest
+ * formed exactly to 2^-32 turns and reduced to one turn before its sine and
+ * cosine, for any position and |inv_freq| < 2^24 (NaN from there on); the rest
  * is fp32, and each output is rounded to bf16 once.  positions int32 [rows],
  * inv_freq fp32 [rotary_dim/2] (both may be NULL when rotary_dim == 0).
  * q_out may be q (same stride) and k_out may be k: each head is read whole
@@ -332,6 +333,7 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * the request concerned, sv_kv_read leaves their output rows as they were,
  * and sv_tree_attention's output for that request is undefined (no access
  * leaves the arrays).  Two requests may share pages that none of them writes.
+ * k and v are two arrays, not one.
  *
  * sv_kv_append writes row i of request b (k, v bf16 [rows, n_kv_heads*head_dim],
  * strides ldk, ldv) at position kv_len[b] + i.  Quantization of a group
@@ -365,8 +367,10 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * Softmax statistics and sums are fp32; the probabilities enter the second
  * product in 16 bits.  The result does not depend on timing: it is bitwise
  * reproducible for given inputs on one device.
+ * out may be q (same stride); other overlap is not allowed.
  * Workspace: sv_tree_attention_workspace_bytes (0 for a bad argument), 256-byte
- * aligned, no zero fill, free for other use once the call has run.
+ * aligned; it need not be zero, and what the call wrote is zero again after it,
+ * so it may be the one that other calls use (rules at the top).
  *
  * sv_kv_commit: after the accept step, request b keeps path_len[b] of its
  * drafted rows, namely rows path[b*max_path + j], j = 0 .. path_len[b] - 1,
@@ -374,7 +378,7 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * topological order; the anchor is row 0).  Moves what position kv_len[b] +
  * path[j] holds to position kv_len[b] + j, codes, scales and biases as they
  * are, in each of n_layers caches (a HOST array; same sizes and bits, n_layers
- * <= 1024) that share the block table.  path, path_len int32, DEVICE;
+ * <= 1024, no array in it twice) that share the block table.  path, path_len int32, DEVICE;
  * 1 <= max_path <= 64.  A path that is not increasing or out of range is bad
  * input (above). */
 typedef struct {

@@ -15,6 +15,8 @@
 // lookup by every thread is three dependent loads against one load of data.
 #include "sv_kv.cuh"
 
+#include <algorithm>
+#include <functional>
 #include <type_traits>
 
 namespace sv {
@@ -420,8 +422,8 @@ int check_cache(const sv_kv_cache* c, KvCache* out) {
     return fail(SV_EUNSUPPORTED, "page_size must be a power of two in [16, 65536] (got %d)", c->page_size);
   if (c->n_kv_heads < 1 || c->n_kv_heads > 256) return fail(SV_EINVAL, "n_kv_heads must be in [1, 256] (got %d)", c->n_kv_heads);
   if (c->n_pages < 1) return fail(SV_EINVAL, "n_pages must be >= 1 (got %d)", c->n_pages);
-  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
-    return fail(SV_EINVAL, "cache k and v must be non-null and 16-byte aligned");
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) || c->k == c->v)
+    return fail(SV_EINVAL, "cache k and v must be non-null, 16-byte aligned and not the same");
   if (c->bits != 16) {
     const void* s[4] = {c->k_scales, c->k_biases, c->v_scales, c->v_biases};
     for (const void* p : s)
@@ -546,6 +548,12 @@ int sv_kv_commit(const sv_kv_cache* layers, int n_layers, int B, const int32_t* 
               c.bits != p.c.bits))
       return fail(SV_EINVAL, "layer %d's cache differs in size or bits from layer 0's", l);
   }
+  // A cache listed twice would be moved twice at once.
+  const void* seen[2 * 1024];
+  for (int l = 0; l < n_layers; ++l) seen[2 * l] = layers[l].k, seen[2 * l + 1] = layers[l].v;
+  std::sort(seen, seen + 2 * n_layers, std::less<const void*>());
+  for (int i = 1; i < 2 * n_layers; ++i)
+    if (seen[i] == seen[i - 1]) return fail(SV_EINVAL, "the same cache memory is listed twice");
   const int st = check_table(p.c, kv_len, block_table, table_pages);
   if (st) return st;
   if (!path || !path_len || !aligned(path, 4) || !aligned(path_len, 4))

@@ -19,7 +19,7 @@
 // Angles.  position * inv_freq reaches 1e6 radians, where one fp32 ulp is 0.06
 // rad, and fp64 is slow here.  In units of 2^-64 turns the product is one of integers,
 // and whole turns fall off at the top: 64 bits of inv_freq / 2 pi times the position,
-// mod 2^64, off by at most |position| * 2^-63 turns.  Its upper 32 bits, as a float
+// mod 2^64, off by at most |position| * 2^-63 turns for any frequency.  Its upper 32 bits, as a float
 // (2^-26 turns), go to sincospif.
 #include "sv_kv.cuh"
 
@@ -57,8 +57,8 @@ __device__ __forceinline__ uint4 load_chunk(const __nv_bfloat16* p, bool vec) {
   return r;
 }
 
-// 2^64 / 2 pi, to the unit: a turn's part that one radian is.
-constexpr unsigned long long TURN_PER_RADIAN = 2935890503282001226ull;
+// 2^96 / 2 pi: the turns in a radian, its first 64 bits and the next 32.
+constexpr unsigned long long RADIAN_HIGH = 2935890503282001226ull, RADIAN_LOW = 2131351028ull;
 
 // (cos, sin) of position * f.  f = m * 2^(e - 23) with a 24-bit m; from 2^24 on (and for
 // infinity and NaN) no phase is left in it and the result is NaN.
@@ -66,8 +66,8 @@ __device__ __forceinline__ float2 rope_turn(int position, float f) {
   const uint32_t u = __float_as_uint(f);
   const int e = (int)((u >> 23) & 255) - 127, shift = 23 - e;
   const uint64_t m = (u & 0x7fffff) | (e > -127 ? 0x800000u : 0u);
-  const uint64_t lo = m * TURN_PER_RADIAN, hi = __umul64hi(m, TURN_PER_RADIAN);
-  uint64_t c = 0;               // the 128-bit product, shifted right by 0 to 150
+  const uint64_t main = m * RADIAN_HIGH, lo = main + (m * RADIAN_LOW >> 32), hi = __umul64hi(m, RADIAN_HIGH) + (lo < main);
+  uint64_t c = 0;               // the product hi:lo in units of 2^(e - 87) turns, shifted right to 2^-64 (by 0 to 150)
   if (shift <= 0) c = lo;
   else if (shift < 64) c = (lo >> shift) | (hi << (64 - shift));
   else if (shift < 128) c = hi >> (shift - 64);

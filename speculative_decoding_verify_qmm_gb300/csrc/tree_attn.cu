@@ -12,7 +12,8 @@ constexpr int TA_MAX_BLOCK = 128, TA_NARROW_ROWS = 32;
 
 // Joins the partial sums of items that spanned CTAs, in CTA order.  WPP warps per (row, query head) take every WPP-th part,
 // eight parts on their way at once, and meet in shared memory in warp order.  PAIRS such pairs a CTA at a time.  All that
-// does not read the parts is done before the wait for them.
+// does not read the parts is done before the wait for them.  A part is read once, and its place left at zero, as other calls
+// that use the same workspace expect.
 template <int D, int WPP, int PAIRS>
 __global__ void __launch_bounds__(32 * WPP * PAIRS) tree_attn_join_kernel(const __grid_constant__ TreeAttnParams p) {
   constexpr int E = D / 32;
@@ -52,16 +53,19 @@ __global__ void __launch_bounds__(32 * WPP * PAIRS) tree_attn_join_kernel(const 
     float acc[E] = {}, weight = 0.f, most = -INFINITY;
     for (int c8 = c0 + warp; c8 <= c1; c8 += 8 * WPP) {
       float x[8][E], st[8], wt[8];
+      int from[8];                                     // the part's slot; -1: none
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
         const int c = c8 + WPP * y;
         const long long lo = (long long)c * per;
+        from[y] = -1;
         st[y] = -INFINITY;
         wt[y] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) x[y][e] = 0.f;
         if (c <= c1 && (dense || ta_units_before(lo + per, a0, nt, cost, plan.begin) > ta_units_before(lo, a0, nt, cost, plan.begin))) {
           const size_t slot = 2 * (size_t)c + (a0 > lo ? 1 : 0);   // the CTA's first item if its share begins in it
+          from[y] = (int)slot;
           st[y] = p.stats[2 * slot * p.block + k];
           wt[y] = p.stats[(2 * slot + 1) * p.block + k];
           const float* src = p.partial + (slot * p.block + k) * D + lane * E;
@@ -73,6 +77,16 @@ __global__ void __launch_bounds__(32 * WPP * PAIRS) tree_attn_join_kernel(const 
             x[y][0] = v.x; x[y][1] = v.y;
           }
         }
+      }
+      __syncwarp();                                    // every lane has the statistics: what was read goes back to zero
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        if (from[y] < 0) continue;
+        const size_t at = (size_t)from[y];
+        float* src = p.partial + (at * p.block + k) * D + lane * E;
+        if constexpr (E == 4) *reinterpret_cast<float4*>(src) = make_float4(0.f, 0.f, 0.f, 0.f);
+        else *reinterpret_cast<float2*>(src) = make_float2(0.f, 0.f);
+        if (lane < 2) p.stats[(2 * at + lane) * p.block + k] = 0.f;
       }
       float top = most;
 #pragma unroll

@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
           o[m][n][2 * i] *= factor;
           o[m][n][2 * i + 1] *= factor;
         }
-        if (!whole && warp == 0 && q == 0) {
+        if (!whole && warp == 0 && q == 0 && k < s.rows) {
           p.stats[(2 * slot) * p.block + k] = most;
           p.stats[(2 * slot + 1) * p.block + k] = weight;
         }

@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       for (int g = 0; g < split; ++g) weight += s_sum[g * span + rr] * ta_exp2(s_max[g * span + rr] - base);
       const float own = ta_exp2(ref - base);
       const float factor = whole ? (weight == 0.f ? 0.f : own / weight) : own;
-      if (!whole && grp == 0) {
+      if (!whole && grp == 0 && rr < s.rows) {
         p.stats[(2 * slot) * p.block + rr] = most;
         p.stats[(2 * slot + 1) * p.block + rr] = weight;
       }

@@ -17,7 +17,7 @@ def raw():
 
 
 def _cache(**kw):
-    f = dict(k=256, v=256, k_scales=256, k_biases=256, v_scales=256, v_biases=256, n_pages=8, page_size=16,
+    f = dict(k=256, v=512, k_scales=256, k_biases=256, v_scales=256, v_biases=256, n_pages=8, page_size=16,
              n_kv_heads=2, head_dim=64, bits=8)
     f.update(kw)
     return binding.KVCacheView(*[f[n] for n, _ in binding.KVCacheView._fields_])
@@ -56,7 +56,7 @@ CACHE_BAD = [
     (dict(head_dim=0), SV_EUNSUPPORTED), (dict(head_dim=320), SV_EUNSUPPORTED), (dict(page_size=8), SV_EUNSUPPORTED),
     (dict(page_size=48), SV_EUNSUPPORTED), (dict(page_size=1 << 17), SV_EUNSUPPORTED), (dict(n_kv_heads=0), SV_EINVAL),
     (dict(n_kv_heads=257), SV_EINVAL), (dict(n_pages=0), SV_EINVAL), (dict(k=None), SV_EINVAL), (dict(v=None), SV_EINVAL),
-    (dict(k=264), SV_EINVAL), (dict(v_biases=None), SV_EINVAL), (dict(k_scales=258), SV_EINVAL)]
+    (dict(k=264), SV_EINVAL), (dict(v=256), SV_EINVAL), (dict(v_biases=None), SV_EINVAL), (dict(k_scales=258), SV_EINVAL)]
 
 
 def _append(raw, cache, B=1, offs=None, lens=16, table=16, pages=4, k=16, ldk=128, v=16, ldv=128, read=False):
@@ -102,6 +102,7 @@ def test_tree_attention_refuses(raw):
                         (dict(ws_bytes=0), SV_EINVAL)]:
         assert _attend(raw, ok, **bad) == status, bad
     assert _attend(raw, _cache(head_dim=192), ldq=1024, ldo=1024) == SV_EUNSUPPORTED
+    assert _attend(raw, ok, pages=1, offs=_offs(0, ok.page_size + 1)) == SV_EINVAL    # more rows than the table has places
     assert raw.sv_tree_attention_workspace_bytes(ctypes.byref(ok), 1, _offs(0, 65), 4) == 0
     assert raw.sv_tree_attention_workspace_bytes(None, 1, _offs(0, 1), 4) == 0
 
@@ -119,6 +120,8 @@ def test_commit_refuses(raw):
         assert call(**bad) == status, bad
     assert call((binding.KVCacheView * 2)(_cache(), _cache(n_pages=9)), n=2) == SV_EINVAL
     assert call((binding.KVCacheView * 2)(_cache(), _cache(bits=4)), n=2) == SV_EINVAL
+    assert call((binding.KVCacheView * 2)(_cache(), _cache()), n=2) == SV_EINVAL          # the same memory twice
+    assert call((binding.KVCacheView * 2)(_cache(), _cache(k=1024, v=256)), n=2) == SV_EINVAL
     assert raw.sv_kv_commit(None, 1, 1, 16, 16, 4, 16, 8, 16, None) == SV_EINVAL
 
 

@@ -17,6 +17,8 @@ Tolerances, from the arithmetic (u = half a step: bf16 2^-8, fp16 2^-11, fp32 2^
   (log2 T + 16) u32 in any tree of 128-token tiles.  Last, one bf16 rounding of the output.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -597,3 +599,246 @@ def test_a_round_with_attention(lib):
         a, b = (layer(c, tb, nxt, 32, [0], None) for c in (tree, chain))
         assert (a.float() - b.float()).abs().max() <= 2.0 ** -6 * b.float().abs().max()
     assert lib.device_error() == 0
+
+
+# ------------------------------------------------- long calls, and every way that work is split
+
+def rising(k, hk, d, z0=0.0):
+    """Scores that climb by up to 20 within a few tiles and fall again, through element 0 of each key (q there is 8, scale 1 / 8)."""
+    t = np.arange(len(k))
+    level = -60.0 + 20.0 * ((t // 16) % 7) + 12.0 * ((t // 128) % 5) + z0
+    k.view(len(k), hk, d)[:, :, 0] = torch.from_numpy(level.astype(np.float32)).to(torch.bfloat16)[:, None]
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("counts,lens,hq,hk,page", [
+    ([4], [30003], 8, 2, 64), ([8], [30003], 8, 2, 64),                       # one row tile, two
+    ([12], [30003], 8, 2, 128), ([25], [30003], 8, 2, 256),                   # up to 64 rows, up to 128
+    ([64], [20001], 8, 2, 64), ([40, 3], [14000, 9000], 8, 2, 16)])           # several blocks of rows
+def test_growing_scores(lib, bits, counts, lens, hq, hk, page):
+    """Every kernel moves its reference maximum, in runs of several tiles and across joined runs."""
+    r = np.random.default_rng(100 + counts[0])
+    d = 128
+    masks = tree_masks(r, counts)
+
+    def spoil(k, v, roff):
+        for b in range(len(counts)):
+            rising(k[roff[b]:roff[b + 1]], hk, d)
+    cache, offs, table, q, mask = attend_case(lib, r, bits, counts, lens, hq, hk, d, page, masks, qscale=0.1, spoil=spoil)
+    q.view(offs[-1], hq, d)[:, :, 0] = 8.0
+    out = lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), hq, scale=0.125, tree_mask=mask)
+    assert lib.device_error() == 0
+    rows = {0, offs[-1] - 1, offs[1] - 1, offs[1] // 2}
+    check_attention(out, cache, bits, offs, lens, table, page, q, masks, hq, 0.125, rows=rows)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("batch,rows,hq", [(3, 4, 8), (24, 9, 8), (48, 5, 16), (96, 4, 8)])
+def test_many_requests(lib, bits, batch, rows, hq):
+    """Ragged batches whose output rows are joined one to a CTA, eight, and sixteen."""
+    r = np.random.default_rng(110 + batch)
+    counts = [int(x) for x in r.integers(0, rows + 1, batch)]
+    counts[0], counts[-1], counts[1] = rows, 0, 1
+    lens = [int(x) for x in r.integers(0, 1500, batch)]
+    lens[2] = 4000
+    masks = tree_masks(r, counts)
+    cache, offs, table, q, mask = attend_case(lib, r, bits, counts, lens, hq, 2, 64, 16, masks)
+    out = torch.full((offs[-1] + 3, hq * 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), hq, tree_mask=mask, out=out)
+    assert lib.device_error() == 0 and torch.all(out[offs[-1]:] == 5.0)
+    check_attention(out, cache, bits, offs, lens, table, 16, q, masks, hq, 0.125, rows=set(range(0, offs[-1], 5)))
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("counts,lens", [([1, 64, 0, 17, 5], [900, 300, 7, 0, 2000]), ([0, 1, 5, 0, 8], [3, 700, 0, 9, 1300]),
+                                         ([5, 1, 1, 0, 0], [100, 300, 0, 0, 0]), ([0, 0, 0, 2, 0], [5, 0, 9, 128, 1])])
+def test_mixed_row_counts(lib, bits, counts, lens):
+    r = np.random.default_rng(120 + sum(counts))
+    masks = tree_masks(r, counts)
+    cache, offs, table, q, mask = attend_case(lib, r, bits, counts, lens, 8, 2, 128, 32, masks)
+    out = lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), 8, tree_mask=mask)
+    check_attention(out, cache, bits, offs, lens, table, 32, q, masks, 8, 128 ** -0.5)
+    none = lib.tree_attention(cache, [0] * 6, i32(lens), i32(table.tolist()), q.cuda(), 8, out=out.clone())
+    assert torch.equal(none, out)                                             # no rows: nothing is written
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("m", [3, 14, 40])
+def test_empty_masks_in_every_kernel(lib, bits, m):
+    """Rows that see nothing are zero beside rows that see something, for any number of rows."""
+    r = np.random.default_rng(130 + m)
+    masks = [0 if i % 3 == 0 else 1 << i for i in range(m)]
+    cache, offs, table, q, mask = attend_case(lib, r, bits, [m], [0], 8, 2, 128, 16, masks)
+    out = lib.tree_attention(cache, offs, i32([0]), i32(table.tolist()), q.cuda(), 8, tree_mask=mask)
+    check_attention(out, cache, bits, offs, [0], table, 16, q, masks, 8, 128 ** -0.5)
+    assert torch.all(out[::3] == 0)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("m,length", [(2, 400), (16, 260), (33, 95)])
+def test_strided_rows_and_a_full_table(lib, bits, m, length):
+    """q inside a projection's output, out inside a wider buffer and over q; every place of the table in use."""
+    r = np.random.default_rng(140 + m)
+    hq, hk, d, page = 8, 2, 128, 32
+    length = (length + m + page - 1) // page * page - m
+    cache, offs, table, q, _ = attend_case(lib, r, bits, [m], [length], hq, hk, d, page)
+    t = i32(table[:, :(length + m) // page].tolist())
+    want = lib.tree_attention(cache, offs, i32([length]), t, q.cuda(), hq)
+    assert lib.device_error() == 0
+    check_attention(want, cache, bits, offs, [length], table, page, q, None, hq, d ** -0.5, rows={0, m - 1})
+    qkv = torch.full((m + 1, (hq + 4) * d), 3.0, dtype=torch.bfloat16, device="cuda")
+    qkv[:m, d:d + hq * d] = q.cuda()
+    view = qkv[:m, d:d + hq * d]
+    wide = torch.full((m + 1, hq * d + 64), 4.0, dtype=torch.bfloat16, device="cuda")
+    lib.tree_attention(cache, offs, i32([length]), t, view, hq, out=wide[:m, 64:])
+    assert torch.equal(wide[:m, 64:], want) and torch.all(wide[m:] == 4.0) and torch.all(wide[:, :64] == 4.0)
+    lib.tree_attention(cache, offs, i32([length]), t, view, hq, out=view)
+    assert torch.equal(view, want)
+    assert torch.all(qkv[:, :d] == 3.0) and torch.all(qkv[:, d + hq * d:] == 3.0) and torch.all(qkv[m:] == 3.0)
+
+
+def test_graphs_that_share_a_workspace(lib):
+    """Two captured calls with one workspace, replayed one after the other in any order, and between eager calls."""
+    r = np.random.default_rng(150)
+    hq, hk, d, page = 8, 2, 128, 16
+    calls = []
+    for counts, lens, bits in (([3], [3000], 8), ([30, 2], [2000, 700], 16)):
+        cache, offs, table, q, _ = attend_case(lib, r, bits, counts, lens, hq, hk, d, page)
+        calls.append((cache, lib.row_offsets(offs), i32(lens), i32(table.tolist()), q.cuda(), hq))
+    ws = lib.workspace(max(lib.tree_attention_workspace_bytes(c[0], c[1], hq) for c in calls))
+    assert not ws.any()
+    for c in calls:                                                           # other calls share it and want zeros
+        lib.tree_attention(*c, workspace=ws)
+        assert not ws.any()
+    outs = [torch.zeros_like(c[4]) for c in calls]
+    want = [lib.tree_attention(*c) for c in calls]
+    graphs = []
+    for c, o in zip(calls, outs):
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            lib.tree_attention(*c, out=o, workspace=ws)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 0, 1):
+        ws.fill_(255)                                                         # a word read before it is written would be NaN
+        outs[i].zero_()
+        graphs[i].replay()
+        graphs[1 - i].replay()
+        assert torch.equal(outs[i], want[i]) and torch.equal(outs[1 - i], want[1 - i])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("counts,hk,d,page", [([700, 1, 333], 8, 128, 64), ([9000, 2001], 1, 64, 16), ([500, 900], 3, 192, 32),
+                                              ([40, 220], 16, 256, 16)])
+def test_long_appends_round_every_tie(lib, bits, counts, hk, d, page):
+    """Groups of every magnitude, with half steps that lie exactly between two codes: codes, scales and biases to the last bit."""
+    r = np.random.default_rng(160 + d)
+    rows = sum(counts)
+    top = 2 ** bits - 1
+    x = r.integers(0, 2 * top + 1, (rows, hk, d // 64, 64)) / 2.0             # scale 1: every second value is a tie
+    x[..., 0], x[..., 1] = 0, top
+    e = r.integers(-30, 9, (rows, hk, d // 64, 1)).astype(np.float64)
+    x *= 2.0 ** e                                                             # subnormal fp16 scales among them
+    x[::7] = r.standard_normal(x[::7].shape) * 2.0 ** r.integers(-4, 5, x[::7].shape)
+    k = torch.from_numpy(x.reshape(rows, hk * d).astype(np.float32)).to(torch.bfloat16)
+    v = bf16(r, rows, hk * d)
+    v.view(-1)[r.integers(0, v.numel(), 50)] = float("inf")
+    v.view(-1)[r.integers(0, v.numel(), 50)] = -float("inf")
+    v.view(-1)[r.integers(0, v.numel(), 50)] = float("nan")
+    lens = [5] * len(counts)
+    table, n_pages = tables(r, [n + c for n, c in zip(lens, counts)], page)
+    cache = lib.kv_cache_alloc(n_pages, page, hk, d, bits)
+    offs = offsets(counts)
+    lib.kv_append(cache, offs, i32(lens), i32(table.tolist()), k.cuda(), v.cuda())
+    assert lib.device_error() == 0
+    got = [t.cpu().numpy() for t in cache.tensors]
+    for b, n in enumerate(counts):
+        pos = lens[b] + np.arange(n)
+        pages, at = table[b, pos // page], pos % page
+        for i, rowset in ((0, k), (1, v)):
+            c, s, z = oa.kv_quantize(rowset[offs[b]:offs[b + 1]].float().numpy().reshape(n, hk, d), bits)
+            assert np.array_equal(got[i][pages, :, at].view(np.uint32), oa.pack(c, bits))
+            assert np.array_equal(got[2 + 2 * i][pages, :, at], s, equal_nan=True)
+            assert np.array_equal(got[3 + 2 * i][pages, :, at], z, equal_nan=True)
+    kk, vv = lib.kv_read(cache, offs, i32(lens), i32(table.tolist()))
+    short = [torch.cat(p) for p in zip(*[lib.kv_read(cache, [0, 100], i32([lens[0] + a]), i32(table[:1].tolist()))
+                                         for a in range(0, counts[0] - 99, 100)])]
+    for long, part in zip((kk, vv), short):                                   # the long call's values are the short calls'
+        a, b = long[:len(part)].view(torch.int16), part.view(torch.int16)
+        assert torch.equal(a, b) and len(part) == counts[0] // 100 * 100
+
+
+@pytest.mark.parametrize("rows,hq,hk,d,rot,interleaved,norm", [
+    (801, 48, 8, 128, 64, True, True), (2500, 12, 3, 128, 128, False, True), (3300, 18, 2, 64, 32, False, False),
+    (2000, 9, 2, 80, 80, True, True), (700, 40, 7, 256, 128, False, True), (1200, 33, 1, 128, 0, False, True)])
+def test_norm_rope_of_prompts(lib, rows, hq, hk, d, rot, interleaved, norm):
+    r = np.random.default_rng(170 + d)
+    q, k = bf16(r, rows, hq * d, scale=3.0).cuda(), bf16(r, rows, hk * d).cuda()
+    qw, kw = (1 + bf16(r, d, scale=0.2)).cuda(), (1 + bf16(r, d, scale=0.2)).cuda()
+    pos = r.integers(0, 1000000, rows)
+    inv = (1e6 ** (-np.arange(rot // 2) / max(1, rot // 2))).astype(np.float32)
+    args = dict(positions=i32(pos.tolist()), inv_freq=torch.from_numpy(inv).cuda()) if rot else {}
+    qo, ko = lib.qk_norm_rope(q, k, d, q_weight=qw, k_weight=kw, norm=norm, interleaved=interleaved, **args)
+    some = sorted(set(range(0, rows, 13)) | {rows - 1})
+    for out, x, w, n in ((qo, q, qw, hq), (ko, k, kw, hk)):
+        check_rope(f64(out[some]).reshape(-1, n, d), f64(x[some]).reshape(-1, n, d), f64(w), norm, pos[some], inv if rot else None,
+                   interleaved)
+    one, _ = lib.qk_norm_rope(q[7:8], None, d, q_weight=qw, norm=norm, interleaved=interleaved,
+                              **(dict(args, positions=args["positions"][7:8]) if rot else {}))
+    assert torch.equal(one[0], qo[7])                                         # few rows and many: the same values
+
+
+def test_rope_at_the_ends_of_the_positions(lib):
+    """Angles are exact products mod a turn: any int32 position, frequencies from 2^-40 to 2^23 (of either sign); from 2^24 on
+    and for infinity and NaN the pair is NaN."""
+    r = np.random.default_rng(180)
+    d, e = 64, [0, -1, 3, -7, -40, -20, 10, 23, -31, 1, 5, -3, 2, -10, -15, 7]
+    inv = np.array([2.0 ** x * (-1 if i % 3 == 2 else 1) for i, x in enumerate(e)] +
+                   [2.0 ** 24, 3e38, -2.0 ** 30, np.inf, -np.inf, np.nan, 0.0, 2.0 ** -149] + [1.0] * 8, np.float32)
+    pos = [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 123456789, -7654321, 65536]
+    x = bf16(r, len(pos), d).cuda()
+    got, _ = lib.qk_norm_rope(x, None, d, i32(pos), torch.from_numpy(inv).cuda(), norm=False)
+    good = np.isfinite(inv) & (np.abs(inv) < 2.0 ** 24)
+    g, xs = f64(got), f64(x)
+    assert np.isnan(g[:, :32][:, ~good]).all() and np.isnan(g[:, 32:][:, ~good]).all()
+    # positions times powers of two are exact in fp64, and the C library reduces them mod 2 pi exactly
+    a = np.array(pos, np.float64)[:, None] * np.where(good, inv, 0).astype(np.float64)
+    c, s = np.vectorize(math.cos)(a), np.vectorize(math.sin)(a)
+    want = np.concatenate([xs[:, :32] * c - xs[:, 32:] * s, xs[:, 32:] * c + xs[:, :32] * s], 1)
+    keep = np.concatenate([good, good])
+    pair = np.abs(xs[:, :32]) + np.abs(xs[:, 32:])
+    bound = 2.0 ** -8 * np.abs(want) + 32 * U32 * np.concatenate([pair, pair], 1) + 1e-38
+    assert np.all(np.abs(g - want)[:, keep] <= bound[:, keep])
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_a_cache_past_32_bits(lib, bits):
+    """Pages beyond 2^31 elements (and, in 16 bits, 2^32 bytes): the calls give what they give in a small cache."""
+    r = np.random.default_rng(190)
+    hk, d, page, hq = 8, 128, 256, 16
+    n_pages = 2 ** 31 // (hk * d * page) + 9
+    big, small = lib.kv_cache_alloc(n_pages, page, hk, d, bits), lib.kv_cache_alloc(9, page, hk, d, bits)
+    at = [n_pages - 9 + i for i in (4, 0, 8, 2)], [4, 0, 8, 2]
+    rows = bf16(r, 1000, 2 * hk * d).cuda()
+    for m in (2, 20, 64):
+        q = bf16(r, m, hq * d).cuda()
+        got = []
+        for cache, pages in zip((big, small), at):
+            t = i32([pages])
+            lib.kv_append(cache, [0, 1000], i32([0]), t, rows[:, :hk * d], rows[:, hk * d:])
+            o = lib.tree_attention(cache, [0, m], i32([1000 - m]), t, q, hq)
+            lib.kv_commit([cache], i32([1000 - m]), t, i32([[1] if m == 2 else [1, 5, 19]]), i32([1 if m == 2 else 3]))
+            got.append([o] + list(lib.kv_read(cache, [0, 1000], i32([0]), t)))
+        assert lib.device_error() == 0
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+        assert got[0][0].float().abs().max() > 0
+
+
+def test_commit_refuses_a_cache_listed_twice(lib):
+    cache, other = (lib.kv_cache_alloc(2, 16, 1, 64, 16) for _ in range(2))
+    args = (i32([0]), i32([[0, 1]]), i32([[2]]), i32([1]))
+    lib.kv_commit([cache, other], *args)
+    with pytest.raises(SVError):
+        lib.kv_commit([cache, other, cache], *args)
+    with pytest.raises(SVError):
+        lib.kv_append(lib.kv_cache(cache.k, cache.k), [0, 1], i32([0]), i32([[0, 1]]), other.k[0, 0, :1], other.k[0, 0, :1])
