@@ -378,8 +378,8 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * topological order; the anchor is row 0).  Moves what position kv_len[b] +
  * path[j] holds to position kv_len[b] + j, codes, scales and biases as they
  * are, in each of n_layers caches (a HOST array; same sizes and bits, n_layers
- * <= 1024, no array in it twice) that share the block table.  path, path_len int32, DEVICE;
- * 1 <= max_path <= 64.  A path that is not increasing or out of range is bad
+ * <= 1024, no array in it twice) that share the block table.  path, path_len
+ * int32, DEVICE; 1 <= max_path <= 64.  A path that is not increasing or out of range is bad
  * input (above). */
 typedef struct {
   void* k;
