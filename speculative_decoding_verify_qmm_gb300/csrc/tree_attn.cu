@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(32 * WPP * PAIRS) tree_attn_join_kernel(const 
   __shared__ float s_acc[PAIRS][WPP][WPP > 1 ? D : 1], s_most[PAIRS][WPP], s_weight[PAIRS][WPP];
   const int lane = threadIdx.x & 31, pair = (threadIdx.x >> 5) / WPP, warp = (threadIdx.x >> 5) % WPP;
   // The kernel before lets this one start only after its own wait, so what came before it is there already.
-  if (threadIdx.x < 32) ta_plan(p, &plan, false);
+  if (threadIdx.x < 32) ta_plan(p, &plan, true, false);
   __syncthreads();
   const long long all = plan.pre[p.map.B], per = ta_div(all + p.grid - 1, p.grid);
   const int heads = p.c.heads * p.group;
@@ -211,6 +211,7 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.ldq = ldq;
   p.group = n_q_heads / p.c.heads;
+  p.per_group = ((1u << 20) + p.group - 1) / p.group;
   p.scale = scale;
   p.mask = tree_mask;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);

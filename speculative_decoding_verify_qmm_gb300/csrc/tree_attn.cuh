@@ -23,6 +23,7 @@ struct TreeAttnParams {
   int table_pages;
   const __nv_bfloat16* q; int ldq;
   int group;                 // query heads per key head
+  uint32_t per_group;        // 2^20 / group, rounded up
   float scale;
   const uint64_t* mask;
   __nv_bfloat16* out; int ldo;
@@ -37,6 +38,7 @@ struct TreeAttnParams {
 // What every CTA derives from the lengths: prefix sums of units.
 struct TaPlan {
   long long pre[MAX_BATCH + 1];   // cost of the requests before b
+  int items[MAX_BATCH + 1];       // their items (its first entry is not used)
   int len[MAX_BATCH];             // committed tokens, brought into the table's range
   int begin;                      // p.begin_cost, or nothing where the shares are too small to hold a second beginning
 };
@@ -45,43 +47,45 @@ __host__ __device__ __forceinline__ int ta_blocks(int rows, int block) { return 
 
 __device__ __forceinline__ int ta_cost(const TreeAttnParams& p, int m) { return p.cost[m * p.group > 16]; }
 
-// By one warp.
-__device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool report) {
+// By one warp; `real` false: with lengths of zero, which reads nothing.
+__device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool real, bool report) {
   const int lane = threadIdx.x & 31;
   const RowMap& map = p.map;
   const long long cap = (long long)p.table_pages << p.c.page_shift;   // at least every request's rows (checked by the host)
-  long long all = 0;
-  for (int b = lane; b < map.B; b += 32) {
-    const int m = map.offs[b + 1] - map.offs[b];
-    long long len = p.kv_len[b];
-    if (m && (len < 0 || len + m > cap)) {
-      if (report) raise_error(ERR_BAD_INPUT);
-      len = len < 0 ? 0 : cap - m;
-    }
-    plan->len[b] = (int)len;
-    if (m) all += (long long)p.c.heads * ta_blocks(m * p.group, p.block) * ((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT) * ta_cost(p, m);
-  }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-  const int begin = all / p.grid >= 4 * p.cost[0] ? p.begin_cost : 0;
-  long long run = 0;
+  long long run = 0;             // of the units' cost
+  int items = 0;
   for (int b0 = 0; b0 < map.B; b0 += 32) {
     const int b = b0 + lane;
-    long long cost = 0;
+    long long inc = 0;
+    int n = 0;
     if (b < map.B) {
       const int m = map.offs[b + 1] - map.offs[b];
-      const long long nt = ((long long)plan->len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
-      if (m) cost = (long long)p.c.heads * ta_blocks(m * p.group, p.block) * (nt * ta_cost(p, m) + begin);
+      long long len = real ? p.kv_len[b] : 0;
+      if (m && (len < 0 || len + m > cap)) {
+        if (report) raise_error(ERR_BAD_INPUT);
+        len = len < 0 ? 0 : cap - m;
+      }
+      plan->len[b] = (int)len;
+      if (m) {
+        n = p.c.heads * ta_blocks(m * p.group, p.block);
+        inc = (long long)n * ((len + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT) * ta_cost(p, m);
+      }
     }
-    long long inc = cost;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long up = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += up;
+      const int more = __shfl_up_sync(0xffffffffu, n, off);
+      if (lane >= off) inc += up, n += more;
     }
-    if (b < map.B) plan->pre[b + 1] = run + inc;
+    if (b < map.B) {
+      plan->pre[b + 1] = run + inc;
+      plan->items[b + 1] = items + n;
+    }
     run += __shfl_sync(0xffffffffu, inc, 31);
+    items += __shfl_sync(0xffffffffu, n, 31);
   }
+  const int begin = run >= 4ll * p.cost[0] * p.grid ? p.begin_cost : 0;
+  for (int b = lane; b < map.B; b += 32) plan->pre[b + 1] += (long long)begin * plan->items[b + 1];   // its own entries
   if (lane == 0) {
     plan->pre[0] = 0;
     plan->begin = begin;
@@ -144,6 +148,38 @@ __device__ __forceinline__ bool ta_next(const TreeAttnParams& p, const TaPlan& p
   }
   return false;
 }
+
+// A CTA's share of the count, from u0 to u1, and its first run.
+struct TaShare {
+  long long u0, u1, u;
+  TaSeg s;
+  bool more;
+};
+// By the whole CTA, up to and past its wait for the kernels before.  Lengths may be those kernels' results, but the same
+// instructions are run once before the wait, on lengths of zero: they are in the caches when it counts (a first run of the
+// planning takes 2.5 us, a second 0.7).
+__device__ __forceinline__ TaShare ta_begin(const TreeAttnParams& p, TaPlan* plan) {
+  TaShare x;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) {
+      __syncthreads();         // the dry run's plan has been read
+      pdl_wait();
+      pdl_trigger();           // after the wait: the join may then read what this kernel's predecessors wrote before its own
+    }
+    if (threadIdx.x < 32) ta_plan(p, plan, pass, pass && blockIdx.x == 0);
+    __syncthreads();
+    const long long units = plan->pre[p.map.B], per = ta_div(units + p.grid - 1, p.grid);
+    x.u0 = x.u = blockIdx.x * per;
+    x.u1 = x.u0 + per < units ? x.u0 + per : units;
+    x.more = ta_next(p, *plan, &x.u, x.u0, x.u1, &x.s);
+  }
+  return x;
+}
+
+// r / p.group for a row of a block: r < 64 p.group + 128, so the product is below 2^28 and the quotient off by less than
+// r / 2^20 < 1 / p.group.
+__device__ __forceinline__ int ta_by_group(const TreeAttnParams& p, int r) { return (int)(((uint32_t)r * p.per_group) >> 20); }
 
 // Drafted tokens a row sees, as bits 0 .. m - 1.
 __device__ __forceinline__ uint64_t ta_mask(const TreeAttnParams& p, int row, int i, int m) {

@@ -142,17 +142,14 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
   const uint32_t ring_a = smem_u32(ring);
   float* const tiles = reinterpret_cast<float*>(smem + Sh::QBYTES + Sh::WEIGHTS);
 
-  pdl_wait();
-  pdl_trigger();             // after the wait: the join may then read what this kernel's predecessors wrote before its own
-  if (warp == 0) ta_plan(p, &plan, blockIdx.x == 0);
-  __syncthreads();
-  const long long units = plan.pre[p.map.B], per = ta_div(units + p.grid - 1, p.grid);
-  const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
+  const TaShare share = ta_begin(p, &plan);
+  const long long u0 = share.u0, u1 = share.u1;
   const int pm = (1 << p.c.page_shift) - 1;
 
-  TaSeg s;
-  for (long long u = u0; ta_next(p, plan, &u, u0, u1, &s);) {
-    // ------------------------------------------------------------ the ring's first copies
+  TaSeg s = share.s;
+  long long u = share.u;
+  for (bool more = share.more; more; more = ta_next(p, plan, &u, u0, u1, &s)) {
+    // ------------------------------------------------------------ the ring
     const int mts = s.rows > 16 ? MT : 1;                                   // row tiles with rows
     const int first = s.tile0 << (TA_UNIT_SHIFT - 4), all = (s.total + TN_STEP - 1) / TN_STEP;   // in steps
     const int run = all - first < s.n << (TA_UNIT_SHIFT - 4) ? all - first : s.n << (TA_UNIT_SHIFT - 4);
@@ -214,7 +211,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
     for (int i = 0; i < 2; ++i) {
       const int k = 16 * t + 8 * i + g;
       real[i] = has_q && k < s.rows;
-      const int r = s.rb * p.block + k, di = real[i] ? r / p.group : 0, hg = real[i] ? r - di * p.group : 0;
+      const int r = s.rb * p.block + k, di = real[i] ? ta_by_group(p, r) : 0, hg = real[i] ? r - di * p.group : 0;
       const __nv_bfloat16* src = p.q + (size_t)(s.row0 + di) * p.ldq + (s.h * p.group + hg) * D;
 #pragma unroll
       for (int c = 0; c < NP; ++c)
@@ -224,11 +221,11 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
     }
     uint64_t mask = 0;                                 // of row 16 t + 8 q + g, kept by the lanes with q < 2
     if (has_q && q < 2 && 16 * t + 8 * q + g < s.rows) {
-      const int di = (s.rb * p.block + 16 * t + 8 * q + g) / p.group;
+      const int di = ta_by_group(p, s.rb * p.block + 16 * t + 8 * q + g);
       mask = ta_mask(p, s.row0 + di, di, s.m);
     }
     // (asked for before the ring's copies, which would hold these loads up)
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < NST - 1; ++k) issue(k);
     if (has_q) {
       float up[2] = {minus ? -1.f : 1.f, minus ? -1.f : 1.f};
@@ -263,7 +260,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
                                                    ta_pack(x[0][2], x[0][3], RAW16), ta_pack(x[1][2], x[1][3], RAW16));
       }
       if (q < 2) {
-        const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = r / p.group;
+        const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = ta_by_group(p, r);
         s_f[k] = q ? f[1] : f[0];
         s_mask[k] = mask;
         s_out[k] = s.n == s.nt ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
@@ -584,10 +581,16 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int k = 16 * m + 8 * i + g;
-        float most = -INFINITY, weight = 0.f;
-        for (int x = 0; x < Sh::W; ++x) most = fmaxf(most, s_max[x][k]);
+        float most = -INFINITY, weight = 0.f;            // over the warps, each of the row's lanes a quarter of them
+#pragma unroll
+        for (int x = 0; x < Sh::W; x += 4) most = fmaxf(most, s_max[x + q][k]);
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
         const float base = most == -INFINITY ? 0.f : most;
-        for (int x = 0; x < Sh::W; ++x) weight += s_sum[x][k] * ta_exp2(s_max[x][k] - base);
+#pragma unroll
+        for (int x = 0; x < Sh::W; x += 4) weight += s_sum[x + q][k] * ta_exp2(s_max[x + q][k] - base);
+        weight += __shfl_xor_sync(0xffffffffu, weight, 1);
+        weight += __shfl_xor_sync(0xffffffffu, weight, 2);
         const float own = ta_exp2(s_max[warp][k] - base), factor = whole ? (weight == 0.f ? 0.f : own / weight) : own;
 #pragma unroll
         for (int n = 0; n < NTW; ++n) {
@@ -631,7 +634,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
         }
         if (odd) {
           // V held infinities or NaN in drafted tokens, which were left out of the products: the rows that see one get it
-          const int r = s.rb * p.block + k, di = r / p.group;
+          const int r = s.rb * p.block + k, di = ta_by_group(p, r);
           const uint64_t see = ta_mask(p, s.row0 + di, di, s.m);
           float* e = reinterpret_cast<float*>(&a);
 #pragma unroll 1

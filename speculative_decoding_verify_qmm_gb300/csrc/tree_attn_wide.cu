@@ -205,15 +205,12 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_trigger();             // after the wait: the join may then read what this kernel's predecessors wrote before its own
-  if (warp == 0) ta_plan(p, &plan, blockIdx.x == 0);
+  const TaShare share = ta_begin(p, &plan);
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
   const uint32_t tmem = s_tmem;
-  const long long units = plan.pre[p.map.B], per = ta_div(units + p.grid - 1, p.grid);
-  const long long u0 = blockIdx.x * per, u1 = u0 + per < units ? u0 + per : units;
+  const long long u0 = share.u0, u1 = share.u1;
 
   if (warp == Sh::PROD) {
     // ============================================================ copies of a 16-bit cache into the ring
@@ -224,8 +221,9 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       const int my_chunk = lane / PER, part = lane - my_chunk * PER;
       TaRing<Sh::OPS> ring;
       bool ok = true;
-      TaSeg s;
-      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s);) {
+      TaSeg s = share.s;
+      long long u = share.u;
+      for (bool more = share.more; ok && more; more = ta_next(p, plan, &u, u0, u1, &s)) {
         // the table's entry for this lane's chunk of tile j, checked when it is used: the load is a tile ahead
         auto page_of = [&](int j) -> int {
           const int t = (s.tile0 + j) * TA_TILE + (my_chunk << shift);
@@ -272,8 +270,9 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       const int pm = (1 << p.c.page_shift) - 1;
       int n_seg = 0;
       bool ok = true;
-      TaSeg s;
-      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s); ++n_seg) {
+      TaSeg s = share.s;
+      long long u = share.u;
+      for (bool more = share.more; ok && more; more = ta_next(p, plan, &u, u0, u1, &s), ++n_seg) {
         auto page_of = [&](int j) -> int {             // of 16-token piece `lane` of tile j; checked when it is used
           const int t = (s.tile0 + j) * TA_TILE + 16 * lane;
           if (j >= s.n || lane >= TA_TILE / 16 || t >= s.total) return 0;
@@ -332,8 +331,9 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       // descriptors differ in the start address alone
       constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
       constexpr uint32_t LO_K = 1u << 16, LO_V = (uint32_t)(TA_TILE * 128 >> 4) << 16;
-      TaSeg s;
-      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s);) {
+      TaSeg s = share.s;
+      long long u = share.u;
+      for (bool more = share.more; ok && more; more = ta_next(p, plan, &u, u0, u1, &s)) {
         const int n = __shfl_sync(0xffffffffu, s.n, 0);
         ok = ta_wait(&q_full, n_q++ & 1, abort_v, ERR_TIMEOUT_FULL);
         for (int i = 0; i < 2 * n && ok; ++i) {
@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       TaRing<Sh::OPS> ring;
       int n_seg = 0;
       bool ok = true;
-      TaSeg s;
-      for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s); ++n_seg) {
+      TaSeg s = share.s;
+      long long u = share.u;
+      for (bool more = share.more; ok && more; more = ta_next(p, plan, &u, u0, u1, &s), ++n_seg) {
         for (int i = 0; i < 2 * s.n; ++i, ring.next()) {
           int j;
           const bool is_v = ta_item(i, s.n, &j);
@@ -555,14 +556,15 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
     uint32_t n_tile = 0;                                // tiles so far: phases of s_full, pv_done
     int n_seg = 0;
     bool ok = true;
-    TaSeg s;
-    for (long long u = u0; ok && ta_next(p, plan, &u, u0, u1, &s); ++n_seg) {
+    TaSeg s = share.s;
+    long long u = share.u;
+    for (bool more = share.more; ok && more; more = ta_next(p, plan, &u, u0, u1, &s), ++n_seg) {
       const int split = s.rows <= 64 ? 2 : 1;           // copies of the rows in the lanes
       const int span = TA_ROWS / split;               // lanes of one group
       const int rr = L & (span - 1), grp = L / span;
       const bool real = rr < s.rows;
       const int r = s.rb * p.block + rr;
-      const int di = real ? r / p.group : 0, hg = real ? r - di * p.group : 0;
+      const int di = real ? ta_by_group(p, r) : 0, hg = real ? r - di * p.group : 0;
       const int row = s.row0 + di;
       const uint64_t bits = real ? ta_mask(p, row, di, s.m) : 0;
       float f;                                          // score -> exponent of 2
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
         // (what they are added to was written before the last barrier)
 #pragma unroll 1
         for (int k = 0; k < s.rows; ++k) {
-          const int rk = s.rb * p.block + k, ik = rk / p.group;
+          const int rk = s.rb * p.block + k, ik = ta_by_group(p, rk);
           const uint64_t see = ta_mask(p, s.row0 + ik, ik, s.m);
           float extra = 0.f;
 #pragma unroll 1
