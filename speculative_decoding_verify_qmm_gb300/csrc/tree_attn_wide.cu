@@ -45,7 +45,7 @@ struct TaShape {
   static constexpr int PROD = TA_SOFT + TEAMS * TA_TEAM, MMA = PROD + 1, THREADS = (MMA + 1) * 32;
   static constexpr int OP = TA_TILE * D * 2;                                       // one operand tile, 16 bits a value
   static constexpr int SCRATCH = TA_ROWS * TA_PAD * 4;
-  static constexpr int OPS = D == 128 ? 6 : 12;                                    // ring of operand tiles
+  static constexpr int OPS = (BITS == 16 ? 6 : 3) * (128 / D);                     // ring of operand tiles (codes, 6 of them: 57.2 us against 55.6)
   static constexpr int SMEM = 1024 + OPS * OP + SCRATCH;
   static_assert(SMEM <= 220 * 1024, "shared memory");
   static_assert(OPS % TEAMS == 0, "a team meets its slots in every turn, so it sees every phase of their barriers");
@@ -258,11 +258,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
           }
           ring.next();
         }
-      }
-      // every copy is waited for by its reader; after a failure, give those in flight time to land
-      if (!ok || *abort_v) {
-        const unsigned long long w0 = global_ns();
-        while (global_ns() - w0 < 50000ull) __nanosleep(1000);
       }
     } else {
       // ========================================================== descriptors for the transforming warps
@@ -838,6 +833,10 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
   }
   tc05_fence_before();
   __syncthreads();
+  if (*abort_v) {              // every copy is waited for by its reader; after a failure, those in flight get time to land
+    const unsigned long long w0 = global_ns();
+    while (global_ns() - w0 < 50000ull) __nanosleep(1000);
+  }
   if (warp == Sh::MMA) {
     tc05_fence_after();
     tmem_dealloc(tmem, 512);
