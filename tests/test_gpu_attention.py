@@ -842,3 +842,28 @@ def test_commit_refuses_a_cache_listed_twice(lib):
         lib.kv_commit([cache, other, cache], *args)
     with pytest.raises(SVError):
         lib.kv_append(lib.kv_cache(cache.k, cache.k), [0, 1], i32([0]), i32([[0, 1]]), other.k[0, 0, :1], other.k[0, 0, :1])
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("hq", [16, 32, 64])                                  # 48, 96 and 192 rows a key head
+@pytest.mark.parametrize("length", [0, 125, 2500])
+def test_what_a_row_does_not_see_stays_out_of_wide_blocks(lib, bits, hq, length):
+    r = np.random.default_rng(200 + length + hq)
+    masks = [0b000001, 0b000010, 0b000101, 0b001001, 0b010010, 0b110010]
+
+    def spoil(k, v, roff):
+        k[length + 2, 5] = float("nan")
+        v[length + 3, 70] = float("nan")
+        v[length + 4, 3] = float("inf")
+    cache, offs, table, q, mask = attend_case(lib, r, bits, [6], [length], hq, 2, 128, 16, masks, spoil=spoil)
+    out = lib.tree_attention(cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq, tree_mask=mask)
+    check_attention(out, cache, bits, offs, [length], table, 16, q, masks, hq, 128 ** -0.5, rows=[0, 1])
+    o, half = f64(out).reshape(6, hq, 128), hq // 2
+    assert np.isnan(o[2, :half]).all() and np.isfinite(o[2, half:]).all()
+    group = slice(64, 128) if bits != 16 else slice(70, 71)
+    assert np.isnan(o[3, :half, group]).all() and np.isfinite(o[3, half:]).all() and np.isfinite(o[3, :half, :64]).all()
+    if bits == 16:
+        assert np.isposinf(o[4:, :half, 3]).all()
+    keep = np.ones(128, bool)
+    keep[3] = False
+    assert np.isfinite(o[4:, :, keep]).all()
