@@ -64,14 +64,16 @@ __device__ __forceinline__ bool ta_item(int e, int n, int* tile) {
   return true;
 }
 
-// One operand tile of codes as the transforming warps need it: the cache's token index of each 16 tokens (-1: past the
-// end), and what is odd about it.
+// One operand tile of codes as the transforming warps need it: where each 16 tokens' codes, scales and biases are (past the
+// end, the cache's first tokens stand in: nothing comes of them), and what is odd about it.
 struct TaPiece {
-  long long tok[TA_TILE / 16];
-  long long valid;              // tokens of the tile before the end of the sequence
-  long long drafted;            // first drafted token of the tile (TA_TILE and more: none)
-  long long is_v;
-  long long flag;               // the segment's flag in s_bad
+  const uint8_t* codes[TA_TILE / 16];
+  const __half* scales[TA_TILE / 16];
+  const __half* biases[TA_TILE / 16];
+  int valid;                    // tokens of the tile before the end of the sequence; 0: the work has ended
+  int drafted;                  // first drafted token of the tile (TA_TILE and more: none)
+  int is_v;
+  int flag;                     // the segment's flag in s_bad
 };
 constexpr int TA_PIECES = 12;   // descriptors in flight
 
@@ -100,16 +102,6 @@ __device__ __forceinline__ void ta_dequant(uint32_t w, __half2 s2, __half2 b2, u
     }
   }
 }
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-// 16 bytes that are read once: kept out of L1.
-__device__ __forceinline__ uint4 ld_stream16(const uint8_t* a) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
-  return v;
-}
-
 // max of three (NaN operands are passed over, as by fmaxf)
 __device__ __forceinline__ float ta_max3(float a, float b, float c) {
   float r;
@@ -290,11 +282,19 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
             raise_error(ERR_BAD_INPUT);
             page = 0;                                  // stay inside the arrays: the result is undefined
           }
-          // one store for the whole descriptor: lane i writes its i-th word
-          long long word = t < s.total ? (long long)kv_token(p.c, page, s.h, t & pm) : -1;
-          word = lane == 8 ? s.total - t0 : (lane == 9 ? s.len - t0 : word);
-          word = lane == 10 ? (long long)is_v : (lane == 11 ? n_seg % TA_FLAGS : word);
-          if (lane < (int)(sizeof(TaPiece) / 8)) reinterpret_cast<long long*>(&pieces[ring.slot])[lane] = word;
+          TaPiece& x = pieces[ring.slot];
+          if (lane < TA_TILE / 16) {
+            const size_t tok = t < s.total ? kv_token(p.c, page, s.h, t & pm) : 0;
+            x.codes[lane] = (is_v ? p.c.p.v : p.c.p.k) + tok * (D * BITS / 8);
+            x.scales[lane] = (is_v ? p.c.p.vs : p.c.p.ks) + tok * (D / GROUP);
+            x.biases[lane] = (is_v ? p.c.p.vb : p.c.p.kb) + tok * (D / GROUP);
+          }
+          if (lane == 8) {
+            x.valid = s.total - t0;
+            x.drafted = s.len - t0;
+            x.is_v = is_v;
+            x.flag = n_seg % TA_FLAGS;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&piece_full[ring.slot]);
           ring.next();
@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       for (int e = 0; e < Sh::TEAMS && ok; ++e) {
         ok = ta_wait(&piece_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
         if (!ok) break;
-        if (lane < TA_TILE / 16) pieces[ring.slot].tok[lane] = -1;
         if (lane == 8) pieces[ring.slot].valid = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&piece_full[ring.slot]);
@@ -430,16 +429,17 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       // as they are used, so the loads of a whole tile are always on their way.
       constexpr int ROWB = D * BITS / 8, LPT = ROWB / 16, TPS = 32 / LPT, PERT = 128 / BITS;  // codes per 16 bytes
       constexpr int NCH = PERT / 8, G = D / GROUP;      // 16-byte operand chunks a lane makes per step; groups per token
-      const int part = lane & (LPT - 1), sub = lane / LPT;
+      // The lane's 16 bytes of a token, and its token of a step: where 8 neighbouring lanes would meet the same banks with their
+      // operand chunks - the two 64-element halves of a token lie 16 KB apart - they take each other's tokens.
+      const int part = lane & (LPT - 1);
+      const int sub = LPT == 8 ? lane / LPT ^ part >> 2 : (NCH == 4 && LPT == 4 ? lane / LPT ^ (part >> 1) << 1 : lane / LPT);
       const int grp = part * PERT / GROUP, c0 = (part * PERT / 8) & 7;
-      // Which of its chunks a lane stores first, so that 8 neighbouring lanes meet 8 different bank groups.
-      const int sel = LPT == 8 ? part >> 2 : (NCH == 4 && LPT == 4 ? (part >> 1) | ((sub & 1) << 1) : 0);
       const uint32_t pick = G == 2 && grp ? 0x3232 : 0x1010;
       // Where this lane's chunks go in its first row; the rows of later steps differ in the swizzle by one bit at most.
       uint32_t to[NCH];
 #pragma unroll
       for (int y = 0; y < NCH; ++y)
-        to[y] = smem_u32(ops) + (part * PERT / 64) * (TA_TILE * 128) + (32 * tw + sub) * 128 + (((c0 + (y ^ sel)) ^ (sub & 7)) << 4);
+        to[y] = (part * PERT / 64) * (TA_TILE * 128) + (32 * tw + sub) * 128 + (((c0 + y) ^ (sub & 7)) << 4);
       TaRing<Sh::OPS> ring;
       TaRing<TA_PIECES> ahead, here;
       ring.next(team);
@@ -448,46 +448,36 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       uint4 raw[LPT];
       uint32_t sc = 0, bi = 0;                          // scales and biases of this lane's token (two groups, or one)
       const uint8_t* at[2] = {};                        // the warp's two 16-token halves
+      const int lane_at = sub * ROWB + part * 16;
       bool live = true;
       // the next tile's addresses, scales and biases
       auto locate = [&]() -> bool {
         if (!ta_wait(&piece_full[ahead.slot], ahead.phase, abort_v, ERR_TIMEOUT_FULL)) return false;
         const TaPiece& x = pieces[ahead.slot];
-        sc = bi = 0;
-        const int valid = (int)x.valid;
-        live = valid > 0;
-        const bool is_v = x.is_v;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const long long tok = x.tok[2 * tw + hf];
-          // (past the end, the cache's first tokens stand in: the loads need no branch, and nothing comes of them)
-          at[hf] = (is_v ? p.c.p.v : p.c.p.k) + (tok < 0 ? 0 : tok) * ROWB + lane * 16;
-          if (tok >= 0 && lane / 16 == hf && t < valid) {
-            const size_t g = ((size_t)tok + (lane & 15)) * G;
-            const __half *ps = (is_v ? p.c.p.vs : p.c.p.ks) + g, *pb = (is_v ? p.c.p.vb : p.c.p.kb) + g;
-            if constexpr (G == 2) {
-              sc = *reinterpret_cast<const uint32_t*>(ps);
-              bi = *reinterpret_cast<const uint32_t*>(pb);
-            } else {
-              sc = *reinterpret_cast<const unsigned short*>(ps);
-              bi = *reinterpret_cast<const unsigned short*>(pb);
-            }
+        live = x.valid > 0;
+        if (live) {
+          at[0] = x.codes[2 * tw] + lane_at;
+          at[1] = x.codes[2 * tw + 1] + lane_at;
+          const __half *ps = x.scales[2 * tw + lane / 16] + (lane & 15) * G, *pb = x.biases[2 * tw + lane / 16] + (lane & 15) * G;
+          if constexpr (G == 2) {
+            sc = *reinterpret_cast<const uint32_t*>(ps);
+            bi = *reinterpret_cast<const uint32_t*>(pb);
+          } else {
+            sc = *reinterpret_cast<const unsigned short*>(ps);
+            bi = *reinterpret_cast<const unsigned short*>(pb);
           }
         }
         ahead.next(Sh::TEAMS);
         return true;
       };
-      auto fetch = [&](int i) {
-        const int hf = i * TPS / 16;
-        raw[i] = ld_stream16(at[hf] + (i * TPS - 16 * hf) * ROWB);
+      auto fetch = [&] {
+#pragma unroll
+        for (int i = 0; i < LPT; ++i) raw[i] = __ldcs(reinterpret_cast<const uint4*>(at[i * TPS / 16] + (i * TPS % 16) * ROWB));
       };
 #pragma unroll
       for (int i = 0; i < LPT; ++i) raw[i] = make_uint4(0, 0, 0, 0);
       bool ok = locate();
-      if (ok) {
-#pragma unroll
-        for (int i = 0; i < LPT; ++i) fetch(i);
-      }
+      if (ok && live) fetch();
       while (ok && live) {
         uint32_t sv = sc, bv = bi;
         ok = ta_wait(&op_empty[ring.slot], ring.phase ^ 1, abort_v, ERR_TIMEOUT_EMPTY);
@@ -509,26 +499,24 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
           }
           if (odd) s_bad[x.flag] = 1;
         }
-        const uint32_t dst = ring.slot * Sh::OP;
+        uint32_t even[NCH], odd[NCH];                   // in the rows of even steps, and of odd ones
+#pragma unroll
+        for (int y = 0; y < NCH; ++y) {
+          even[y] = to[y] + ring.slot * Sh::OP;
+          odd[y] = even[y] ^ ((TPS & 7) << 4);
+        }
 #pragma unroll
         for (int i = 0; i < LPT; ++i) {
-          uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
           const uint32_t s1 = __shfl_sync(0xffffffffu, sv, i * TPS + sub), b1 = __shfl_sync(0xffffffffu, bv, i * TPS + sub);
           const uint32_t sp = __byte_perm(s1, 0, pick), bp = __byte_perm(b1, 0, pick);
           const __half2 s2 = *reinterpret_cast<const __half2*>(&sp), b2 = *reinterpret_cast<const __half2*>(&bp);
-          // chunk y comes from the words of chunk y ^ sel
-          if constexpr (NCH == 4 && LPT == 4) {
-            if (sel & 1) { const uint32_t a = w[0], b = w[2]; w[0] = w[1]; w[1] = a; w[2] = w[3]; w[3] = b; }
-          }
-          if constexpr (LPT == 8 || (NCH == 4 && LPT == 4)) {
-            if (sel & (NCH / 2)) { const uint32_t a = w[0], b = w[1]; w[0] = w[2]; w[2] = a; w[1] = w[3]; w[3] = b; }
-          }
           uint32_t o[64 / BITS];
 #pragma unroll
           for (int y = 0; y < 4; ++y) ta_dequant<BITS>(w[y], s2, b2, o + y * (16 / BITS));
 #pragma unroll
           for (int y = 0; y < NCH; ++y)
-            sts128((to[y] ^ (((i * TPS) & 7) << 4)) + dst + i * TPS * 128, o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            *reinterpret_cast<uint4*>(ops + (i & 1 ? odd[y] : even[y]) + i * TPS * 128) = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
         }
         fence_proxy_async_smem();  // the tensor cores read these writes through the async proxy
         __syncwarp();
@@ -540,8 +528,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
         here.next(Sh::TEAMS);
         ok = locate();
         if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < LPT; ++i) fetch(i);
+        if (live) fetch();
       }
     }
   } else {
