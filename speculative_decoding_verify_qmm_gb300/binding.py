@@ -282,6 +282,16 @@ def _vector(name, t, dtype, dev, n):
     return t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialized tensor from the pool of the stream that writes it: memory just freed on another stream may still
+    be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _table(t, dtype, dev, B):
     """(data pointer, width) of a block table."""
     shape = t.shape
@@ -627,13 +637,13 @@ class Library:
         handle = self._launch_stream(stream, dev)
         (rows, qw), kw = q.shape, 0
         if q_out is None:
-            q_out = torch.empty((rows, qw), dtype=bf16, device=q.device)
+            q_out = _empty((rows, qw), bf16, q.device, stream)
         ldq, ldqo, ldk, ldko = _matrix("q", q, bf16, dev, rows, qw), _matrix("q_out", q_out, bf16, dev, rows, qw), 0, 0
         kp = kop = qwp = kwp = pos = inv = None
         if k is not None:
             kw = k.shape[-1]
             if k_out is None:
-                k_out = torch.empty((rows, kw), dtype=bf16, device=q.device)
+                k_out = _empty((rows, kw), bf16, q.device, stream)
             ldk, ldko = _matrix("k", k, bf16, dev, rows, kw), _matrix("k_out", k_out, bf16, dev, rows, kw)
             kp, kop = k.data_ptr(), k_out.data_ptr()
         if head_dim < 1 or qw % head_dim or kw % head_dim:
@@ -646,6 +656,8 @@ class Library:
         if inv_freq is not None:
             rot = 2 * inv_freq.numel()
             inv = _vector("inv_freq", inv_freq, torch.float32, dev, rot // 2)
+            if rot and positions is None:
+                raise SVError(SV_EINVAL, "a rotation needs positions")
             if rot:
                 pos = _vector("positions", positions, torch.int32, dev, rows)
         if rows:
@@ -665,7 +677,7 @@ class Library:
         lens, (table, pages) = _vector("the lengths", first, i32, dev, B), _table(block_table, i32, dev, B)
         ldk, ldv = _matrix("k", k, bf16, dev, rows, width), _matrix("v", v, bf16, dev, rows, width)
         handle = self._launch_stream(stream, dev)
-        if rows:
+        if rows or B < 1:
             status = call(cache.ref, B, offs, lens, table, pages, k.data_ptr(), ldk, v.data_ptr(), ldv, handle)
             if status:
                 self.check(status)
@@ -679,8 +691,8 @@ class Library:
         if k is None or v is None:
             import torch
             shape = (row_offsets[len(row_offsets) - 1], cache.width)
-            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-            v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+            k = _empty(shape, torch.bfloat16, cache.device, stream) if k is None else k
+            v = _empty(shape, torch.bfloat16, cache.device, stream) if v is None else v
         self._kv_rows(self.lib.sv_kv_read, cache, row_offsets, first, block_table, k, v, stream)
         return k, v
 
@@ -700,17 +712,15 @@ class Library:
         lens, (table, pages) = _vector("kv_len", kv_len, i32, dev, B), _table(block_table, i32, dev, B)
         mask = None if tree_mask is None else _vector("tree_mask", tree_mask, torch.int64, dev, rows)
         if out is None:
-            out = torch.empty((q.shape[0], width), dtype=bf16, device=cache.device)
+            out = _empty((q.shape[0], width), bf16, cache.device, stream)
         ldq, ldo = _matrix("q", q, bf16, dev, rows, width), _matrix("out", out, bf16, dev, rows, width)
         handle = self._launch_stream(stream, dev)
         if workspace is None:
-            workspace = torch.empty(max(256, self.tree_attention_workspace_bytes(cache, offs, n_q_heads)),
-                                    dtype=torch.uint8, device=cache.device)
-            if stream is not None:
-                workspace.record_stream(stream)  # the call outlives this tensor on that stream
+            workspace = _empty(max(256, self.tree_attention_workspace_bytes(cache, offs, n_q_heads)), torch.uint8, cache.device,
+                               stream)           # freed into the same pool: the call may outlive the tensor
         elif workspace.get_device() != dev:
             _refuse("the workspace must be on cuda:%d" % dev, workspace)
-        if rows:
+        if rows or B < 1:
             status = self.lib.sv_tree_attention(cache.ref, B, offs, lens, table, pages, q.data_ptr(), ldq, n_q_heads,
                                                 dim ** -0.5 if scale is None else scale, mask, out.data_ptr(), ldo,
                                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)

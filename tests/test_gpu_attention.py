@@ -867,3 +867,36 @@ def test_what_a_row_does_not_see_stays_out_of_wide_blocks(lib, bits, hq, length)
     keep = np.ones(128, bool)
     keep[3] = False
     assert np.isfinite(o[4:, :, keep]).all()
+
+
+def test_binding_refuses_what_is_missing(lib):
+    x = torch.zeros((2, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(SVError):
+        lib.qk_norm_rope(x, None, 64, None, torch.ones(32, device="cuda"))    # an angle without a position
+    cache = lib.kv_cache_alloc(2, 16, 1, 64, 16)
+    for offs in ([0], [0, 3, 1], [1, 2], [0, -1]):
+        with pytest.raises(SVError):
+            lib.kv_append(cache, offs, i32([0, 0]), i32([[0, 1], [1, 0]]), x, x)
+        with pytest.raises(SVError):
+            lib.tree_attention(cache, offs, i32([0, 0]), i32([[0, 1], [1, 0]]), x, 1)
+
+
+def test_results_on_a_side_stream_do_not_share_memory_with_pending_work(lib):
+    """What a call on another stream allocates is not memory that the current stream still works on."""
+    r = np.random.default_rng(210)
+    counts, lens = [3], [300]
+    cache, offs, table, q, _ = attend_case(lib, r, 16, counts, lens, 8, 2, 64, 16)
+    q, n, t = q.cuda(), i32(lens), i32(table.tolist())
+    want = lib.tree_attention(cache, offs, n, t, q, 8)
+    side, big = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        y = big
+        for _ in range(20):
+            y = y @ big                                                       # pending on the current stream
+        scratch = torch.zeros_like(want)
+        scratch += y[0, 0].to(torch.bfloat16)                                 # written after all of it
+        del scratch                                                           # and free for the current stream's next tensor
+        got = lib.tree_attention(cache, offs, n, t, q, 8, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
