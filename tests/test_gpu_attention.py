@@ -900,3 +900,29 @@ def test_results_on_a_side_stream_do_not_share_memory_with_pending_work(lib):
         got = lib.tree_attention(cache, offs, n, t, q, 8, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_the_largest_batch_and_the_widest_request(lib, bits):
+    r = np.random.default_rng(220 + bits)
+    counts, lens = [int(x) for x in r.integers(0, 3, 256)], [int(x) for x in r.integers(0, 200, 256)]
+    counts[255] = 2
+    masks = tree_masks(r, counts)
+    cache, offs, table, q, mask = attend_case(lib, r, bits, counts, lens, 2, 1, 64, 16, masks)
+    n = i32([a if c else -7 for a, c in zip(lens, counts)])                   # lengths of requests without rows are not looked at
+    out = lib.tree_attention(cache, offs, n, i32(table.tolist()), q.cuda(), 2, tree_mask=mask)
+    assert lib.device_error() == 0
+    check_attention(out, cache, bits, offs, lens, table, 16, q, masks, 2, 0.125)
+    path = np.zeros((256, 1), dtype=np.int32)
+    path[255, 0] = 1
+    before = lib.kv_read(cache, [0] * 256 + [1], i32([0] * 255 + [lens[255] + 1]), i32(table.tolist()))
+    lib.kv_commit([cache], n, i32(table.tolist()), i32(path.tolist()), i32([0] * 255 + [1]))
+    after = lib.kv_read(cache, [0] * 256 + [1], i32([0] * 255 + [lens[255]]), i32(table.tolist()))
+    assert lib.device_error() == 0 and all(torch.equal(a, b) for a, b in zip(before, after))
+
+    counts, lens, hq = [64], [140], 64                                        # 4096 rows over one key head
+    masks = tree_masks(r, counts)
+    cache, offs, table, q, mask = attend_case(lib, r, bits, counts, lens, hq, 1, 128, 64, masks)
+    out = lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), hq, tree_mask=mask)
+    assert lib.device_error() == 0
+    check_attention(out, cache, bits, offs, lens, table, 64, q, masks, hq, 128 ** -0.5, rows={0, 1, 31, 32, 62, 63})
