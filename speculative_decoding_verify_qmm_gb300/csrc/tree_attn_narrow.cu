@@ -225,49 +225,55 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
       mask = ta_mask(p, s.row0 + di, di, s.m);
     }
     // (asked for before the ring's copies, which would hold these loads up)
+    // The warps that convert Q fill their rings afterwards, but for two stages: the others' copies keep the memory busy.
 #pragma unroll 1
-    for (int k = 0; k < NST - 1; ++k) issue(k);
-    if (has_q) {
-      float up[2] = {minus ? -1.f : 1.f, minus ? -1.f : 1.f};
-      float f[2];
-      f[0] = f[1] = fabsf(p.scale) * 1.4426950408889634f;
-      auto elem = [&](int i, int e) -> float {           // the e-th of the share
-        const uint4 v = raw[i][e / 8];
-        const uint32_t w = (e / 2) % 4 == 0 ? v.x : ((e / 2) % 4 == 1 ? v.y : ((e / 2) % 4 == 2 ? v.z : v.w));
-        return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
-      };
-      if constexpr (!RAW16) {
+    for (int turn = 0, next = 0; turn < 2; ++turn) {
+#pragma unroll 1
+      for (; next < (turn || !has_q || NST < 4 ? NST - 1 : 2); ++next) issue(next);
+      if (turn == 0) {
+        if (has_q) {
+          float up[2] = {minus ? -1.f : 1.f, minus ? -1.f : 1.f};
+          float f[2];
+          f[0] = f[1] = fabsf(p.scale) * 1.4426950408889634f;
+          auto elem = [&](int i, int e) -> float {           // the e-th of the share
+            const uint4 v = raw[i][e / 8];
+            const uint32_t w = (e / 2) % 4 == 0 ? v.x : ((e / 2) % 4 == 1 ? v.y : ((e / 2) % 4 == 2 ? v.z : v.w));
+            return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+          };
+          if constexpr (!RAW16) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = 0.f;
+            for (int i = 0; i < 2; ++i) {
+              float mx = 0.f;
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) mx = fmaxf(mx, fabsf(elem(i, e)));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int ex = scale_exponent(mx);
-          up[i] *= pow2_exact(ex);
-          f[i] *= pow2_exact(-ex);
+              for (int e = 0; e < D / 4; ++e) mx = fmaxf(mx, fabsf(elem(i, e)));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              const int ex = scale_exponent(mx);
+              up[i] *= pow2_exact(ex);
+              f[i] *= pow2_exact(-ex);
+            }
+          }
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) {
+            float x[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][e] = elem(i, tn_k_pick<BITS>(kk, e)) * up[i];
+            qf[(t * KK + kk) * 32 + lane] = make_uint4(ta_pack(x[0][0], x[0][1], RAW16), ta_pack(x[1][0], x[1][1], RAW16),
+                                                       ta_pack(x[0][2], x[0][3], RAW16), ta_pack(x[1][2], x[1][3], RAW16));
+          }
+          if (q < 2) {
+            const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = ta_by_group(p, r);
+            s_f[k] = q ? f[1] : f[0];
+            s_mask[k] = mask;
+            s_out[k] = s.n == s.nt ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
+                                   : (long long)(ta_slot(s) * p.block + k) * D;
+          }
         }
-      }
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        float x[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] = elem(i, tn_k_pick<BITS>(kk, e)) * up[i];
-        qf[(t * KK + kk) * 32 + lane] = make_uint4(ta_pack(x[0][0], x[0][1], RAW16), ta_pack(x[1][0], x[1][1], RAW16),
-                                                   ta_pack(x[0][2], x[0][3], RAW16), ta_pack(x[1][2], x[1][3], RAW16));
-      }
-      if (q < 2) {
-        const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = ta_by_group(p, r);
-        s_f[k] = q ? f[1] : f[0];
-        s_mask[k] = mask;
-        s_out[k] = s.n == s.nt ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
-                               : (long long)(ta_slot(s) * p.block + k) * D;
+        __syncthreads();
       }
     }
-    __syncthreads();
     // ------------------------------------------------------------ this warp's rows
     float o[MT][NTW][4], f[MT][2], nref[MT][2], lim[MT][2], sum[MT][2];   // nref: minus the reference, lim: how far a score may outgrow it
 #pragma unroll
