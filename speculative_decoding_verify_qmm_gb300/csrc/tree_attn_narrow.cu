@@ -35,7 +35,7 @@ struct TnShape {
   static constexpr int QBYTES = MT * (D / 16) * 512;
   static constexpr int WEIGHTS = TEAM == 2 ? W * MT * 512 : 0;                   // handed over within a team
   static constexpr int LD = D == 128 ? 144 : 72;                                // floats per row of a joined tile (conflict-free)
-  static constexpr int TILE = 16 * LD * 4, JOIN = 8 * TILE;
+  static constexpr int TILE = 16 * LD * 4, JOIN = 8 * MT * TILE;
   static constexpr int BUDGET = 218 * 1024 - QBYTES - WEIGHTS;
   static constexpr int FIT = BUDGET / (W * STAGE);
   static constexpr int NST = FIT > 8 ? 8 : FIT;
@@ -624,18 +624,17 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
           }
     };
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      put(m, tiles + team * (Sh::TILE / 4));
-      __syncthreads();
+    for (int m = 0; m < MT; ++m) put(m, tiles + (8 * m + team) * (Sh::TILE / 4));
+    __syncthreads();
+    {
       constexpr int QUADS = D / 4;
-      for (int idx = threadIdx.x; idx < 16 * QUADS; idx += Sh::THREADS) {
-        const int row = idx / QUADS, d0 = 4 * (idx % QUADS);
-        const int k = 16 * m + row;
+      for (int idx = threadIdx.x; idx < 16 * MT * QUADS; idx += Sh::THREADS) {
+        const int k = idx / QUADS, d0 = 4 * (idx % QUADS);
         if (k >= s.rows) continue;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
-          const float4 t = *reinterpret_cast<const float4*>(tiles + y * (Sh::TILE / 4) + row * LD + d0 + (d0 >> 5) * 4);
+          const float4 t = *reinterpret_cast<const float4*>(tiles + (8 * (k / 16) + y) * (Sh::TILE / 4) + (k % 16) * LD + d0 + (d0 >> 5) * 4);
           a.x += t.x; a.y += t.y; a.z += t.z; a.w += t.w;
         }
         if (odd) {
