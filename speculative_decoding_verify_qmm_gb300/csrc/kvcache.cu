@@ -29,8 +29,6 @@ namespace sv {
 constexpr float KV_FAR = 65280.f;  // bf16; with it scale * code + bias <= 65344 stays finite in fp16
 constexpr int KV_THREADS = 256;    // at most
 constexpr int KV_AHEAD = 4;        // chunks a thread has in flight when rows are many
-// Times that many rows of a thread per tile (32771 rows read: 35.8 us, with 1 36.6; 8253 written as codes: 14.9, with 2 16.0).
-constexpr int KV_APPEND_STEPS = 1, KV_READ_STEPS = 2;
 // CTAs per SM of a long call: what is resident at once (read: 3 38.0 us, 4 36.1, 5 37.5, 6 49.0; append: 2 18.0, 3 15.9, 4 14.9).
 constexpr int KV_APPEND_CTAS = 4;
 constexpr int KV_READ_CTAS = 4;
@@ -505,9 +503,12 @@ static int kv_rows_call(bool append, const sv_kv_cache* cache, int B, const int3
   const int wide = (a.cols + KV_THREADS - 1) / KV_THREADS;   // CTAs across a row
   // Few rows: a chunk per thread, for parallelism.  Many: KV_AHEAD of them at once, for bytes in flight.
   const bool many = (long long)rows * a.cols >= (long long)KV_AHEAD * KV_THREADS * sms;
-  a.tile = a.step * (many ? KV_AHEAD * (append ? KV_APPEND_STEPS : KV_READ_STEPS) : 1);
-  a.tiles = (rows + a.tile - 1) / a.tile;
+  a.tile = a.step * (many ? KV_AHEAD : 1);
   const int most = (sms * (append ? KV_APPEND_CTAS : KV_READ_CTAS) + wide - 1) / wide;
+  // A long read takes tiles of twice that, fewer lookups to wait for (32771 rows: 35.7 us against 36.6); where a CTA would have
+  // less than two, they only balance worse (8253 rows written and read: 24.9 us against 26.2).
+  if (many && !append && rows >= 4ll * a.tile * most) a.tile *= 2;
+  a.tiles = (rows + a.tile - 1) / a.tile;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pdl_config(dim3(a.tiles < most ? a.tiles : most, wide), dim3(threads), 0,
                                       static_cast<cudaStream_t>(stream), attr);
