@@ -367,14 +367,15 @@ __global__ void __launch_bounds__(KV_THREADS) kv_commit_kernel(const __grid_cons
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.y, tid = threadIdx.x;
-  if (tid == 0) s_n = s_bad = 0;
-  __syncthreads();
+  // the path is asked for before its length is known: one wait less
+  const int* path = p.path + (size_t)b * p.max_path;
+  const int at = tid < p.max_path ? path[tid] : 0, before = tid && tid < p.max_path ? path[tid - 1] : -1;
   const int n = p.path_len[b];
   const long long len = p.kv_len[b];
+  if (tid == 0) s_n = s_bad = 0;
+  __syncthreads();
   bool bad = n < 0 || n > p.max_path || (n > 0 && len < 0);
   if (!bad && tid < n) {
-    const int at = p.path[(size_t)b * p.max_path + tid];
-    const int before = tid ? p.path[(size_t)b * p.max_path + tid - 1] : -1;
     bad = at <= before || at < 0 || at >= KV_MAX_DRAFT;
     if (!bad) {
       const long long sp = kv_page_of(p.c, p.table, p.table_pages, b, len + at);
