@@ -336,9 +336,10 @@ __global__ void __launch_bounds__(KV_THREADS, KV_READ_CTAS) kv_read_kernel(const
 // source of a later step i > j (path[i] > path[j] >= j), so a thread that owns a
 // fixed slice of a token's bytes may read several sources ahead and still
 // write in order; threads own disjoint slices and never meet.  Measured: 24 paths of 9 in 64 layers of 8 heads of 128, bf16,
-// 14.3 us (4.4 TB/s); one path of 5 in 36 layers 2.5 us, a launch.
+// 12.7 us (5.0 TB/s); one path of 5 in 36 layers 2.5 us, a launch.
 constexpr int COMMIT_LAYERS = 64;   // caches per launch: their pointers ride in the launch parameters
-constexpr int COMMIT_AHEAD = 8;
+constexpr int COMMIT_AHEAD = 6;      // sources in flight per thread, and CTAs per SM: what 40 registers a thread allow
+constexpr int COMMIT_CTAS = 6;       // (24 paths in 64 layers: 12.7 us; 8 and 5 12.8, 4 and 8 13.2, 8 and 6 15.7)
 
 struct CommitParams {
   KvPtrs L[COMMIT_LAYERS];
@@ -361,7 +362,7 @@ __device__ __forceinline__ void move_slices(T* base, size_t stride_t, int lane_t
   }
 }
 
-__global__ void __launch_bounds__(KV_THREADS) kv_commit_kernel(const __grid_constant__ CommitParams p) {
+__global__ void __launch_bounds__(KV_THREADS, COMMIT_CTAS) kv_commit_kernel(const __grid_constant__ CommitParams p) {
   __shared__ long long s_src[KV_MAX_DRAFT], s_dst[KV_MAX_DRAFT];  // token index of head 0
   __shared__ int s_n, s_bad;
   pdl_trigger();
