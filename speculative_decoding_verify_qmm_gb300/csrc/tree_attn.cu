@@ -237,10 +237,12 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   // rows takes 4.  (One request of 32 rows over 16384 tokens: 22.7 us in a block of 32, 25.4 in two of 16; 48 requests of 4 to 20
   // rows: 192.6 in blocks of 32, 165.5 in blocks of 16.)
   p.block = narrow ? (by16 < by32 ? 16 : 32) : TA_MAX_BLOCK;
-  // Beginning an item costs some 7 us against 1.2 a unit in the narrow kernel, 10 against 1.6 in the wide one.
+  // Beginning an item, in the same measure: what gave the least time over several batches and lengths.  (Wide, bf16, 32 rows of
+  // 65536 tokens: 60.8 us with 30, 59.0 with 60; 4 x 8 rows in 48 heads 68.0 and 64.2, over codes 54.8 and 56.1.  Narrow, 8-bit,
+  // 8 rows of 65536 tokens: 57.4 with 25, 52.8 with 35; 8 x 4 rows 32.4 and 33.2.)
   p.cost[0] = 5;
   p.cost[1] = p.block == 32 ? 7 : 5;
-  p.begin_cost = narrow ? 25 : 30;
+  p.begin_cost = narrow ? (p.block == 16 ? 25 : 35) : (p.c.bits == 16 ? 60 : 35);
   // the lengths are on the device: size the grid for the longest the table allows
   const long long most_units = (((long long)table_pages << p.c.page_shift) + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
   long long most = 0;
