@@ -13,8 +13,8 @@
 // four to a scheduler.  Two row tiles: 8 warps, and a warp takes two steps at once where it can, so that two chains overlap.
 // (Teams for two row tiles spill: 207 us against 193; 16 warps without teams join in two rounds: 11.6 us for one row against 10.1.)
 //
-// Measured (32 query and 8 key heads of 128): one row over 2048 tokens, 8-bit, 9.4 us; 8 rows over 16384 tokens, 8-bit, 22.4 us
-// (1.6 TB/s); 48 requests of 1 to 5 rows, up to 12007 tokens, 4-bit, 158 us (2.6 TB/s of the 6.8 that a copy reaches).
+// Measured (32 query and 8 key heads of 128): one row over 2048 tokens, 8-bit, 9.4 us; 8 rows over 16384 tokens, 8-bit, 23.3 us
+// (1.5 TB/s); 48 requests of 1 to 5 rows, up to 12007 tokens, 4-bit, 158 us (2.6 TB/s of the 6.8 that a copy reaches).
 //
 // Codes become MMA operands in registers, without a second trip through shared memory.  S = Q K^T: the contraction may run
 // over a head's elements in any order, so the lane that holds column q of a token's k-slices takes whole 16-byte pieces of
