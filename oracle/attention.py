@@ -35,7 +35,7 @@ def norm_rope(x, weight, eps, norm, positions, inv_freq, interleaved):
 def kv_quantize(x, bits):
     """(codes int [..., dim], scales fp16, biases fp16 [..., dim / 64]) of fp32 values, the format's own roundings."""
     x = np.asarray(x, dtype=np.float32)
-    g = x.reshape(x.shape[:-1] + (-1, GROUP))
+    g = x.reshape(x.shape[:-1] + (x.shape[-1] // GROUP, GROUP))
     bad = np.isnan(g).any(axis=-1)
     g = np.clip(np.where(bad[..., None], np.float32(0), g), -KV_FAR, KV_FAR)
     lo, hi = g.min(axis=-1), g.max(axis=-1)
@@ -58,14 +58,14 @@ def kv_dequantize(codes, s, b):
 def pack(codes, bits):
     """uint32 words [..., dim * bits / 32], least significant field first."""
     per = 32 // bits
-    c = np.asarray(codes, dtype=np.uint64).reshape(codes.shape[:-1] + (-1, per))
+    c = np.asarray(codes, dtype=np.uint64).reshape(codes.shape[:-1] + (codes.shape[-1] // per, per))
     return (c << (np.arange(per, dtype=np.uint64) * np.uint64(bits))).sum(axis=-1).astype(np.uint32)
 
 
 def unpack(words, bits):
     per = 32 // bits
     w = np.asarray(words, dtype=np.uint32)[..., None] >> (np.arange(per, dtype=np.uint32) * np.uint32(bits))
-    return (w & np.uint32(2 ** bits - 1)).astype(np.int64).reshape(words.shape[:-1] + (-1,))
+    return (w & np.uint32(2 ** bits - 1)).astype(np.int64).reshape(words.shape[:-1] + (words.shape[-1] * (32 // bits),))
 
 
 def chain_masks(m):

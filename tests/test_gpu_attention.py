@@ -729,7 +729,7 @@ def test_graphs_that_share_a_workspace(lib):
 
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("counts,hk,d,page", [([700, 1, 333], 8, 128, 64), ([9000, 2001], 1, 64, 16), ([500, 900], 3, 192, 32),
-                                              ([40, 220], 16, 256, 16)])
+                                              ([40, 220], 16, 256, 16), ([301, 240], 5, 256, 32), ([7, 0, 12], 5, 256, 16)])
 def test_long_appends_round_every_tie(lib, bits, counts, hk, d, page):
     """Groups of every magnitude, with half steps that lie exactly between two codes: codes, scales and biases to the last bit."""
     r = np.random.default_rng(160 + d)
