@@ -156,8 +156,8 @@ struct TaShare {
   bool more;
 };
 // By the whole CTA, up to and past its wait for the kernels before.  Lengths may be those kernels' results, but the same
-// instructions are run once before the wait, on lengths of zero: they are in the caches when it counts (a first run of the
-// planning takes 2.5 us, a second 0.7).
+// instructions are run once before the wait, on lengths of zero: they are in the caches when it counts.  (A first run of the
+// planning takes 2.5 us; with the dry run before it one row over 2048 tokens takes 9.4 us against 10.3.)
 __device__ __forceinline__ TaShare ta_begin(const TreeAttnParams& p, TaPlan* plan) {
   TaShare x;
 #pragma unroll 1
