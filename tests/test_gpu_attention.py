@@ -926,3 +926,30 @@ def test_the_largest_batch_and_the_widest_request(lib, bits):
     out = lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), hq, tree_mask=mask)
     assert lib.device_error() == 0
     check_attention(out, cache, bits, offs, lens, table, 64, q, masks, hq, 128 ** -0.5, rows={0, 1, 31, 32, 62, 63})
+
+
+def test_two_streams_at_once(lib):
+    """Rounds on two streams, each with its own cache and workspace, do not touch each other."""
+    r = np.random.default_rng(230)
+    hq, hk, d, page = 8, 2, 128, 32
+    sides = []
+    for counts, lens, bits in (([7, 2], [3000, 500], 8), ([40], [2500], 16)):
+        cache, offs, table, q, _ = attend_case(lib, r, bits, counts, lens, hq, hk, d, page)
+        offs = lib.row_offsets(offs)
+        rows = [bf16(r, offs[len(counts)], hk * d).cuda() for _ in range(2)]
+        args = (cache, offs, i32(lens), i32(table.tolist()))
+        ws = lib.workspace(lib.tree_attention_workspace_bytes(cache, offs, hq))
+        lib.kv_append(*args, *rows)
+        want = lib.tree_attention(*args, q.cuda(), hq)
+        path = i32([[1, 2]] * len(counts)), i32([2] + [0] * (len(counts) - 1))
+        sides.append((args, rows, q.cuda(), ws, want, path, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for args, rows, q, ws, want, path, stream in sides:
+            with torch.cuda.stream(stream):
+                lib.kv_append(*args, *rows)
+                outs.append((lib.tree_attention(*args, q, hq, workspace=ws), want))
+                lib.kv_commit([args[0]], args[2], args[3], *path)             # undone by the next append
+    torch.cuda.synchronize()
+    assert lib.device_error() == 0 and all(torch.equal(a, b) for a, b in outs)
