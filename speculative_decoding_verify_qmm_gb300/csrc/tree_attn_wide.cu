@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
               lim = move ? Sh::GROW : lim;
               nref = now;
               sum *= fix;
+              tmem_st_wait();                           // the tile's weights so far are read back below
               if (!product_over) {
                 // S of this tile is there, so the product before the last has ended: one phase is open at most
                 ok = ta_wait(&pv_done, (n_tile - 1) & 1, abort_v, ERR_TIMEOUT_FULL);

@@ -1,0 +1,69 @@
+"""Tree attention where its number formats end: references that move in every chunk of tokens, far queries and values,
+weights at the bottom of fp16, codes at the top of it.
+
+The tolerance is that of test_gpu_attention.py (its docstring derives it) and one term more.  Over codes a weight is fp16,
+and below 2^-14 its rounding is no longer relative: it is off by up to 2^-25.  A row's reference is set so that its largest
+weight then is 2^5, and stays there or grows; so that is at most 2^-30 of the largest weight, and a token's share of
+the numerator moves by up to 2^-30 max(p) |v|.  A run of a row with a lower maximum of its own is nearer still.  Over a 16-bit
+cache weights are bf16, whose range is fp32's: nothing is added.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_attention import U32, attend_case, f64, i32, stored
+
+pytestmark = pytest.mark.gpu
+
+
+def check(got, cache, bits, offs, lens, table, page, q, hq, scale, floor=0.0):
+    """Every row of chains against fp64; `floor`: what a case adds to the bound, as a share of max(p) |v|."""
+    hk, d = cache.view.n_kv_heads, cache.view.head_dim
+    tail = (2.0 ** -30 if bits != 16 else 0.0) + floor
+    worst = 0.0
+    for b in range(len(offs) - 1):
+        m = offs[b + 1] - offs[b]
+        k, v = stored(cache, bits, table, page, b, lens[b] + m)
+        for i in range(m):
+            n = lens[b] + i + 1
+            qi, gi = f64(q[offs[b] + i]).reshape(hq, d), f64(got[offs[b] + i]).reshape(hq, d)
+            for h in range(hq):
+                kk, vv = k[:n, h // (hq // hk)], v[:n, h // (hq // hk)]
+                z = scale * (kk @ qi[h])
+                p = np.exp(z - z.max())
+                p /= p.sum()
+                want = p @ vv
+                mag = abs(scale) * (np.abs(kk) @ np.abs(qi[h]))
+                e = mag * ((2.0 ** -11 if bits != 16 else 0.0) + (d + 8) * U32) + 8 * U32 * (np.abs(z) + np.abs(z).max() + 1)
+                rw = (2.0 ** -8 if bits == 16 else 2.0 ** -11) + (np.log2(n + 1) + 16) * U32
+                rr = rw + (0.0 if bits == 16 else 2.0 ** -11)
+                den = p @ np.expm1(e + rw)
+                assert den < 0.5
+                bound = ((p * np.expm1(e + rr) + tail * p.max()) @ np.abs(vv) + np.abs(want) * den) / (1 - den)
+                bound = bound * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(want) + 1e-30
+                worst = max(worst, float((np.abs(gi[h] - want) / bound).max()))
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("hq", [3, 8, 16, 32])                                # 9, 24, 48 and 96 rows over one key head
+@pytest.mark.parametrize("first", [0, 96])
+def test_a_reference_that_moves_in_every_chunk(lib, bits, hq, first):
+    """Scores climb by 11 (16 powers of two) every 32 tokens of a tile of 128, so the weights that a tile has so far are read
+    back and rescaled; the values of the tokens one step below the top are large enough to count."""
+    r = np.random.default_rng(300 + hq + first)
+    d, m, length = 128, 3, 700 + first
+    step = np.arange(length + m) // 32 % 4
+
+    def spoil(k, v, roff):
+        k[:, 0] = torch.from_numpy((11.0 * step - 16.0).astype(np.float32)).to(torch.bfloat16)
+        v *= torch.from_numpy(np.where(step == 2, 4096.0, 1.0).astype(np.float32)).to(torch.bfloat16)[:, None]
+    cache, offs, table, q, _ = attend_case(lib, r, bits, [m], [length], hq, 1, d, 64, qscale=0.05, spoil=spoil)
+    q.view(m, hq, d)[:, :, 0] = 8.0
+    args = (cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq)
+    out = lib.tree_attention(*args, scale=0.125)
+    assert lib.device_error() == 0
+    check(out, cache, bits, offs, [length], table, 64, q, hq, 0.125)
+    for _ in range(20):
+        assert torch.equal(lib.tree_attention(*args, scale=0.125), out)
