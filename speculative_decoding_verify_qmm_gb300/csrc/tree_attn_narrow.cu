@@ -51,8 +51,8 @@ struct TnShape {
   static constexpr int RING = W * NST * STAGE;
   static constexpr int SMEM = QBYTES + WEIGHTS + (RING > JOIN ? RING : JOIN);             // the join's tiles lie in the drained ring
   static_assert(NST >= 2 * PAIR && MT <= W, "stages, and a warp for each row tile of Q");
-  // as in the kernel for many rows: room for a score to outgrow its row's reference, in the weights' 16-bit type
-  static constexpr float BIAS = BITS == 16 ? 0.f : 5.f, GROW = BITS == 16 ? 60.f : 15.f;
+  // as in the kernel for many rows: the largest weight's exponent when the reference is set, and what it may grow to
+  static constexpr float BIAS = BITS == 16 ? -30.f : 5.f, GROW = BITS == 16 ? -15.f : 15.f;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

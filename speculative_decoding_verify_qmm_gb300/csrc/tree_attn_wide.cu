@@ -7,7 +7,7 @@
 // Per tile, S = Q K^T with Q (A operand) resident in tensor memory, K from shared memory, S [row x token] in tensor memory;
 // softmax of a lane by one thread; P (16 bits) in S's place as the A operand of O += P V, V from shared memory as it lies
 // ([token][element], MN-major).  O stays in tensor memory.  A row's weights are 2^(S f - ref) with a reference that moves
-// only when a score has outgrown it by 2^15 (fp16) or 2^60 (bf16): rarely, and then O and what there is of P are rescaled.
+// only when a score has outgrown it by 2^10 (fp16) or 2^15 (bf16): rarely, and then O and what there is of P are rescaled.
 //
 // Up to 64 rows are laid into the lanes twice, and each copy takes its own half of every tile's tokens - the off-diagonal
 // blocks of P are zero - as an independent softmax that meets the other at the end of the item: all four softmax warps
@@ -58,9 +58,12 @@ struct TaShape {
   static_assert(SMEM <= 220 * 1024, "shared memory");
   static_assert(OPS % TEAMS == 0, "a team meets its slots in every turn, so it sees every phase of their barriers");
   static_assert(OPS <= 2 * TA_FLAGS - 4, "flags");
-  // A weight enters the second product in 16 bits: bf16 has room for any score difference that fp32 sums can bear, fp16
-  // for 2^15; there the reference starts 2^5 below the largest score, so that weights down to 2^-29 of it keep all their bits.
-  static constexpr float BIAS = BITS == 16 ? 0.f : 5.f, GROW = BITS == 16 ? 60.f : 15.f;
+  // A weight enters the second product in 16 bits.  BIAS: exponent of the largest weight when the reference is set, GROW: what
+  // it may grow to before the reference moves.  fp16 has room up to 2^15; there the reference starts 2^5 below the largest
+  // score, so that weights down to 2^-29 of it keep all their bits.  bf16 has the range of fp32, and so have the values of a
+  // 16-bit cache: weights of at most 2^-15 keep the sums of any finite values finite (of 2^15 tokens at GROW, of 2^30 at BIAS), and
+  // at BIAS those down to 2^-96 of the largest keep all their bits.
+  static constexpr float BIAS = BITS == 16 ? -30.f : 5.f, GROW = BITS == 16 ? -15.f : 15.f;
 };
 
 // Order of a segment's operand tiles: K0, K1, V0, K2, V1, ..., V(n-1).

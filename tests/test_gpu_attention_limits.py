@@ -17,12 +17,12 @@ from tests.test_gpu_attention import U32, attend_case, f64, i32, stored
 pytestmark = pytest.mark.gpu
 
 
-def check(got, cache, bits, offs, lens, table, page, q, hq, scale, floor=0.0):
-    """Every row of chains against fp64; `floor`: what a case adds to the bound, as a share of max(p) |v|."""
+def check(got, cache, bits, offs, lens, table, page, q, hq, scale, requests=None):
+    """Every row of chains (of some requests) against fp64."""
     hk, d = cache.view.n_kv_heads, cache.view.head_dim
-    tail = (2.0 ** -30 if bits != 16 else 0.0) + floor
+    tail = 2.0 ** -30 if bits != 16 else 0.0
     worst = 0.0
-    for b in range(len(offs) - 1):
+    for b in requests or range(len(offs) - 1):
         m = offs[b + 1] - offs[b]
         k, v = stored(cache, bits, table, page, b, lens[b] + m)
         for i in range(m):
@@ -67,3 +67,23 @@ def test_a_reference_that_moves_in_every_chunk(lib, bits, hq, first):
     check(out, cache, bits, offs, [length], table, 64, q, hq, 0.125)
     for _ in range(20):
         assert torch.equal(lib.tree_attention(*args, scale=0.125), out)
+
+
+@pytest.mark.parametrize("hq", [3, 8, 16, 32])
+@pytest.mark.parametrize("climb,size", [(35.0, 2.0 ** 110), (0.0, 3e38), (35.0, 2.0 ** -90)])
+def test_large_and_small_values_of_a_16_bit_cache(lib, hq, climb, size):
+    """Finite values give finite averages, however far scores have climbed since the reference was set: by 40 powers of two in each
+    SM's share of 128 requests."""
+    r = np.random.default_rng(310 + hq)
+    d, m, length, batch = 128, 3, 1500, 128
+
+    def spoil(k, v, roff):
+        for b in range(batch):
+            k[roff[b]:roff[b + 1], 0] = torch.linspace(-climb / 2, climb / 2, length + m).to(torch.bfloat16)
+        v.copy_((v.double().clamp(-1, 1) * size).to(torch.bfloat16) if climb else torch.full_like(v, size))
+    lens = [length] * batch
+    cache, offs, table, q, _ = attend_case(lib, r, 16, [m] * batch, lens, hq, 1, d, 64, qscale=0.05, spoil=spoil)
+    q.view(m * batch, hq, d)[:, :, 0] = 8.0
+    out = lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), hq, scale=0.125)
+    assert lib.device_error() == 0 and out.isfinite().all()
+    check(out, cache, 16, offs, lens, table, 64, q, hq, 0.125, requests=range(0, batch, 41))
