@@ -361,7 +361,7 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * not reach it, infinities and NaN included; a visible value of +-inf gives
  * +-inf or NaN.  q and out bf16 [rows, n_q_heads*head_dim] (strides ldq, ldo);
  * query head h reads key head h / (n_q_heads / n_kv_heads).  One row (m = 1)
- * is the plain decode step.  scale is finite.  head_dim 64 or 128
+ * is the plain decode step.  |scale| <= 2^127.  head_dim 64 or 128
  * (SV_EUNSUPPORTED otherwise), n_q_heads a multiple of n_kv_heads and at most
  * 64 times as many.  q and out 16-byte aligned, strides multiples of 8.
  * Softmax statistics and sums are fp32 (q . k too); the probabilities enter

@@ -206,6 +206,16 @@ __device__ __forceinline__ uint32_t ta_pack(float lo, float hi, bool bf16) {
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Over codes a row of q enters the products as fp16 times 2^e, its largest magnitude mx at 2^14 to 2^15 (less for a subnormal
+// mx, exactly all the same): e for any finite mx, and for infinity one with which finite elements stay finite.
+__device__ __forceinline__ int ta_query_exponent(float mx) {
+  const int e = 141 - (int)(__float_as_uint(mx) >> 23);
+  return mx > 0.f ? (e < 126 ? e : 126) : 0;
+}
+// score -> exponent of 2, from products of a row times 2^e.  2^-e times the scale comes first: the scale alone may be subnormal.
+__device__ __forceinline__ float ta_score_factor(float scale, int e) {
+  return fminf(fabsf(scale) * pow2_exact(-e) * 1.4426950408889634f, 3.402823466e38f);
+}
 __device__ __forceinline__ bool ta_half_bad(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
 
 // Where a CTA's run of an item leaves its partial sums.

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
         if (has_q) {
           float up[2] = {minus ? -1.f : 1.f, minus ? -1.f : 1.f};
           float f[2];
-          f[0] = f[1] = fabsf(p.scale) * 1.4426950408889634f;
+          f[0] = f[1] = ta_score_factor(p.scale, 0);
           auto elem = [&](int i, int e) -> float {           // the e-th of the share
             const uint4 v = raw[i][e / 8];
             const uint32_t w = (e / 2) % 4 == 0 ? v.x : ((e / 2) % 4 == 1 ? v.y : ((e / 2) % 4 == 2 ? v.z : v.w));
@@ -257,9 +257,9 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
               for (int e = 0; e < D / 4; ++e) mx = fmaxf(mx, fabsf(elem(i, e)));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              const int ex = scale_exponent(mx);
+              const int ex = ta_query_exponent(mx);
               up[i] *= pow2_exact(ex);
-              f[i] *= pow2_exact(-ex);
+              f[i] = ta_score_factor(p.scale, ex);
             }
           }
 #pragma unroll

@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)row * p.ldq + (s.h * p.group + hg) * D);
         const bool minus = p.scale < 0.f;               // the sign goes into q, so a larger S is a larger score
-        f = fabsf(p.scale) * 1.4426950408889634f;
+        f = ta_score_factor(p.scale, 0);
         float up = minus ? -1.f : 1.f;
         if constexpr (!RAW16) {
           float mx = 0.f;
@@ -576,9 +576,9 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
             for (int y = 0; y < 4; ++y)
               mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u))));
           }
-          const int ex = scale_exponent(mx);
+          const int ex = ta_query_exponent(mx);
           up *= pow2_exact(ex);
-          f *= pow2_exact(-ex);
+          f = ta_score_factor(p.scale, ex);
         }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {

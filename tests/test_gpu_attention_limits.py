@@ -87,3 +87,18 @@ def test_large_and_small_values_of_a_16_bit_cache(lib, hq, climb, size):
     out = lib.tree_attention(cache, offs, i32(lens), i32(table.tolist()), q.cuda(), hq, scale=0.125)
     assert lib.device_error() == 0 and out.isfinite().all()
     check(out, cache, 16, offs, lens, table, 64, q, hq, 0.125, requests=range(0, batch, 41))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hq", [3, 8, 16, 32])
+@pytest.mark.parametrize("size,scale", [(3e37, 2e-38), (2.0 ** 117, 2.0 ** -117), (2.0 ** -125, 2.0 ** 124), (2.0 ** -131, 2.0 ** 127)])
+def test_queries_of_any_size_over_codes(lib, bits, hq, size, scale):
+    """A row of q enters the products as fp16 times a power of two, for any finite bf16 values."""
+    r = np.random.default_rng(320 + hq)
+    d, m, length = 128, 3, 300
+    cache, offs, table, q, _ = attend_case(lib, r, bits, [m], [length], hq, 1, d, 64, qscale=1.0)
+    q = (q.double() * size / 3).to(torch.bfloat16)
+    assert q.isfinite().all()
+    out = lib.tree_attention(cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq, scale=scale)
+    assert lib.device_error() == 0 and out.isfinite().all()
+    check(out, cache, bits, offs, [length], table, 64, q, hq, scale)
