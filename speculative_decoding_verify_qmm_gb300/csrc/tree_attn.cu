@@ -202,6 +202,7 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8)
     return fail(SV_EINVAL, "q and out must be non-null, 16-byte aligned, with strides that are multiples of 8");
   if (ldq < n_q_heads * p.c.dim || ldo < n_q_heads * p.c.dim) return fail(SV_EINVAL, "ldq and ldo must be >= n_q_heads * head_dim");
+  if (q == out && ldq != ldo && p.map.offs[B] > 1) return fail(SV_EINVAL, "an in-place call needs equal strides");
   if (!(std::fabs(scale) <= 0x1p127f)) return fail(SV_EINVAL, "scale must be at most 2^127 in magnitude");
   if (!aligned(tree_mask, 8)) return fail(SV_EINVAL, "tree_mask must be 8-byte aligned");
   const int sms = ta_sms();
