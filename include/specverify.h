@@ -365,9 +365,10 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * (SV_EUNSUPPORTED otherwise), n_q_heads a multiple of n_kv_heads and at most
  * 64 times as many.  q and out 16-byte aligned, strides multiples of 8.
  * Softmax statistics and sums are fp32 (q . k too); the probabilities enter
- * the second product in 16 bits.  Over a 16-bit cache the weights of that sum
- * are at most 2^-15: finite values give finite outputs where |v| adds up to
- * less than 2^142 over the tokens.  The result does not depend on timing: it is bitwise
+ * the second product in 16 bits: over a 16-bit cache as bf16, over codes as
+ * fp16 (2^-11 of themselves, or 2^-30 of the row's largest where that is more).
+ * Over a 16-bit cache the weights of that sum are at most 2^-15: finite values
+ * give finite outputs where |v| adds up to less than 2^142 over the tokens.  The result does not depend on timing: it is bitwise
  * reproducible for given inputs on one device.
  * out may be q (same stride); other overlap is not allowed.
  * Workspace: sv_tree_attention_workspace_bytes (0 for a bad argument), 256-byte

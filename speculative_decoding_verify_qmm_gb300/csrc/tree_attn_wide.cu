@@ -59,8 +59,9 @@ struct TaShape {
   static_assert(OPS % TEAMS == 0, "a team meets its slots in every turn, so it sees every phase of their barriers");
   static_assert(OPS <= 2 * TA_FLAGS - 4, "flags");
   // A weight enters the second product in 16 bits.  BIAS: exponent of the largest weight when the reference is set, GROW: what
-  // it may grow to before the reference moves.  fp16 has room up to 2^15; there the reference starts 2^5 below the largest
-  // score, so that weights down to 2^-29 of it keep all their bits.  bf16 has the range of fp32, and so have the values of a
+  // it may grow to before the reference moves.  fp16 has room up to 2^15; there the largest weight starts at 2^5, so that weights
+  // down to 2^-19 of it keep all their bits and smaller ones are off by at most 2^-30 of it (2^20 such tokens: 2^-10 of their values;
+  // a higher start would move the reference, and rescale, more often).  bf16 has the range of fp32, and so have the values of a
   // 16-bit cache: weights of at most 2^-15 keep the sums of any finite values finite (of 2^15 tokens at GROW, of 2^30 at BIAS), and
   // at BIAS those down to 2^-96 of the largest keep all their bits.
   static constexpr float BIAS = BITS == 16 ? -30.f : 5.f, GROW = BITS == 16 ? -15.f : 15.f;

@@ -102,3 +102,24 @@ def test_queries_of_any_size_over_codes(lib, bits, hq, size, scale):
     out = lib.tree_attention(cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq, scale=scale)
     assert lib.device_error() == 0 and out.isfinite().all()
     check(out, cache, bits, offs, [length], table, 64, q, hq, scale)
+
+
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("hq", [3, 8, 16, 32])
+def test_a_long_tail_behind_large_weights(lib, bits, hq):
+    """Every 16th token has a weight 2^22 to 2^30 times the others', and zeros in half of the head: there the output is the tail's alone."""
+    r = np.random.default_rng(330 + hq)
+    d, m, length = 128, 3, 5000
+
+    def spoil(k, v, roff):
+        large = torch.arange(length + m) % 16 == 0
+        far = -np.log(2) * r.uniform(22, 30, length + m)
+        k[:, 0] = torch.where(large, torch.zeros(length + m), torch.from_numpy(far.astype(np.float32))).to(torch.bfloat16)
+        v.abs_()
+        v[large, :64] = 0
+    cache, offs, table, q, _ = attend_case(lib, r, bits, [m], [length], hq, 1, d, 64, qscale=0.02, spoil=spoil)
+    q.view(m, hq, d)[:, :, 0] = 8.0
+    out = lib.tree_attention(cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq, scale=0.125)
+    assert lib.device_error() == 0
+    check(out, cache, bits, offs, [length], table, 64, q, hq, 0.125)
+    assert torch.all(out.view(m, hq, d)[:, :, :64] > 0)
