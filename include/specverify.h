@@ -367,6 +367,10 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * Softmax statistics and sums are fp32 (q . k too); the probabilities enter
  * the second product in 16 bits: over a 16-bit cache as bf16, over codes as
  * fp16 (2^-11 of themselves, or 2^-30 of the row's largest where that is more).
+ * Over codes, keys and values enter the products as fp16: every value that a
+ * row of the request could see must be at most 65504 in magnitude, as those
+ * that sv_kv_append writes are (a cache filled in another way may hold more,
+ * which sv_kv_read returns and this call does not support).
  * Over a 16-bit cache the weights of that sum are at most 2^-15: finite values
  * give finite outputs where |v| adds up to less than 2^142 over the tokens.  The result does not depend on timing: it is bitwise
  * reproducible for given inputs on one device.

@@ -123,3 +123,26 @@ def test_a_long_tail_behind_large_weights(lib, bits, hq):
     assert lib.device_error() == 0
     check(out, cache, bits, offs, [length], table, 64, q, hq, 0.125)
     assert torch.all(out.view(m, hq, d)[:, :, :64] > 0)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hq", [3, 8, 16, 32])
+def test_codes_at_the_top_of_fp16(lib, bits, hq):
+    """A cache that the caller filled: scales of either sign, values up to 65504 in magnitude and no further."""
+    r = np.random.default_rng(340 + hq)
+    d, m, length = 128, 3, 400
+    cache, offs, table, q, _ = attend_case(lib, r, bits, [m], [length], hq, 1, d, 64, qscale=2.0 ** -16)
+    top = 2 ** bits - 1
+    for t in cache.tensors[:2]:
+        t.copy_(torch.from_numpy(r.integers(-2 ** 31, 2 ** 31, tuple(t.shape))).to(torch.int32))
+    for s, z in (cache.tensors[2:4], cache.tensors[4:6]):
+        scale = torch.from_numpy(r.uniform(0, 65504 * 2 / top, tuple(s.shape))).to(torch.float16).double()
+        bias = (65504 - scale * top).clamp(-65504, 65504).to(torch.float16).double()
+        bias = torch.where(scale * top + bias > 65504, torch.zeros_like(bias), bias)      # (its rounding went up)
+        scale = torch.where(scale * top + bias > 65504, torch.zeros_like(scale), scale)
+        sign = torch.from_numpy(r.choice([-1.0, 1.0], tuple(s.shape)))
+        s.copy_((scale * sign).to(torch.float16))
+        z.copy_((bias * sign).to(torch.float16))
+    out = lib.tree_attention(cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq, scale=0.125)
+    assert lib.device_error() == 0 and out.isfinite().all()
+    check(out, cache, bits, offs, [length], table, 64, q, hq, 0.125)
