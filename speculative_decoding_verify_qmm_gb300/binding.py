@@ -266,6 +266,9 @@ def _refuse(what, t):
     raise SVError(SV_EINVAL, "%s, got %s %s with strides %s on %s" % (what, t.dtype, tuple(t.shape), t.stride(), t.device))
 
 
+_INT_MAX = 2 ** 31 - 1      # sizes and strides are C ints
+
+
 def _matrix(name, t, dtype, dev, rows, width):
     """Row stride of a [>= rows, >= width] matrix on device `dev` with adjacent elements; anything else is refused."""
     shape, strides = t.shape, t.stride()
@@ -582,8 +585,21 @@ class Library:
     @staticmethod
     def row_offsets(offsets):
         """Host row offsets [B + 1] as the C calls take them (lists are accepted too, at some cost a call)."""
-        return offsets if isinstance(offsets, ctypes.Array) else (ctypes.c_int32 * len(offsets))(
-            *[int(v) for v in offsets])
+        if isinstance(offsets, ctypes.Array) and offsets._type_ is ctypes.c_int32:
+            return offsets
+        values = [int(v) for v in offsets]
+        if any(abs(v) > _INT_MAX for v in values):                      # ctypes would take them modulo 2^32
+            raise SVError(SV_EINVAL, "row_offsets must be below 2^31")
+        return (ctypes.c_int32 * len(values))(*values)
+
+    def _rows_of(self, row_offsets):
+        """(row_offsets as the C calls take them, B, rows).  A call without rows ends in the binding, so its offsets are checked here."""
+        offs = self.row_offsets(row_offsets)
+        B = len(offs) - 1
+        rows = offs[B] if B >= 0 else -1
+        if rows < 0 or (rows == 0 and any(offs)):
+            raise SVError(SV_EINVAL, "row_offsets must be [B + 1] numbers that start at 0 and do not decrease")
+        return offs, B, rows
 
     @staticmethod
     def kv_cache(k, v, k_scales=None, k_biases=None, v_scales=None, v_biases=None):
@@ -671,9 +687,7 @@ class Library:
     def _kv_rows(self, call, cache, row_offsets, first, block_table, k, v, stream):
         import torch
         i32, bf16, dev, width = torch.int32, torch.bfloat16, cache.index, cache.width
-        offs = row_offsets if isinstance(row_offsets, ctypes.Array) else self.row_offsets(row_offsets)
-        B = len(offs) - 1
-        rows = offs[B]
+        offs, B, rows = self._rows_of(row_offsets)
         lens, (table, pages) = _vector("the lengths", first, i32, dev, B), _table(block_table, i32, dev, B)
         ldk, ldv = _matrix("k", k, bf16, dev, rows, width), _matrix("v", v, bf16, dev, rows, width)
         handle = self._launch_stream(stream, dev)
@@ -690,7 +704,8 @@ class Library:
         """(k, v) bf16 [rows, kv_heads * head_dim]: row i of request b from position first[b] + i."""
         if k is None or v is None:
             import torch
-            shape = (row_offsets[len(row_offsets) - 1], cache.width)
+            row_offsets, _, rows = self._rows_of(row_offsets)
+            shape = (rows, cache.width)
             k = _empty(shape, torch.bfloat16, cache.device, stream) if k is None else k
             v = _empty(shape, torch.bfloat16, cache.device, stream) if v is None else v
         self._kv_rows(self.lib.sv_kv_read, cache, row_offsets, first, block_table, k, v, stream)
@@ -706,9 +721,7 @@ class Library:
         drafted row j), None for a chain; scale defaults to head_dim ** -0.5."""
         import torch
         i32, bf16, dev, dim = torch.int32, torch.bfloat16, cache.index, cache.head_dim
-        offs = row_offsets if isinstance(row_offsets, ctypes.Array) else self.row_offsets(row_offsets)
-        B, width = len(offs) - 1, n_q_heads * dim
-        rows = offs[B]
+        (offs, B, rows), width = self._rows_of(row_offsets), n_q_heads * dim
         lens, (table, pages) = _vector("kv_len", kv_len, i32, dev, B), _table(block_table, i32, dev, B)
         mask = None if tree_mask is None else _vector("tree_mask", tree_mask, torch.int64, dev, rows)
         if out is None:
