@@ -275,7 +275,10 @@ def _matrix(name, t, dtype, dev, rows, width):
     if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] < rows or shape[1] < width \
             or (strides[1] != 1 and width > 1):
         _refuse("%s must be a %s [%d, %d] matrix on cuda:%d with unit inner stride" % (name, dtype, rows, width, dev), t)
-    return strides[0] if shape[0] > 1 else max(strides[0], width)
+    stride = strides[0] if shape[0] > 1 else min(max(strides[0], width), _INT_MAX)
+    if stride > _INT_MAX:
+        _refuse("the row stride of %s must be below 2^31" % name, t)
+    return stride
 
 
 def _vector(name, t, dtype, dev, n):
@@ -298,7 +301,7 @@ def _empty(shape, dtype, device, stream):
 def _table(t, dtype, dev, B):
     """(data pointer, width) of a block table."""
     shape = t.shape
-    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] < B or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or shape[0] < B or shape[1] > _INT_MAX or not t.is_contiguous():
         _refuse("block_table must be a contiguous %s [%d, pages] tensor on cuda:%d" % (dtype, B, dev), t)
     return t.data_ptr(), shape[1]
 

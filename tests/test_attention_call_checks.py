@@ -53,6 +53,16 @@ def test_binding_refuses_row_offsets(offs):
             call()
 
 
+def test_binding_refuses_strides_past_a_c_int():
+    import torch
+    far = torch.empty_strided((2, 128), (2 ** 32 + 128, 1), dtype=torch.bfloat16, device="meta")
+    with pytest.raises(binding.SVError, match="row stride"):
+        binding._matrix("q", far, torch.bfloat16, -1, 2, 128)
+    assert binding._matrix("q", far[:1], torch.bfloat16, -1, 1, 128) >= 128   # one row: no stride is used
+    near = torch.empty_strided((2, 128), (2 ** 31 - 8, 1), dtype=torch.bfloat16, device="meta")
+    assert binding._matrix("q", near, torch.bfloat16, -1, 2, 128) == 2 ** 31 - 8
+
+
 def test_workspace_query_of_bad_offsets_is_zero():
     build.build()
     lib = binding.load()
