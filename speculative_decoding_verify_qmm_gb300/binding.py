@@ -734,8 +734,8 @@ class Library:
         if workspace is None:
             workspace = _empty(max(256, self.tree_attention_workspace_bytes(cache, offs, n_q_heads)), torch.uint8, cache.device,
                                stream)           # freed into the same pool: the call may outlive the tensor
-        elif workspace.get_device() != dev:
-            _refuse("the workspace must be on cuda:%d" % dev, workspace)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse("the workspace must be contiguous and on cuda:%d" % dev, workspace)
         if rows or B < 1:
             status = self.lib.sv_tree_attention(cache.ref, B, offs, lens, table, pages, q.data_ptr(), ldq, n_q_heads,
                                                 dim ** -0.5 if scale is None else scale, mask, out.data_ptr(), ldo,

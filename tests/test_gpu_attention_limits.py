@@ -12,6 +12,7 @@ import numpy as np
 import pytest
 import torch
 
+from speculative_decoding_verify_qmm_gb300.binding import SVError
 from tests.test_gpu_attention import U32, attend_case, f64, i32, stored
 
 pytestmark = pytest.mark.gpu
@@ -146,3 +147,14 @@ def test_codes_at_the_top_of_fp16(lib, bits, hq):
     out = lib.tree_attention(cache, offs, i32([length]), i32(table.tolist()), q.cuda(), hq, scale=0.125)
     assert lib.device_error() == 0 and out.isfinite().all()
     check(out, cache, bits, offs, [length], table, 64, q, hq, 0.125)
+
+
+def test_a_workspace_with_gaps_is_refused(lib):
+    """The call writes adjacent bytes: between a strided tensor's elements is another's memory."""
+    r = np.random.default_rng(350)
+    cache, offs, table, q, _ = attend_case(lib, r, 16, [2], [30], 2, 1, 64, 16)
+    args = (cache, offs, i32([30]), i32(table.tolist()), q.cuda(), 2)
+    n = lib.tree_attention_workspace_bytes(cache, offs, 2)
+    with pytest.raises(SVError):
+        lib.tree_attention(*args, workspace=torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2])
+    assert torch.equal(lib.tree_attention(*args, workspace=lib.workspace(n)), lib.tree_attention(*args))
