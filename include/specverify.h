@@ -305,7 +305,8 @@ int sv_swiglu(const uint16_t* g, int ldg, const uint16_t* u, int ldu, int M, int
  * interleaved != 0; elements from rotary_dim on are not rotated.  The angle is
  * formed exactly to 2^-32 turns and reduced to one turn before its sine and
  * cosine, for any position and |inv_freq| < 2^24 (NaN from there on); the rest
- * is fp32, and each output is rounded to bf16 once.  positions int32 [rows],
+ * is fp32 (with norm, a head's sum of squares too: |x| < 2^60), and each output
+ * is rounded to bf16 once.  positions int32 [rows],
  * inv_freq fp32 [rotary_dim/2] (both may be NULL when rotary_dim == 0).
  * q_out may be q (same stride) and k_out may be k: each head is read whole
  * before it is written; other overlap is not allowed.  n_kv_heads == 0 skips

@@ -14,10 +14,11 @@
 // while the present one is worked on - and handed over in shared memory, for a
 // lookup by every thread is three dependent loads against one load of data.
 //
-// Measured (8 heads of 128): 8253 rows written as 4-bit codes 14.9 us, as 8-bit codes 14.9, as bf16 12.6 (codes are bound by
-// instructions, some 110 for 8 values; bf16 by memory, 5.4 TB/s); read back 11.7, 11.7 and 12.9; 32771 rows read from 8-bit codes
-// 35.8 us (5.7 TB/s); 32 rows 2.2 us a call.  A lookup and two divisions by each thread, and a division a value, took 41 us
-// to write and 74 for the long read.
+// Measured (8 heads of 128): 8253 rows written as 4-bit codes 14.8 us, as 8-bit codes 15.0, as bf16 12.8 (codes: 160
+// instructions a warp for 8 values a lane are 9 us of issue, the rest waits, first for the barriers of a tile; bf16 by memory, 5.3 TB/s);
+// read back 11.8 (100 instructions), 12.1 and 13.1; 32771 rows read from 8-bit codes 35.9 us (5.7 TB/s), from 4-bit codes 34.9, from
+// bf16 44.6 (6.0 TB/s); 32 rows 2.2 us a call.  A lookup and two divisions by each thread, and a division a value, took 41 us to write
+// and 74 for the long read.
 #include "sv_kv.cuh"
 
 #include <algorithm>

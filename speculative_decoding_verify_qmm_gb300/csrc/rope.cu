@@ -14,8 +14,10 @@
 // A warp is on its own: it takes some heads of one row, makes the row's sines and
 // cosines while its first loads are in flight (each lane a few frequencies, handed
 // over through the warp's piece of shared memory) and holds those of its chunk in
-// registers over all its heads.  No barrier joins warps.  Measured: 4093 rows of 56 heads of 128, 64 of them rotated, 23.3 us
-// (5.0 TB/s of the 6.8 that a copy reaches; 77 us with a CTA a row and fp64 angles); 8 rows of 40 heads 2.1 us.
+// registers over all its heads.  No barrier joins warps.  Measured: 4093 rows of 56 heads of 128, 64 of them rotated in adjacent
+// pairs, 23.5 us (5.0 TB/s of the 6.8 that a copy reaches; 77 us with a CTA a row and fp64 angles); 40 heads rotated in halves of all
+// 128 elements 22.0 us (3.8 TB/s: cosines, sines, weights and 40 values do not fit 64 registers, 120 bytes a thread are spilled); 8 rows
+// of 40 heads 2.1 us.
 //
 // Angles.  position * inv_freq reaches 1e6 radians, where one fp32 ulp is 0.06
 // rad, and fp64 is slow here.  In units of 2^-64 turns the product is one of integers,

@@ -41,8 +41,8 @@ __device__ __forceinline__ size_t kv_token(const KvCache& c, int page, int head,
   return (((size_t)page * c.heads + head) << c.page_shift) + place;
 }
 
-// Cache token index of position `pos` of request b, or -1 for bad input (a
-// position outside the table or a page outside the cache).
+// Page of position `pos` of request b, or -1 for bad input (a position outside
+// the table or a page outside the cache).
 __device__ __forceinline__ long long kv_page_of(const KvCache& c, const int32_t* table, int table_pages, int b, long long pos) {
   if (pos < 0) return -1;
   const long long pi = pos >> c.page_shift;

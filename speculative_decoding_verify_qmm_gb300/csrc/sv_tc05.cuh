@@ -93,9 +93,9 @@ __device__ __forceinline__ void tc05_commit(uint64_t* bar) {
 // of 16 advances the start address by 2048 bytes.
 
 // Instruction descriptor of kind::f16 for fp16 or bf16 operands (both the same type: formats 0 or 1), fp32
-// accumulators; a_mn, b_mn: the operand is MN-major (bits 15, 16).
-__host__ __device__ constexpr uint32_t f16_idesc_ex(int M, int N, bool bf16, bool a_mn, bool b_mn) {
-  return f16_idesc(M, N) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+// accumulators; b_mn: operand B is MN-major (bit 16).
+__host__ __device__ constexpr uint32_t f16_idesc_ex(int M, int N, bool bf16, bool b_mn) {
+  return f16_idesc(M, N) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
 // 32 consecutive columns of this thread's lane, loaded and waited for.

@@ -9,8 +9,9 @@
 namespace sv {
 
 // Up to 32 rows a key head the warp-level kernel, above the tensor-memory one.  48 rows (4 requests of 8 rows in 48 heads, 30001
-// tokens, 8-bit): 109 us against 57.  32 rows (8 rows, 32 heads, 8-bit): 16.4 us against 24.4 at 8192 tokens, 22.7 against 22.6 at
-// 16384, 59 against 46 at 65536.  Lengths are on the device, so the better one for short contexts has them all.
+// tokens, 8-bit): 113 us against 54.  32 rows (8 rows, 32 heads, 8-bit): 14.9 us against 15.2 at 2048 tokens, 16.3 against 23.0 at 8192,
+// 23.2 against 21.4 at 16384, 52 against 43 at 65536; 20 rows, 4-bit and bf16 caches alike (bf16: 17.7 and 21.8 at 8192, 54 and 52 at
+// 65536).  Lengths are on the device, so the better one for short contexts has them all.
 constexpr int TA_MAX_BLOCK = 128, TA_NARROW_ROWS = 32;
 
 // Joins the partial sums of items that spanned CTAs, in CTA order.  WPP warps per (row, query head) take every WPP-th part,
@@ -235,8 +236,8 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
   }
   const bool narrow = rows <= TA_NARROW_ROWS;
   // In fifths of the time of a narrow unit of 32-row blocks with one row tile filled: two tiles filled take 7, a block of 16
-  // rows takes 4.  (One request of 32 rows over 16384 tokens: 22.7 us in a block of 32, 25.4 in two of 16; 48 requests of 4 to 20
-  // rows: 192.6 in blocks of 32, 165.5 in blocks of 16.)
+  // rows takes 4.  (One request of 32 rows over 16384 tokens: 23.3 us in a block of 32, 23.8 in two of 16, over 65536 52 and 61; 48
+  // requests of 4 to 20 rows: 191 in blocks of 32, 158 in blocks of 16.)
   p.block = narrow ? (by16 < by32 ? 16 : 32) : TA_MAX_BLOCK;
   // Beginning an item, in the same measure: what gave the least time over several batches and lengths.  (Wide, bf16, 32 rows of
   // 65536 tokens: 60.8 us with 30, 59.0 with 60; 4 x 8 rows in 48 heads 68.0 and 64.2, over codes 54.8 and 56.1.  Narrow, 8-bit,

@@ -2,8 +2,8 @@
 //
 //   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q . k_t - max)
 //
-// Bound by instructions over codes (some 470 a warp for 16 tokens and 16 rows, half of them codes to fp16), by memory over
-// 16-bit caches, by latency for short contexts: a cached byte meets 16 to 64 multiply-adds, far below what warp-level MMA
+// Bound by instructions over codes in blocks of 16 rows (some 470 a warp for 16 tokens, half of them codes to fp16; issue in 63 % of
+// cycles), by latency in blocks of 32 (two warps to a scheduler, issue in 34 %) and for short contexts: a cached byte meets 16 to 64 multiply-adds, far below what warp-level MMA
 // gives.  A warp owns every W-th step of 16 tokens of the CTA's run, with its own ring of cp.async stages in shared memory, its
 // own running maximum, weight and sums in registers, and no barrier of the CTA until the run ends, where the warps' sums are
 // joined in warp order.
@@ -13,7 +13,7 @@
 // four to a scheduler.  Two row tiles: 8 warps, and a warp takes two steps at once where it can, so that two chains overlap.
 // (Teams for two row tiles spill: 207 us against 193; 16 warps without teams join in two rounds: 11.6 us for one row against 10.1.)
 //
-// Measured (32 query and 8 key heads of 128): one row over 2048 tokens, 8-bit, 9.4 us; 8 rows over 16384 tokens, 8-bit, 23.3 us
+// Measured (32 query and 8 key heads of 128): one row over 2048 tokens, 8-bit, 9.5 us; 8 rows over 16384 tokens, 8-bit, 23.2 us
 // (1.5 TB/s); 48 requests of 1 to 5 rows, up to 12007 tokens, 4-bit, 158 us (2.6 TB/s of the 6.8 that a copy reaches).
 //
 // Codes become MMA operands in registers, without a second trip through shared memory.  S = Q K^T: the contraction may run

@@ -19,9 +19,9 @@
 // fp16 step), and Q enters as fp16 scaled by a power of two per row, exact for every bf16 value within 2^29 of the
 // row's largest.
 //
-// Measured (8 key heads of 128): a 32-node tree in 32 heads over 65536 tokens, bf16, 60.9 us (4.4 TB/s; 46 us while tiles run, at
+// Measured (8 key heads of 128): a 32-node tree in 32 heads over 65536 tokens, bf16, 60.3 us (4.5 TB/s; 46 us while tiles run, at
 // the copy rate, the rest is the start, the exchange at the end and the join); 4 x 8 rows in 48 heads over up to 30001
-// tokens, 8-bit, 54.6 us (3.4 TB/s).  Over codes the softmax warps set the pace, some 2500 cycles a tile beside the transforming
+// tokens, 8-bit, 54.4 us (3.4 TB/s).  Over codes the softmax warps set the pace, some 2500 cycles a tile beside the transforming
 // warps, whose issue slots they share.
 //
 // Over codes, copies to shared memory ahead of the transformation were slower than loads straight to registers: 24 bulk copies a
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       TaRing<Sh::OPS> ring;
       uint32_t n_q = 0, n_s = 0, n_p = 0;               // phases seen of each barrier
       bool ok = true;
-      constexpr uint32_t ID_S = f16_idesc_ex(TA_ROWS, TA_TILE, RAW16, false, false);
-      constexpr uint32_t ID_O = f16_idesc_ex(TA_ROWS, D, RAW16, false, true);
+      constexpr uint32_t ID_S = f16_idesc_ex(TA_ROWS, TA_TILE, RAW16, false);
+      constexpr uint32_t ID_O = f16_idesc_ex(TA_ROWS, D, RAW16, true);
       const bool issuer = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t ops0 = (__shfl_sync(0xffffffffu, smem_u32(ops), 0) & 0x3FFFFu) >> 4;
