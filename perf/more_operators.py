@@ -352,7 +352,7 @@ def _prepare_round(case, gen, seed):
         s["layers"] = _handles(s["parts"])
         s["pages"] = lib.kv_pages(s["refs"], s["table"], s["held"], page)
         s["workspace"] = lib.workspace(lib.kv_reserve_workspace_bytes(s["pages"]))
-        s["counts"], s["copies"] = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty((slots, 2), dtype=torch.int32, device="cuda")
+        s["counts"], s["copies"] = torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty((slots, 3), dtype=torch.int32, device="cuda")
     return s
 
 
