@@ -240,6 +240,54 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
                              const int32_t* draft, int V, float temperature, const float* u, int top_k, float top_p,
                              int32_t* out_len, int32_t* out_tokens, void* workspace, size_t workspace_bytes,
                              void* stream);
+/* Accept step of draft trees (as sv_tree_attention verifies and sv_kv_commit
+ * moves them up; the pages state the rule for a chain, which a tree's
+ * nodes apply child after child).  Request b owns rows row_offsets[b] ..
+ * row_offsets[b+1] - 1 (1 .. 64 of them; HOST int32 [B+1], 1 <= B <= 256) of
+ * logits, parent, token, q and u; its row 0 is the anchor, row i > 0 is a
+ * draft token[i] whose parent is row parent[i] < i of the same request (parent
+ * and token of the anchor are not read).  The children of a node are its rows in
+ * ascending order.  From the anchor on, at node v:
+ * T == 0: t = argmax(logits[v]); the first child with token t is next.
+ * T > 0, q given: p = softmax(logits[v] / T) and the draft's distribution q[v]
+ *   (fp32 [rows, V], stride ldq; rows of nodes without children are not read).
+ *   With r_1 = p, child j (token x) is accepted, and next, iff
+ *   u[child] * q_j(x) < r_j(x); otherwise r_{j+1} = max(0, r_j - q_j) / its sum.
+ *   distinct == 0: the children were drawn independently, q_j = q.
+ *   distinct != 0: drawn without replacement, q_j = q without the tokens tried
+ *   at this node, divided by the mass left (1 - their q, at least 2^-24); a child
+ *   with a token tried there before is passed over.
+ *   If no child is accepted the last token is the first k whose cumulative r
+ *   (index order) exceeds u[anchor] times its sum (a residual of zero mass
+ *   falls back to p).  A chain gets sv_spec_accept's rule, draft i's uniform
+ *   being u[i] here and u[i-1] there, the draw's u[0] here and u[m] there.
+ * T > 0, q NULL: t is drawn from p in the same way with u[v]; the first child
+ *   with token t is next (drafts without a distribution: the output is an exact
+ *   sample all the same).
+ * The walk ends where there is no next node, or after max_path nodes (the
+ * children of the last are not tried).  top_k / top_p truncate p as in
+ * sv_spec_accept_truncated.
+ *   out_len int32 [B]: the path's nodes, anchor included, which is also the
+ *     number of tokens; out_tokens int32 [rows]: from row_offsets[b] on the
+ *     accepted drafts and the last token; path int32 [B, max_path]: the path's
+ *     rows (0 first), as sv_kv_commit takes it with out_len as path_len.  Entries
+ *     behind these are untouched.  1 <= max_path <= 64.
+ *   row_max, row_sumexp, row_argmax: the lm_head row outputs, all given or all
+ *     NULL (then the call finds what it needs of the rows it visits).
+ *   u fp32 [rows] in [0, 1), may be NULL when T == 0.  2 <= V <= 2^22.
+ * Tests are taken in fp64.  Residuals and draws count a weight exp((z - max) / T) in
+ * integer units of 2^-40 (a token below half of that is never drawn): sums are exact and
+ * the result does not depend on timing.  Logits of -inf have probability 0.
+ * A parent or token out of range is bad input: that request gets out_len 0
+ * and nothing else, and sv_device_error() reports it.
+ * Workspace: sv_tree_accept_workspace_bytes(rows), 256-byte aligned, used (and
+ * written) only where top_k or top_p truncate, NULL otherwise allowed; it need not be zero. */
+size_t sv_tree_accept_workspace_bytes(int rows);
+int sv_tree_accept(int B, const int32_t* row_offsets, const float* logits, int ldl, const float* row_max,
+                   const float* row_sumexp, const int32_t* row_argmax, const int32_t* parent, const int32_t* token,
+                   const float* q, int ldq, int distinct, int V, float temperature, const float* u, int top_k, float top_p,
+                   int32_t* out_len, int32_t* out_tokens, int32_t* path, int max_path, void* workspace,
+                   size_t workspace_bytes, void* stream);
 /* The same truncation rule on probability rows (the draft side): each row of
  * probs fp32 [rows, V] (stride ldp) is ordered by value (ties to the lower
  * index), truncated by top_k / top_p and renormalised into out (stride ldo;
@@ -415,6 +463,85 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
                       void* stream);
 int sv_kv_commit(const sv_kv_cache* layers, int n_layers, int B, const int32_t* kv_len, const int32_t* block_table,
                  int table_pages, const int32_t* path, int max_path, const int32_t* path_len, void* stream);
+
+/* ------------------------------------------------------ pages of the cache ---
+ * Who has which page of a paged cache (wiki page, "Architecture": the target
+ * keeps its cache over rounds and rolls it back; PyPI page, "Prefix caching":
+ * conversations that begin alike share what they have in common).  One
+ * numbering of the pages serves every layer's cache.  All arrays are DEVICE
+ * arrays that the calls read and write on the stream, so a captured round
+ * replays as the state changes:
+ *   refs        int32 [n_pages]: the table entries that name a page; 0 = free
+ *   block_table int32 [slots, table_pages]: as the attention calls take it, a
+ *               slot being a request of the batch
+ *   held        int32 [slots]: a slot has the entries 0 .. held - 1 of its row
+ * Entries of block_table from held on are neither read nor written, but for
+ * those a call adds.  A fresh state is all zeros.  Results follow from the
+ * inputs alone, whatever the order in which threads run.
+ *
+ * sv_kv_fork: for each f of 0 .. n - 1, slot child[f] (empty: held == 0) gets
+ * the first ceil(tokens[f] / page_size) pages of slot parent[f], shared: no
+ * cache is touched.  parent, child, tokens int32 [n], DEVICE, n <= 256; a
+ * parent may be named many times.  Bad input (reported by sv_device_error(),
+ * nothing is done for that f): a slot outside [0, slots), a child that is not
+ * empty, that an earlier f names too, or that is a parent of this call, more
+ * tokens than the parent's pages hold, a page outside [0, n_pages).
+ *
+ * sv_kv_reserve: slot s keeps its first keep[s] tokens and gets room for
+ * need[s]: afterwards held[s] = ceil(need[s] / page_size), and what lies from
+ * token keep[s] on is its alone (refs == 1).  Pages it has to itself stay; a
+ * page that lies behind the kept tokens and is shared is given up for a fresh
+ * one; the half-filled page that holds token keep[s] - 1, if it is shared, is
+ * replaced by a fresh copy of its first keep[s] % page_size places, in all of
+ * n_layers caches (0 .. 1024; 0: bookkeeping alone, the caller copies) - but
+ * where every entry that names it belongs to such a slot of this call, the lowest
+ * of these slots keeps it.  Pages from held[s] on are given back.  So
+ *   grow before a round:  keep = kv_len, need = kv_len + drafted rows
+ *   trim after it:        keep = need = the new kv_len
+ *   free a request:       keep = need = 0
+ *   leave a slot alone:   need < 0
+ * Fresh pages are the lowest that are free before the call, in slot and entry
+ * order.  If there are too few, nothing is changed.  counts int32 [3], DEVICE:
+ * pages that were missing (0: done), copies made, fresh pages.  copies int32
+ * [slots, 3], DEVICE: the first counts[1] rows are (from, to, places), in slot
+ * order; later rows are untouched.  Bad input (the slot is left alone): keep
+ * outside [0, min(need, held * page_size)], need beyond the table, a page
+ * outside [0, n_pages).
+ * Workspace: sv_kv_reserve_workspace_bytes(pages) (0 for a bad argument),
+ * 256-byte aligned; it need not be zero, and what the call wrote is zero again after it.
+ *
+ * sv_kv_compact: the pages in use become 0 .. live - 1: those from live on move
+ * to the free ones below, both in ascending order, in all of n_layers caches
+ * (0 .. 1024) with their refs, and the slots' entries are renumbered.  counts
+ * int32 [2], DEVICE: live, pages moved.  moves int32 [n_pages, 2], DEVICE: the
+ * first counts[1] rows are (from, to).  An entry that names no page in use is
+ * bad input and left as it is.
+ *
+ * sv_kv_copy_pages: page src[i] of cache from[l] to page dst[i] of to[l], codes,
+ * scales and biases as they are, for i < n <= 2^24 and each of n_layers
+ * (1 .. 1024) pairs of caches, alike in all but n_pages.  to may be from.  A
+ * source may be named many times; a page that is named twice as dst, or as
+ * dst and as src of one cache, ends up with either content, or parts of both.
+ * An index out of range is bad input: that copy is not made.
+ * In all of these no cache may be listed twice, nor one layer's source be another
+ * layer's destination. */
+typedef struct {
+  int32_t* refs;
+  int32_t* block_table;
+  int32_t* held;
+  int n_pages, page_size, slots, table_pages;
+} sv_kv_pages;
+
+int sv_kv_fork(const sv_kv_pages* pages, int n, const int32_t* parent, const int32_t* child, const int32_t* tokens,
+               void* stream);
+size_t sv_kv_reserve_workspace_bytes(const sv_kv_pages* pages);
+int sv_kv_reserve(const sv_kv_pages* pages, const sv_kv_cache* layers, int n_layers, const int32_t* keep,
+                  const int32_t* need, int32_t* counts, int32_t* copies, void* workspace, size_t workspace_bytes,
+                  void* stream);
+int sv_kv_compact(const sv_kv_pages* pages, const sv_kv_cache* layers, int n_layers, int32_t* counts, int32_t* moves,
+                  void* stream);
+int sv_kv_copy_pages(const sv_kv_cache* from, const sv_kv_cache* to, int n_layers, int n, const int32_t* src,
+                     const int32_t* dst, void* stream);
 
 /* --------------------------------------------------------- verify round ---
  * One whole verify round of a dense target whose every linear layer is

@@ -76,6 +76,25 @@ class KVLayers:
         self.array = (KVCacheView * len(self.caches))(*[c.view for c in self.caches])
         self.device, self.index = self.caches[0].device, self.caches[0].index
 
+
+class KVPagesView(ctypes.Structure):
+    """sv_kv_pages."""
+    _fields_ = [("refs", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("slots", ctypes.c_int), ("table_pages", ctypes.c_int)]
+
+
+_c_pages_p = ctypes.POINTER(KVPagesView)
+
+
+class KVPages:
+    """Who has which page: the state's tensors (kept alive here) and the sv_kv_pages over them."""
+
+    def __init__(self, view, refs, block_table, held):
+        self.view, self.ref = view, ctypes.byref(view)
+        self.refs, self.block_table, self.held = refs, block_table, held
+        self.device, self.index, self.slots = refs.device, refs.get_device(), view.slots
+
+
 SV_CAP_MAX = 31
 
 
@@ -158,6 +177,16 @@ _SIGNATURES = {
                                    _c_float, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "sv_kv_commit": (_c_int, [_c_kv_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
                               _c_void_p]),
+    "sv_tree_accept_workspace_bytes": (_c_size_t, [_c_int]),
+    "sv_tree_accept": (_c_int, [_c_int, _c_i32_p, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                _c_void_p, _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_int, _c_float, _c_void_p, _c_void_p,
+                                _c_void_p, _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    "sv_kv_fork": (_c_int, [_c_pages_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "sv_kv_reserve_workspace_bytes": (_c_size_t, [_c_pages_p]),
+    "sv_kv_reserve": (_c_int, [_c_pages_p, _c_kv_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
+                               _c_void_p]),
+    "sv_kv_compact": (_c_int, [_c_pages_p, _c_kv_p, _c_int, _c_void_p, _c_void_p, _c_void_p]),
+    "sv_kv_copy_pages": (_c_int, [_c_kv_p, _c_kv_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p]),
     "sv_expected_committed": (ctypes.c_double, [ctypes.c_double, _c_int]),
     "sv_best_cap": (_c_int, [ctypes.c_double, _c_int, _c_f64_p, _c_f64_p, ctypes.c_double, _c_int_p, _c_f64_p]),
     "sv_verify_knee": (_c_int, [_c_f64_p, _c_int, ctypes.c_double, _c_int_p]),
@@ -526,6 +555,52 @@ class Library:
             workspace.numel() * workspace.element_size(), _stream(stream)))
         return out_len, out_tokens
 
+    def tree_accept_workspace_bytes(self, rows):
+        return self.lib.sv_tree_accept_workspace_bytes(rows)
+
+    def tree_accept(self, row_offsets, logits, parent, tokens, temperature, q=None, u=None, distinct=False, top_k=0, top_p=1.0,
+                    stats=None, out=None, max_path=None, workspace=None, stream=None):
+        """(out_len [B], out_tokens [rows], path [B, max_path]).  Row i > 0 of a request drafts tokens[i] below its row parent[i];
+        q [rows, V]: the distributions that each node's children were drawn from (None: drafts without one), distinct: without
+        replacement; stats: (row_max, row_sumexp, row_argmax) of the head, or None; out: the three outputs to write to
+        (entries behind a request's results are left as they are; fresh outputs hold -1 there)."""
+        import torch
+        f32, i32 = torch.float32, torch.int32
+        offs, B, rows = self._rows_of(row_offsets)
+        dev, V = logits.get_device(), logits.shape[-1]
+        handle = self._launch_stream(stream, dev)
+        ldl, ldq = _matrix("logits", logits, f32, dev, rows, V), 0
+        if q is not None:
+            ldq = _matrix("q", q, f32, dev, rows, V)
+        if out is None:
+            max_path = max([1] + [offs[b + 1] - offs[b] for b in range(B)]) if max_path is None else max_path
+            out = [_empty(shape, i32, logits.device, stream) for shape in ((B,), (rows,), (B, max_path))]
+            for t in out:
+                if stream is None:
+                    t.fill_(-1)
+                else:
+                    with torch.cuda.stream(stream):
+                        t.fill_(-1)
+        out_len, out_tokens, path = out
+        if path.dim() != 2 or path.shape[0] < B or (max_path is not None and path.shape[1] != max_path):
+            _refuse("path must be an int32 [%d, max_path] tensor" % B, path)
+        ptrs = [None if t is None else _vector(name, t, dtype, dev, rows) for name, t, dtype in (
+            ("row_max", None if stats is None else stats[0], f32), ("row_sumexp", None if stats is None else stats[1], f32),
+            ("row_argmax", None if stats is None else stats[2], i32), ("parent", parent, i32), ("tokens", tokens, i32))]
+        up = None if u is None else _vector("u", u, f32, dev, rows)
+        outs = [_vector("out_len", out_len, i32, dev, B), _vector("out_tokens", out_tokens, i32, dev, rows),
+                _vector("path", path, i32, dev, 0)]
+        size, ws = 0, None
+        if temperature > 0 and (0 < top_k < V or top_p < 1):
+            ws, size = self._workspace(workspace, lambda: self.tree_accept_workspace_bytes(rows), logits.device, dev, stream)
+            ws = ws.data_ptr()
+        status = self.lib.sv_tree_accept(B, offs, logits.data_ptr(), ldl, *ptrs, None if q is None else q.data_ptr(), ldq,
+                                         bool(distinct), V, float(temperature), up, int(top_k), float(top_p), *outs,
+                                         path.shape[1], ws, size, handle)
+        if status:
+            self.check(status)
+        return out_len, out_tokens, path
+
     def truncate_probs(self, probs, top_k, top_p, out=None, stream=None):
         import torch
         if out is None:
@@ -758,6 +833,97 @@ class Library:
                                        _vector("path_len", path_len, i32, dev, B), self._launch_stream(stream, dev))
         if status:
             self.check(status)
+
+    # ------------------------------------------------------------ cache pages
+    @staticmethod
+    def kv_pages(refs, block_table, held, page_size):
+        """A KVPages over int32 device tensors: refs [pages], block_table [slots, n], held [slots]."""
+        import torch
+        if refs.device.type != "cuda" or block_table.dim() != 2 or refs.dim() != 1 or held.dim() != 1 or held.numel() != block_table.shape[0]:
+            raise SVError(SV_EINVAL, "refs must be a CUDA vector, block_table [slots, n] and held [slots]")
+        for t in (refs, block_table, held):
+            if t.dtype is not torch.int32 or t.device != refs.device or not t.is_contiguous():
+                _refuse("refs, block_table and held must be contiguous int32 tensors on one device", t)
+        sizes = (refs.numel(), int(page_size), *block_table.shape)
+        if any(abs(n) > _INT_MAX for n in sizes):
+            raise SVError(SV_EINVAL, "sizes must be below 2^31")
+        view = KVPagesView(refs.data_ptr(), block_table.data_ptr(), held.data_ptr(), *sizes)
+        return KVPages(view, refs, block_table, held)
+
+    def kv_pages_alloc(self, n_pages, page_size, slots, table_pages, device="cuda"):
+        """A fresh state: every page free, every slot empty."""
+        import torch
+        zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        return self.kv_pages(zeros(n_pages), zeros(slots, table_pages), zeros(slots), page_size)
+
+    def kv_fork(self, pages, parent, child, tokens, stream=None):
+        """Slot child[f] gets the pages of slot parent[f]'s first tokens[f] tokens, shared (int32 device tensors)."""
+        import torch
+        i32, dev, n = torch.int32, pages.index, parent.numel()
+        if child.numel() != n or tokens.numel() != n:
+            raise SVError(SV_EINVAL, "parent, child and tokens must have one length")
+        ptrs = [_vector(name, t, i32, dev, n) for name, t in (("parent", parent), ("child", child), ("tokens", tokens))]
+        self.check(self.lib.sv_kv_fork(pages.ref, n, *ptrs, self._launch_stream(stream, dev)))
+
+    def kv_reserve_workspace_bytes(self, pages):
+        return self.lib.sv_kv_reserve_workspace_bytes(pages.ref)
+
+    def _page_layers(self, caches, dev):
+        """(array, number) of the layers' caches; none for bookkeeping alone."""
+        if caches is None:
+            return None, 0, None
+        layers = caches if isinstance(caches, KVLayers) else KVLayers(caches)
+        if layers.index != dev:
+            raise SVError(SV_EINVAL, "the caches must be on cuda:%d" % dev)
+        return layers.array, len(layers.array), layers
+
+    def kv_reserve(self, pages, caches, keep, need, counts=None, copies=None, workspace=None, stream=None):
+        """(counts, copies).  Slot s keeps keep[s] tokens and gets room for need[s] (need < 0: left alone), what it will
+        write being its alone; caches: every layer's (a list of KVCache, kv_layers() of one, or None).  counts [3]: pages
+        missing (0: done), copies, fresh pages; copies [slots, 3]: (from, to, places)."""
+        import torch
+        i32, dev, slots = torch.int32, pages.index, pages.slots
+        array, n, _layers = self._page_layers(caches, dev)
+        handle = self._launch_stream(stream, dev)
+        counts = _empty((3,), i32, pages.device, stream) if counts is None else counts
+        copies = _empty((slots, 3), i32, pages.device, stream) if copies is None else copies
+        ptrs = [_vector(name, t, i32, dev, size) for name, t, size in (("keep", keep, slots), ("need", need, slots),
+                                                                       ("counts", counts, 3), ("copies", copies, 3 * slots))]
+        workspace, size = self._workspace(workspace, lambda: self.kv_reserve_workspace_bytes(pages), pages.device, dev, stream)
+        self.check(self.lib.sv_kv_reserve(pages.ref, array, n, *ptrs, workspace.data_ptr(), size, handle))
+        return counts, copies
+
+    def kv_compact(self, pages, caches, counts=None, moves=None, stream=None):
+        """(counts, moves).  The pages in use move to the front; counts [2]: pages in use, pages moved; moves [n_pages, 2]."""
+        import torch
+        i32, dev, n_pages = torch.int32, pages.index, pages.view.n_pages
+        array, n, _layers = self._page_layers(caches, dev)
+        handle = self._launch_stream(stream, dev)
+        counts = _empty((2,), i32, pages.device, stream) if counts is None else counts
+        moves = _empty((n_pages, 2), i32, pages.device, stream) if moves is None else moves
+        self.check(self.lib.sv_kv_compact(pages.ref, array, n, _vector("counts", counts, i32, dev, 2),
+                                          _vector("moves", moves, i32, dev, 2 * n_pages), handle))
+        return counts, moves
+
+    def kv_copy_pages(self, caches, src, dst, to=None, stream=None):
+        """Page src[i] of each cache to page dst[i] of the same layer's cache in `to` (the same caches by default)."""
+        import torch
+        array, n, layers = self._page_layers(caches, src.get_device())
+        array_to, n_to, _to = (array, n, layers) if to is None else self._page_layers(to, src.get_device())
+        if n_to != n or dst.numel() != src.numel():
+            raise SVError(SV_EINVAL, "as many caches to copy to as from, and as many destinations as sources")
+        dev = layers.index if layers is not None else src.get_device()
+        ptrs = [_vector(name, t, torch.int32, dev, t.numel()) for name, t in (("src", src), ("dst", dst))]
+        self.check(self.lib.sv_kv_copy_pages(array, array_to, n, src.numel(), *ptrs, self._launch_stream(stream, dev)))
+
+    def _workspace(self, workspace, nbytes, device, dev, stream):
+        """(the caller's workspace, checked, or a fresh one; its bytes)."""
+        import torch
+        if workspace is None:                     # freed into the pool of the stream that uses it: the call may outlive the tensor
+            workspace = _empty(max(256, nbytes()), torch.uint8, device, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse("the workspace must be contiguous and on cuda:%d" % dev, workspace)
+        return workspace, workspace.numel() * workspace.element_size()
 
     def residual_add(self, h, t, stream=None):
         self.check(self.lib.sv_residual_add(_ptr(h), h.stride(0), _ptr(t), t.stride(0), h.shape[0], h.shape[1],
