@@ -464,6 +464,33 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
 int sv_kv_commit(const sv_kv_cache* layers, int n_layers, int B, const int32_t* kv_len, const int32_t* block_table,
                  int table_pages, const int32_t* path, int max_path, const int32_t* path_len, void* stream);
 
+/* Tree attention of a batch whose requests share prefixes (PyPI page, "Prefix
+ * caching": conversations that begin alike share what they have in common; here
+ * the whole batch meets those tokens at once).  As sv_tree_attention, with
+ * the batch in G groups: group g is requests group_offsets[g] ..
+ * group_offsets[g+1] - 1 (HOST int32 [G+1] from 0 to B, 1 <= G <= 256, empty
+ * groups allowed), and the first shared_pages[g] (HOST int32 [G], 0 .. table_pages)
+ * entries of all its requests' table rows name the same pages, or pages that
+ * hold the same (which request's entries are read is not specified).  Every
+ * request of the group with rows has kv_len >= shared_pages * page_size: the shared
+ * tokens are committed and visible to all its rows.  A smaller kv_len is bad
+ * input: that request's output is undefined.  A group of one request, or
+ * without shared pages, is the plain case, and no groups are ever mixed.
+ * The formulas, formats and rules of sv_tree_attention hold; sums run in another
+ * order.  Prefix tokens are read once per 256 rows (drafted rows of the whole group
+ * times query heads per key head).  A captured call keeps the groups and shared_pages it
+ * was given; lengths, tables and pages are read when it runs.
+ * Workspace: sv_tree_attention_shared_workspace_bytes (0 for a bad argument; it
+ * grows with the rows), same rules as sv_tree_attention's. */
+size_t sv_tree_attention_shared_workspace_bytes(const sv_kv_cache* cache, int G, const int32_t* group_offsets,
+                                                const int32_t* shared_pages, int B, const int32_t* row_offsets,
+                                                int n_q_heads);
+int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* group_offsets, const int32_t* shared_pages,
+                             int B, const int32_t* row_offsets, const int32_t* kv_len, const int32_t* block_table,
+                             int table_pages, const uint16_t* q, int ldq, int n_q_heads, float scale,
+                             const uint64_t* tree_mask, uint16_t* out, int ldo, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 /* ------------------------------------------------------ pages of the cache ---
  * Who has which page of a paged cache (wiki page, "Architecture": the target
  * keeps its cache over rounds and rolls it back; PyPI page, "Prefix caching":

@@ -77,6 +77,13 @@ class KVLayers:
         self.device, self.index = self.caches[0].device, self.caches[0].index
 
 
+class PrefixGroups:
+    """Groups of a batch's requests and the pages that each shares, as host arrays."""
+
+    def __init__(self, offsets, pages):
+        self.offsets, self.pages, self.n = offsets, pages, len(pages)
+
+
 class KVPagesView(ctypes.Structure):
     """sv_kv_pages."""
     _fields_ = [("refs", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
@@ -177,6 +184,10 @@ _SIGNATURES = {
                                    _c_float, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "sv_kv_commit": (_c_int, [_c_kv_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
                               _c_void_p]),
+    "sv_tree_attention_shared_workspace_bytes": (_c_size_t, [_c_kv_p, _c_int, _c_i32_p, _c_i32_p, _c_int, _c_i32_p, _c_int]),
+    "sv_tree_attention_shared": (_c_int, [_c_kv_p, _c_int, _c_i32_p, _c_i32_p, _c_int, _c_i32_p, _c_void_p, _c_void_p, _c_int,
+                                          _c_void_p, _c_int, _c_int, _c_float, _c_void_p, _c_void_p, _c_int, _c_void_p,
+                                          _c_size_t, _c_void_p]),
     "sv_tree_accept_workspace_bytes": (_c_size_t, [_c_int]),
     "sv_tree_accept": (_c_int, [_c_int, _c_i32_p, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                 _c_void_p, _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_int, _c_float, _c_void_p, _c_void_p,
@@ -815,6 +826,41 @@ class Library:
             status = self.lib.sv_tree_attention(cache.ref, B, offs, lens, table, pages, q.data_ptr(), ldq, n_q_heads,
                                                 dim ** -0.5 if scale is None else scale, mask, out.data_ptr(), ldo,
                                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+            if status:
+                self.check(status)
+        return out
+
+    @staticmethod
+    def prefix_groups(offsets, pages):
+        """Group g is requests offsets[g] .. offsets[g + 1] - 1, whose first pages[g] table entries name the same pages."""
+        ints = [int(v) for v in offsets], [int(v) for v in pages]
+        if len(ints[0]) != len(ints[1]) + 1 or any(abs(v) > _INT_MAX for v in ints[0] + ints[1]):
+            raise SVError(SV_EINVAL, "groups need [G + 1] offsets and [G] page counts below 2^31")
+        return PrefixGroups(*[(ctypes.c_int32 * len(v))(*v) for v in ints])
+
+    def tree_attention_shared_workspace_bytes(self, cache, groups, row_offsets, n_q_heads):
+        offs = self.row_offsets(row_offsets)
+        return self.lib.sv_tree_attention_shared_workspace_bytes(cache.ref, groups.n, groups.offsets, groups.pages, len(offs) - 1, offs,
+                                                                 n_q_heads)
+
+    def tree_attention_shared(self, cache, groups, row_offsets, kv_len, block_table, q, n_q_heads, scale=None, tree_mask=None, out=None,
+                              workspace=None, stream=None):
+        """tree_attention of a batch whose requests share prefixes; groups: prefix_groups()."""
+        import torch
+        i32, bf16, dev, dim = torch.int32, torch.bfloat16, cache.index, cache.head_dim
+        (offs, B, rows), width = self._rows_of(row_offsets), n_q_heads * dim
+        lens, (table, pages) = _vector("kv_len", kv_len, i32, dev, B), _table(block_table, i32, dev, B)
+        mask = None if tree_mask is None else _vector("tree_mask", tree_mask, torch.int64, dev, rows)
+        if out is None:
+            out = _empty((q.shape[0], width), bf16, cache.device, stream)
+        ldq, ldo = _matrix("q", q, bf16, dev, rows, width), _matrix("out", out, bf16, dev, rows, width)
+        handle = self._launch_stream(stream, dev)
+        workspace, size = self._workspace(workspace, lambda: self.tree_attention_shared_workspace_bytes(cache, groups, offs, n_q_heads),
+                                          cache.device, dev, stream)
+        if rows or B < 1:
+            status = self.lib.sv_tree_attention_shared(cache.ref, groups.n, groups.offsets, groups.pages, B, offs, lens, table, pages,
+                                                       q.data_ptr(), ldq, n_q_heads, dim ** -0.5 if scale is None else scale, mask,
+                                                       out.data_ptr(), ldo, workspace.data_ptr(), size, handle)
             if status:
                 self.check(status)
         return out

@@ -152,13 +152,99 @@ static int check_heads(const KvCache& c, int n_q_heads) {
   return SV_OK;
 }
 
+int ta_check_batch(const sv_kv_cache* cache, int B, const int32_t* row_offsets, int n_q_heads, KvCache* c, RowMap* m) {
+  int st = check_cache(cache, c);
+  if (!st) st = check_rows_map(B, row_offsets, KV_MAX_DRAFT, 1 << 22, m);
+  return st ? st : check_heads(*c, n_q_heads);
+}
+
 // One CTA per SM (152 where no device is present: sizes only).
-static int ta_sms() {
+int ta_sms() {
   const int n = device_sm_count();
   return n > 0 ? n : 152;
 }
 static size_t ta_partial_bytes(int grid, int dim) { return (size_t)2 * grid * TA_MAX_BLOCK * dim * sizeof(float); }
 static size_t ta_stats_bytes(int grid) { return (size_t)4 * grid * TA_MAX_BLOCK * sizeof(float); }
+size_t ta_workspace_bytes(const KvCache& c) { return ta_partial_bytes(ta_sms(), c.dim) + ta_stats_bytes(ta_sms()); }
+
+bool ta_choose_block(const RowMap& map, int group, int* block) {
+  int rows = 0;                // of the widest request, times the group
+  long long by16 = 0, by32 = 0;
+  for (int b = 0; b < map.B; ++b) {
+    const int m = map.offs[b + 1] - map.offs[b];
+    if (m * group > rows) rows = m * group;
+    by16 += 4 * ta_blocks(m * group, 16);
+    by32 += m ? (m * group > 16 ? 7 : 5) : 0;
+  }
+  const bool narrow = rows <= TA_NARROW_ROWS;
+  // In fifths of the time of a narrow unit of 32-row blocks with one row tile filled: two tiles filled take 7, a block of 16
+  // rows takes 4.  (One request of 32 rows over 16384 tokens: 23.3 us in a block of 32, 23.8 in two of 16, over 65536 52 and 61; 48
+  // requests of 4 to 20 rows: 191 in blocks of 32, 158 in blocks of 16.)
+  *block = narrow ? (by16 < by32 ? 16 : 32) : TA_MAX_BLOCK;
+  return narrow;
+}
+
+int ta_check_call(TreeAttnParams* out, const int32_t* kv_len, const int32_t* block_table, int table_pages, const uint16_t* q, int ldq,
+                  int n_q_heads, float scale, const uint64_t* tree_mask, uint16_t* to, int ldo) {
+  TreeAttnParams& p = *out;
+  const int st = check_table(p.c, kv_len, block_table, table_pages);
+  if (st) return st;
+  if (!q || !to || !aligned(q, 16) || !aligned(to, 16) || ldq % 8 || ldo % 8)
+    return fail(SV_EINVAL, "q and out must be non-null, 16-byte aligned, with strides that are multiples of 8");
+  if (ldq < n_q_heads * p.c.dim || ldo < n_q_heads * p.c.dim) return fail(SV_EINVAL, "ldq and ldo must be >= n_q_heads * head_dim");
+  if (q == to && ldq != ldo && p.map.offs[p.map.B] > 1) return fail(SV_EINVAL, "an in-place call needs equal strides");
+  if (!(std::fabs(scale) <= 0x1p127f)) return fail(SV_EINVAL, "scale must be at most 2^127 in magnitude");
+  if (!aligned(tree_mask, 8)) return fail(SV_EINVAL, "tree_mask must be 8-byte aligned");
+  p.kv_len = kv_len;
+  p.table = block_table;
+  p.table_pages = table_pages;
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.ldq = ldq;
+  p.group = n_q_heads / p.c.heads;
+  p.per_group = ((1u << 20) + p.group - 1) / p.group;
+  p.scale = scale;
+  p.mask = tree_mask;
+  p.out = reinterpret_cast<__nv_bfloat16*>(to);
+  p.ldo = ldo;
+  return SV_OK;
+}
+
+int ta_encode(const KvCache& c, CUtensorMap* tk, CUtensorMap* tv) {
+  const uint64_t slabs = (uint64_t)c.n_pages * c.heads, page = 1ull << c.page_shift;
+  const uint32_t box = page < 128 ? (uint32_t)page : 128u;
+  const int st = encode_tiled_3d_sw128(tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.p.k, c.dim, page, slabs, 2, 64, box);
+  return st ? st : encode_tiled_3d_sw128(tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.p.v, c.dim, page, slabs, 2, 64, box);
+}
+
+int ta_launch(TreeAttnParams* out, cudaStream_t s, bool* one_unit) {
+  TreeAttnParams& p = *out;
+  const bool narrow = ta_choose_block(p.map, p.group, &p.block);
+  // Beginning an item, in the same measure: what gave the least time over several batches and lengths.  (Wide, bf16, 32 rows of
+  // 65536 tokens: 60.8 us with 30, 59.0 with 60; 4 x 8 rows in 48 heads 68.0 and 64.2, over codes 54.8 and 56.1.  Narrow, 8-bit,
+  // 8 rows of 65536 tokens: 57.4 with 25, 52.8 with 35; 8 x 4 rows 32.4 and 33.2.)
+  p.cost[0] = 5;
+  p.cost[1] = p.block == 32 ? 7 : 5;
+  p.begin_cost = narrow ? (p.block == 16 ? 25 : 35) : (p.c.bits == 16 ? 60 : 35);
+  // the lengths are on the device: size the grid for the longest the table allows
+  long long most = 0;
+  *one_unit = true;
+  for (int b = 0; b < p.map.B; ++b) {
+    const int m = p.map.offs[b + 1] - p.map.offs[b];
+    const long long places = (long long)(p.table_pages - p.skip[b]) << p.c.page_shift;
+    if (m > places) return fail(SV_EINVAL, "request %d has more rows than block_table has places", b);
+    const long long units = (places + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
+    most += (long long)p.c.heads * ta_blocks(m * p.group, p.block) * units;
+    if (m && units > 1) *one_unit = false;
+  }
+  const int sms = ta_sms();
+  p.grid = most < sms ? (int)most : sms;
+  if (p.c.bits == 16 && !narrow) {
+    const int st = ta_encode(p.c, &p.tk, &p.tv);
+    if (st) return st;
+  }
+  const cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn_wide(p, s);
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, "tree attention launch");
+}
 
 template <int D, int WPP, int PAIRS>
 static cudaError_t launch_join_w(const TreeAttnParams& p, long long pairs, long long most, cudaStream_t s) {
@@ -185,8 +271,7 @@ extern "C" {
 size_t sv_tree_attention_workspace_bytes(const sv_kv_cache* cache, int B, const int32_t* row_offsets, int n_q_heads) {
   KvCache c;
   RowMap m;
-  if (check_cache(cache, &c) || check_rows_map(B, row_offsets, KV_MAX_DRAFT, 1 << 22, &m) || check_heads(c, n_q_heads)) return 0;
-  return ta_partial_bytes(ta_sms(), c.dim) + ta_stats_bytes(ta_sms());
+  return ta_check_batch(cache, B, row_offsets, n_q_heads, &c, &m) ? 0 : ta_workspace_bytes(c);
 }
 
 int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offsets, const int32_t* kv_len,
@@ -194,73 +279,21 @@ int sv_tree_attention(const sv_kv_cache* cache, int B, const int32_t* row_offset
                       const uint64_t* tree_mask, uint16_t* out, int ldo, void* workspace, size_t workspace_bytes,
                       void* stream) {
   TreeAttnParams p;
-  memset(static_cast<void*>(&p), 0, offsetof(TreeAttnParams, c));
-  int st = check_cache(cache, &p.c);
-  if (!st) st = check_rows_map(B, row_offsets, KV_MAX_DRAFT, 1 << 22, &p.map);
-  if (!st) st = check_table(p.c, kv_len, block_table, table_pages);
-  if (!st) st = check_heads(p.c, n_q_heads);
+  memset(static_cast<void*>(&p), 0, sizeof(p));
+  int st = ta_check_batch(cache, B, row_offsets, n_q_heads, &p.c, &p.map);
+  if (!st) st = ta_check_call(&p, kv_len, block_table, table_pages, q, ldq, n_q_heads, scale, tree_mask, out, ldo);
   if (st) return st;
-  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8)
-    return fail(SV_EINVAL, "q and out must be non-null, 16-byte aligned, with strides that are multiples of 8");
-  if (ldq < n_q_heads * p.c.dim || ldo < n_q_heads * p.c.dim) return fail(SV_EINVAL, "ldq and ldo must be >= n_q_heads * head_dim");
-  if (q == out && ldq != ldo && p.map.offs[B] > 1) return fail(SV_EINVAL, "an in-place call needs equal strides");
-  if (!(std::fabs(scale) <= 0x1p127f)) return fail(SV_EINVAL, "scale must be at most 2^127 in magnitude");
-  if (!aligned(tree_mask, 8)) return fail(SV_EINVAL, "tree_mask must be 8-byte aligned");
   const int sms = ta_sms();
-  const size_t partial = ta_partial_bytes(sms, p.c.dim), need = partial + ta_stats_bytes(sms);
   if (!workspace || !aligned(workspace, 256)) return fail(SV_EINVAL, "workspace must be non-null and 256-byte aligned");
-  if (workspace_bytes < need) return fail(SV_EINVAL, "workspace too small: %zu < %zu", workspace_bytes, need);
+  if (workspace_bytes < ta_workspace_bytes(p.c)) return fail(SV_EINVAL, "workspace too small: %zu < %zu", workspace_bytes, ta_workspace_bytes(p.c));
   if (!p.map.offs[B]) return SV_OK;
-  p.kv_len = kv_len;
-  p.table = block_table;
-  p.table_pages = table_pages;
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  p.ldq = ldq;
-  p.group = n_q_heads / p.c.heads;
-  p.per_group = ((1u << 20) + p.group - 1) / p.group;
-  p.scale = scale;
-  p.mask = tree_mask;
-  p.out = reinterpret_cast<__nv_bfloat16*>(out);
-  p.ldo = ldo;
   p.partial = static_cast<float*>(workspace);
-  p.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + partial);
-  int rows = 0;                // of the widest request, times the group
-  long long by16 = 0, by32 = 0;
-  for (int b = 0; b < B; ++b) {
-    const int m = p.map.offs[b + 1] - p.map.offs[b];
-    if ((long long)m > ((long long)table_pages << p.c.page_shift))
-      return fail(SV_EINVAL, "request %d has more rows than block_table has places", b);
-    if (m * p.group > rows) rows = m * p.group;
-    by16 += 4 * ta_blocks(m * p.group, 16);
-    by32 += m ? (m * p.group > 16 ? 7 : 5) : 0;
-  }
-  const bool narrow = rows <= TA_NARROW_ROWS;
-  // In fifths of the time of a narrow unit of 32-row blocks with one row tile filled: two tiles filled take 7, a block of 16
-  // rows takes 4.  (One request of 32 rows over 16384 tokens: 23.3 us in a block of 32, 23.8 in two of 16, over 65536 52 and 61; 48
-  // requests of 4 to 20 rows: 191 in blocks of 32, 158 in blocks of 16.)
-  p.block = narrow ? (by16 < by32 ? 16 : 32) : TA_MAX_BLOCK;
-  // Beginning an item, in the same measure: what gave the least time over several batches and lengths.  (Wide, bf16, 32 rows of
-  // 65536 tokens: 60.8 us with 30, 59.0 with 60; 4 x 8 rows in 48 heads 68.0 and 64.2, over codes 54.8 and 56.1.  Narrow, 8-bit,
-  // 8 rows of 65536 tokens: 57.4 with 25, 52.8 with 35; 8 x 4 rows 32.4 and 33.2.)
-  p.cost[0] = 5;
-  p.cost[1] = p.block == 32 ? 7 : 5;
-  p.begin_cost = narrow ? (p.block == 16 ? 25 : 35) : (p.c.bits == 16 ? 60 : 35);
-  // the lengths are on the device: size the grid for the longest the table allows
-  const long long most_units = (((long long)table_pages << p.c.page_shift) + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
-  long long most = 0;
-  for (int b = 0; b < B; ++b)
-    most += (long long)p.c.heads * ta_blocks((p.map.offs[b + 1] - p.map.offs[b]) * p.group, p.block) * most_units;
-  p.grid = most < sms ? (int)most : sms;
-  if (p.c.bits == 16 && !narrow) {
-    const uint64_t slabs = (uint64_t)p.c.n_pages * p.c.heads, page = 1ull << p.c.page_shift;
-    const uint32_t box = page < 128 ? (uint32_t)page : 128u;
-    st = encode_tiled_3d_sw128(&p.tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.c.p.k, p.c.dim, page, slabs, 2, 64, box);
-    if (!st) st = encode_tiled_3d_sw128(&p.tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.c.p.v, p.c.dim, page, slabs, 2, 64, box);
-    if (st) return st;
-  }
+  p.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ta_partial_bytes(sms, p.c.dim));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn_wide(p, s);
-  if (e == cudaSuccess && most_units > 1) e = p.c.dim == 128 ? launch_join<128>(p, sms, s) : launch_join<64>(p, sms, s);
+  bool one_unit;
+  st = ta_launch(&p, s, &one_unit);
+  if (st || one_unit) return st;         // (an item of one unit is never dealt to two CTAs)
+  const cudaError_t e = p.c.dim == 128 ? launch_join<128>(p, sms, s) : launch_join<64>(p, sms, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "tree attention launch");
 }
 

@@ -33,7 +33,14 @@ struct TreeAttnParams {
   int block;                 // rows (drafted row x query head of the group) per item
   int cost[2];               // of a unit with up to 16 rows, and with more
   int begin_cost;            // of beginning an item
+  // of a call over shared prefixes: the pages in front of each request's own tokens, which another kernel attends to, and whether
+  // every part is left for the join
+  int skip[MAX_BATCH];
+  int keep;
 };
+
+// Of request b: the table's entries of its own tokens.
+__device__ __forceinline__ const int32_t* ta_table(const TreeAttnParams& p, int b) { return p.table + (size_t)b * p.table_pages + p.skip[b]; }
 
 // What every CTA derives from the lengths: prefix sums of units.
 struct TaPlan {
@@ -51,7 +58,6 @@ __device__ __forceinline__ int ta_cost(const TreeAttnParams& p, int m) { return 
 __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool real, bool report) {
   const int lane = threadIdx.x & 31;
   const RowMap& map = p.map;
-  const long long cap = (long long)p.table_pages << p.c.page_shift;   // at least every request's rows (checked by the host)
   long long run = 0;             // of the units' cost
   int items = 0;
   for (int b0 = 0; b0 < map.B; b0 += 32) {
@@ -60,7 +66,8 @@ __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, b
     int n = 0;
     if (b < map.B) {
       const int m = map.offs[b + 1] - map.offs[b];
-      long long len = real ? p.kv_len[b] : 0;
+      const long long cap = (long long)(p.table_pages - p.skip[b]) << p.c.page_shift;   // at least the request's rows (checked by the host)
+      long long len = real ? p.kv_len[b] - ((long long)p.skip[b] << p.c.page_shift) : 0;
       if (m && (len < 0 || len + m > cap)) {
         if (report) raise_error(ERR_BAD_INPUT);
         len = len < 0 ? 0 : cap - m;
@@ -108,6 +115,7 @@ __device__ __forceinline__ int ta_units_before(long long x, long long a0, int nt
 struct TaSeg {
   int b, h, rb, m, row0, rows;   // request, key head, row block; drafted rows, first row, rows of the block
   int tile0, n, nt, len, total;  // first unit, units, the item's units; committed and all tokens
+  int item;                      // number of the item
   long long next;                // where the count goes on
   bool first;                    // of the item that the CTA's share begins in
 };
@@ -129,6 +137,7 @@ __device__ __forceinline__ TaSeg ta_segment(const TreeAttnParams& p, const TaPla
   const int item = (int)ta_div(local, count);
   const long long a0 = plan.pre[lo] + (long long)item * count;
   const int nrb = ta_blocks(s.m * p.group, p.block);
+  s.item = (lo ? plan.items[lo] : 0) + item;
   s.h = item / nrb;
   s.rb = item - s.h * nrb;
   const int left = s.m * p.group - s.rb * p.block;
@@ -218,8 +227,25 @@ __device__ __forceinline__ float ta_score_factor(float scale, int e) {
 }
 __device__ __forceinline__ bool ta_half_bad(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
 
-// Where a CTA's run of an item leaves its partial sums.
-__device__ __forceinline__ size_t ta_slot(const TaSeg& s) { return 2 * (size_t)blockIdx.x + (s.first ? 0 : 1); }
+// Whether a run is written to the output at once, and where it leaves its partial sums otherwise.  Where every run leaves them, item plus
+// CTA tells runs apart: neither goes down from run to run, and one of them goes up.
+__device__ __forceinline__ bool ta_whole(const TreeAttnParams& p, const TaSeg& s) { return s.n == s.nt && !p.keep; }
+__device__ __forceinline__ size_t ta_slot(const TreeAttnParams& p, const TaSeg& s) {
+  return p.keep ? (size_t)s.item + blockIdx.x : 2 * (size_t)blockIdx.x + (s.first ? 0 : 1);
+}
+
+// Host side.  Checks of a batch; the same workspace for every batch; the rows per block (16, 32, or 128 of the tensor-memory kernel:
+// false).
+int ta_check_batch(const sv_kv_cache* cache, int B, const int32_t* row_offsets, int n_q_heads, KvCache* c, RowMap* m);
+int ta_sms();
+size_t ta_workspace_bytes(const KvCache& c);
+bool ta_choose_block(const RowMap& map, int group, int* block);
+// Checks of a call's other arguments, which p gets; c and map are there already.
+int ta_check_call(TreeAttnParams* p, const int32_t* kv_len, const int32_t* block_table, int table_pages, const uint16_t* q, int ldq,
+                  int n_q_heads, float scale, const uint64_t* tree_mask, uint16_t* to, int ldo);
+int ta_encode(const KvCache& c, CUtensorMap* tk, CUtensorMap* tv);     // tensor maps of a 16-bit cache
+// The kernel for p's rows (partial, stats, skip and keep are set).  one_unit: no item can have more than one unit.
+int ta_launch(TreeAttnParams* p, cudaStream_t s, bool* one_unit);
 
 cudaError_t launch_tree_attn_wide(const TreeAttnParams& p, cudaStream_t s);     // blocks of 128 rows
 cudaError_t launch_tree_attn_narrow(const TreeAttnParams& p, cudaStream_t s);   // of 16 or 32

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
       pages = 0;
       if (k < own) {
         const int t = (first + warp + k * Sh::W) * TN_STEP;
-        pages = p.table[(size_t)s.b * p.table_pages + (t >> p.c.page_shift)];
+        pages = ta_table(p, s.b)[t >> p.c.page_shift];
       }
     };
     load_pages(0);
@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
             const int k = 16 * t + 8 * q + g, r = s.rb * p.block + k, di = ta_by_group(p, r);
             s_f[k] = q ? f[1] : f[0];
             s_mask[k] = mask;
-            s_out[k] = s.n == s.nt ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
-                                   : (long long)(ta_slot(s) * p.block + k) * D;
+            s_out[k] = ta_whole(p, s) ? (long long)(s.row0 + di) * p.ldo + (s.h * p.group + r - di * p.group) * D
+                                   : (long long)(ta_slot(p, s) * p.block + k) * D;
           }
         }
         __syncthreads();
@@ -589,8 +589,8 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
         }
       }
     __syncthreads();
-    const bool whole = s.n == s.nt, odd = s_odd != 0;
-    const size_t slot = ta_slot(s);
+    const bool whole = ta_whole(p, s), odd = s_odd != 0;
+    const size_t slot = ta_slot(p, s);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
           for (int i = 0; i < 4 * s.m; ++i) {
             const int pos = s.len + i / 4;
             if (!(see >> (i / 4) & 1) || pos < s.tile0 << TA_UNIT_SHIFT || pos >= (s.tile0 + s.n) << TA_UNIT_SHIFT) continue;
-            const int page = p.table[(size_t)s.b * p.table_pages + (pos >> p.c.page_shift)];
+            const int page = ta_table(p, s.b)[pos >> p.c.page_shift];
             if ((unsigned)page >= (unsigned)p.c.n_pages) continue;
             const float v = ta_cache_value<BITS>(p.c.p.v, p.c.p.vs, p.c.p.vb, kv_token(p.c, page, s.h, pos & pm), D, d0 + i % 4);
             if (!isfinite(v)) e[i % 4] += v;
