@@ -280,8 +280,8 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
  * the result does not depend on timing.  Logits of -inf have probability 0.
  * A parent or token out of range is bad input: that request gets out_len 0
  * and nothing else, and sv_device_error() reports it.
- * Workspace: sv_tree_accept_workspace_bytes(rows), 256-byte aligned, used (and
- * written) only where top_k or top_p truncate, NULL otherwise allowed; it need not be zero. */
+ * Workspace: none (what a step keeps stays on the SMs): the query returns 0, and
+ * workspace may be NULL. */
 size_t sv_tree_accept_workspace_bytes(int rows);
 int sv_tree_accept(int B, const int32_t* row_offsets, const float* logits, int ldl, const float* row_max,
                    const float* row_sumexp, const int32_t* row_argmax, const int32_t* parent, const int32_t* token,

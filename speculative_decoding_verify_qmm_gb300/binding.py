@@ -601,13 +601,10 @@ class Library:
         up = None if u is None else _vector("u", u, f32, dev, rows)
         outs = [_vector("out_len", out_len, i32, dev, B), _vector("out_tokens", out_tokens, i32, dev, rows),
                 _vector("path", path, i32, dev, 0)]
-        size, ws = 0, None
-        if temperature > 0 and (0 < top_k < V or top_p < 1):
-            ws, size = self._workspace(workspace, lambda: self.tree_accept_workspace_bytes(rows), logits.device, dev, stream)
-            ws = ws.data_ptr()
+        ws, size = (None, 0) if workspace is None else self._workspace(workspace, None, logits.device, dev, stream)
         status = self.lib.sv_tree_accept(B, offs, logits.data_ptr(), ldl, *ptrs, None if q is None else q.data_ptr(), ldq,
                                          bool(distinct), V, float(temperature), up, int(top_k), float(top_p), *outs,
-                                         path.shape[1], ws, size, handle)
+                                         path.shape[1], None if ws is None else ws.data_ptr(), size, handle)
         if status:
             self.check(status)
         return out_len, out_tokens, path
