@@ -18,9 +18,9 @@ namespace sv {
 constexpr int PG_THREADS = 1024, PG_WARPS = PG_THREADS / 32;
 constexpr int PG_SCAN = 16;                         // counts a thread looks at in one step of a scan
 constexpr int PG_LAYERS = 64;                       // caches per launch: their pointers ride in the launch parameters
-constexpr int PG_COPY_THREADS = 256, PG_AHEAD = 8;  // 16-byte pieces a thread has in flight
-constexpr int PG_TILE = PG_COPY_THREADS * PG_AHEAD; // pieces of a tile
-constexpr int PG_CTAS = 4;                          // per SM
+constexpr int PC_THREADS = 256;                     // of a copying CTA
+constexpr int PC_STAGES = 6, PC_LEAD = 4;           // whole pages: tiles of a warp in shared memory, and on their way in
+constexpr int PC_SMEM = 192 * 1024;                 // of all its warps that copy
 
 struct PagePool {
   int32_t *refs, *table, *held;
@@ -43,6 +43,8 @@ struct PageCopyParams {
   int step, n;                           // copies, or at most so many
   const int32_t* count;                  // DEVICE: copies (NULL: n)
   int tiles_kv, tiles;                   // tiles of K (and of V), and of all arrays of a page
+  int stage;                             // whole pages: bytes of a tile
+  int side_tiles;                        // tiles of each array of scales or biases; 0: the four share one
   // after a reserve or a compact: what is left of the bookkeeping
   PagePool g;
   int32_t *list, *before;
@@ -324,7 +326,7 @@ __device__ __forceinline__ void drop_page(const PagePool& g, int id) {
 
 // The rest of a reserve: counts of pages that were replaced or given back.
 __device__ __forceinline__ void finish_reserve(const PageCopyParams& p) {
-  const int at = blockIdx.x * PG_COPY_THREADS + threadIdx.x, all = gridDim.x * PG_COPY_THREADS;
+  const int at = blockIdx.x * PC_THREADS + threadIdx.x, all = gridDim.x * PC_THREADS;
   for (int i = at, n = *p.fresh; i < n; i += all) {
     const int old = p.list[i];
     if (old) {
@@ -337,7 +339,7 @@ __device__ __forceinline__ void finish_reserve(const PageCopyParams& p) {
     __syncthreads();
     if (before == 0) continue;
     if (threadIdx.x == 0) p.before[s] = 0;
-    for (int e = now + threadIdx.x; e < before; e += PG_COPY_THREADS) drop_page(p.g, p.g.table[(size_t)s * p.g.table_pages + e]);
+    for (int e = now + threadIdx.x; e < before; e += PC_THREADS) drop_page(p.g, p.g.table[(size_t)s * p.g.table_pages + e]);
   }
 }
 
@@ -350,7 +352,7 @@ __device__ __forceinline__ void finish_compact(const PageCopyParams& p) {
       if (threadIdx.x == 0) raise_error(ERR_BAD_INPUT);
       continue;
     }
-    for (int e = threadIdx.x; e < has; e += PG_COPY_THREADS) {
+    for (int e = threadIdx.x; e < has; e += PC_THREADS) {
       int32_t* at = p.g.table + (size_t)s * p.g.table_pages + e;
       const int id = *at;
       if ((unsigned)id < (unsigned)live) continue;
@@ -365,21 +367,22 @@ __device__ __forceinline__ void finish_compact(const PageCopyParams& p) {
   }
 }
 
-// Tiles of 32 KB of one array of one page and layer, in turn.
-template <int REST>
-__global__ void __launch_bounds__(PG_COPY_THREADS, PG_CTAS) kv_page_copy_kernel(const __grid_constant__ PageCopyParams p) {
+// ---- beginnings of pages (copies of a reserve): pieces of 16 bytes by threads.  Strided pieces of a few KB are
+// nothing for bulk copies (93 copies of 7 places in 64 layers: 61 us by threads, 77 by bulk copies of each head's).
+constexpr int PP_AHEAD = 8, PP_TILE = PC_THREADS * PP_AHEAD;   // pieces a thread has in flight; of a tile
+constexpr int PP_CTAS = 3;   // per SM (93 copies of 7 places in 64 layers, with the calls around them: 68.9 us, 4 86.5, 2 67.4)
+template <bool REST>
+__global__ void __launch_bounds__(PC_THREADS, PP_CTAS) kv_part_copy_kernel(const __grid_constant__ PageCopyParams p) {
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x;
-  if constexpr (REST == 1) finish_reserve(p);
-  if constexpr (REST == 2) finish_compact(p);
-  const int n = p.count ? *p.count : p.n;
+  if constexpr (REST) finish_reserve(p);
+  const int n = p.count ? *p.count : p.n, tid = threadIdx.x;
   const int page = 1 << p.c.page_shift, row16 = p.c.dim * p.c.bits / 128, groups = p.c.dim / GROUP;
   const long long all = (long long)n * p.n_layers * p.tiles;
   for (long long t = blockIdx.x; t < all; t += gridDim.x) {
     const long long pl = t / p.tiles;
     const int tile = (int)(t - pl * p.tiles), i = (int)(pl / p.n_layers), layer = (int)(pl - (long long)i * p.n_layers);
-    const int src = p.src[(size_t)i * p.step], dst = p.dst[(size_t)i * p.step], places = p.places ? p.places[(size_t)i * p.step] : page;
+    const int src = p.src[(size_t)i * p.step], dst = p.dst[(size_t)i * p.step], places = p.places[(size_t)i * p.step];
     if ((unsigned)src >= (unsigned)p.c.n_pages || (unsigned)dst >= (unsigned)p.to_pages || (unsigned)places > (unsigned)page) {
       if (tid == 0) raise_error(ERR_BAD_INPUT);
       continue;
@@ -387,37 +390,158 @@ __global__ void __launch_bounds__(PG_COPY_THREADS, PG_CTAS) kv_page_copy_kernel(
     const KvPtrs &from = p.from[layer], &to = p.to[layer];
     if (tile < 2 * p.tiles_kv) {
       const bool is_v = tile >= p.tiles_kv;
-      const int per = places * row16;                 // 16-byte pieces of a head
-      const int pieces = p.c.heads * per, base = (is_v ? tile - p.tiles_kv : tile) * PG_TILE;
+      const unsigned per = places * row16, pieces = p.c.heads * per, base = (unsigned)(is_v ? tile - p.tiles_kv : tile) * PP_TILE + tid;
       const size_t page16 = (size_t)p.c.heads * page * row16;
-      const uint4* a = reinterpret_cast<const uint4*>(is_v ? from.v : from.k) + (size_t)src * page16;
-      uint4* b = reinterpret_cast<uint4*>(is_v ? to.v : to.k) + (size_t)dst * page16;
-      uint4 x[PG_AHEAD];
-      uint32_t at[PG_AHEAD];
+      const uint4* a = reinterpret_cast<const uint4*>(is_v ? from.v : from.k) + src * page16;
+      uint4* b = reinterpret_cast<uint4*>(is_v ? to.v : to.k) + dst * page16;
+      uint4 x[PP_AHEAD];
+      unsigned at[PP_AHEAD];
 #pragma unroll
-      for (int y = 0; y < PG_AHEAD; ++y) {
-        const int k = base + y * PG_COPY_THREADS + tid;
-        at[y] = (uint32_t)k;
-        if (k < pieces) {
-          if (places != page) at[y] = (uint32_t)(k / per * (page * row16) + k % per);
-          x[y] = a[at[y]];
-        }
+      for (int y = 0; y < PP_AHEAD; ++y) {
+        const unsigned k = base + y * PC_THREADS;
+        if (k >= pieces) continue;
+        at[y] = k / per * (page * row16) + k % per;
+        x[y] = a[at[y]];
       }
 #pragma unroll
-      for (int y = 0; y < PG_AHEAD; ++y)
-        if (base + y * PG_COPY_THREADS + tid < pieces) b[at[y]] = x[y];
+      for (int y = 0; y < PP_AHEAD; ++y)
+        if (base + y * PC_THREADS < pieces) b[at[y]] = x[y];
     } else {
       // scales and biases, two bytes at a time: 1/32 or 1/16 of the codes
       const int per = places * groups, pieces = p.c.heads * per;
-      const int z = tile - 2 * p.tiles_kv;
-      const size_t page2 = (size_t)p.c.heads * page * groups;
-      const __half* a = (z == 0 ? from.ks : z == 1 ? from.kb : z == 2 ? from.vs : from.vb) + (size_t)src * page2;
-      __half* b = (z == 0 ? to.ks : z == 1 ? to.kb : z == 2 ? to.vs : to.vb) + (size_t)dst * page2;
-      for (int k = tid; k < pieces; k += PG_COPY_THREADS) {
+      const size_t page2 = (size_t)p.c.heads * page * groups, a = src * page2, b = dst * page2;
+      for (int k = tid; k < pieces; k += PC_THREADS) {
         const size_t at = (size_t)(k / per) * (page * groups) + k % per;
-        b[at] = a[at];
+        const __half s = from.ks[a + at], t2 = from.kb[a + at], u = from.vs[a + at], v = from.vb[a + at];
+        to.ks[b + at] = s;
+        to.kb[b + at] = t2;
+        to.vs[b + at] = u;
+        to.vb[b + at] = v;
       }
     }
+  }
+}
+
+// ---- whole pages: a warp moves tiles of up to PC_STAGE bytes through shared memory with bulk copies, PC_LEAD of them on their way in while
+// those before are on their way out.  Tiles of 16 KB and two warps where an array's page has as much (257 pages of 64 KB in 36 layers: 394
+// us against 407), of 8 KB and four warps otherwise (pages of 8 KB: 161 against 210).
+struct PageTile {
+  int layer, src, dst, tile;             // tile < 0: nothing to do
+};
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// This lane's piece of a tile: its place in the arrays and in the stage, and its bytes (a multiple of 16, perhaps 0); all: the tile's.
+struct PagePiece {
+  size_t from, to;                       // byte offsets in the arrays
+  uint32_t at, bytes, all;
+  int array;                             // K, V, then their scales and biases
+};
+template <int PC_STAGE>
+__device__ __forceinline__ PagePiece page_piece(const PageCopyParams& p, const PageTile& t, int lane) {
+  PagePiece x = {};
+  if (t.tile < 0) return x;
+  const int page = 1 << p.c.page_shift;
+  const bool kv = t.tile < 2 * p.tiles_kv;
+  const size_t size = (size_t)p.c.heads * page * (kv ? p.c.dim * p.c.bits / 8 : p.c.dim / GROUP * 2);   // of an array's page
+  size_t off = 0;
+  if (!kv && p.side_tiles == 0) {        // all four arrays at once, a lane each
+    x.array = 2 + (lane & 3);
+    x.all = (uint32_t)(4 * size);
+    x.bytes = lane < 4 ? (uint32_t)size : 0;
+    x.at = (uint32_t)((lane & 3) * size);
+  } else {
+    const int per = kv ? p.tiles_kv : p.side_tiles, tile = kv ? t.tile : t.tile - 2 * p.tiles_kv, a = tile / per;
+    x.array = kv ? a : 2 + a;
+    off = (size_t)(tile - a * per) * PC_STAGE;
+    x.all = size - off < PC_STAGE ? (uint32_t)(size - off) : PC_STAGE;
+    x.bytes = lane == 0 ? x.all : 0;
+  }
+  x.from = t.src * size + off;
+  x.to = t.dst * size + off;
+  return x;
+}
+__device__ __forceinline__ uint8_t* page_array(const KvPtrs& c, int array) {
+  return array == 0 ? c.k : array == 1 ? c.v : reinterpret_cast<uint8_t*>(array == 2 ? c.ks : array == 3 ? c.kb : array == 4 ? c.vs : c.vb);
+}
+
+template <int PC_STAGE, bool REST>
+__global__ void __launch_bounds__(PC_THREADS, 1) kv_page_copy_kernel(const __grid_constant__ PageCopyParams p) {
+  constexpr int PC_WARPS = PC_SMEM / (PC_STAGES * PC_STAGE);
+  static_assert(PC_WARPS <= PC_THREADS / 32 && PC_LEAD < PC_STAGES, "warps, and a stage to store from");
+  extern __shared__ __align__(128) uint8_t s_stage[];   // [PC_WARPS][PC_STAGES][PC_STAGE]
+  __shared__ uint64_t s_full[PC_WARPS][PC_STAGES];
+  __shared__ PageTile s_tile[PC_WARPS][PC_STAGES];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < PC_WARPS * PC_STAGES) mbar_init(&s_full[0][0] + threadIdx.x, 1);
+  fence_mbar_init();
+  __syncthreads();
+  pdl_trigger();
+  pdl_wait();
+  if constexpr (REST) finish_compact(p);
+  if (warp >= PC_WARPS) return;
+  const int n = p.count ? *p.count : p.n;
+  const long long all = (long long)n * p.n_layers * p.tiles, first = (long long)blockIdx.x * PC_WARPS + warp, step = (long long)gridDim.x * PC_WARPS;
+  const int mine = first < all ? (int)((all - first + step - 1) / step) : 0;
+  // lane i: tile base + i of this warp's
+  PageTile ahead = {};
+  auto look = [&](int base) {
+    const int k = base + lane;
+    ahead.tile = -1;
+    if (k >= mine) return;
+    const long long id = first + k * step, pl = id / p.tiles;
+    const int i = (int)(pl / p.n_layers);
+    ahead.layer = (int)(pl - (long long)i * p.n_layers);
+    ahead.src = p.src[(size_t)i * p.step];
+    ahead.dst = p.dst[(size_t)i * p.step];
+    if ((unsigned)ahead.src >= (unsigned)p.c.n_pages || (unsigned)ahead.dst >= (unsigned)p.to_pages) raise_error(ERR_BAD_INPUT);
+    else ahead.tile = (int)(id - pl * p.tiles);
+  };
+  auto load = [&](int k) {
+    const int st = k % PC_STAGES;
+    if (!(k & 31)) look(k);
+    PageTile t;
+    t.layer = __shfl_sync(0xffffffffu, ahead.layer, k & 31);
+    t.src = __shfl_sync(0xffffffffu, ahead.src, k & 31);
+    t.dst = __shfl_sync(0xffffffffu, ahead.dst, k & 31);
+    t.tile = __shfl_sync(0xffffffffu, ahead.tile, k & 31);
+    if (lane == 0) s_tile[warp][st] = t;
+    const PagePiece x = page_piece<PC_STAGE>(p, t, lane);
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][st], x.all);
+    __syncwarp();
+    if (x.bytes)
+      bulk_load(s_stage + (warp * PC_STAGES + st) * PC_STAGE + x.at, page_array(p.from[t.layer], x.array) + x.from, x.bytes, &s_full[warp][st], l2_evict_first());
+  };
+  volatile int never = 0;
+  bool ok = true;
+  for (int k = 0; k < PC_LEAD && k < mine; ++k) load(k);
+  for (int k = 0; k < mine && ok; ++k) {
+    const int st = k % PC_STAGES;
+    // the stage of the next tile to load was stored from PC_STAGES - PC_LEAD tiles ago
+    if (k + PC_LEAD < mine) {
+      bulk_wait_read<PC_STAGES - PC_LEAD - 1>();
+      __syncwarp();
+      load(k + PC_LEAD);
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][st], (k / PC_STAGES) & 1, &never));
+    if (ok) {
+      const PageTile t = s_tile[warp][st];
+      const PagePiece x = page_piece<PC_STAGE>(p, t, lane);
+      if (x.bytes) bulk_store(page_array(p.to[t.layer], x.array) + x.to, s_stage + (warp * PC_STAGES + st) * PC_STAGE + x.at, x.bytes);
+    }
+    bulk_commit();
+  }
+  bulk_wait_all();
+  if (!ok) {                             // copies in flight get time to land
+    raise_error(ERR_TIMEOUT_FULL);
+    const unsigned long long w0 = global_ns();
+    while (global_ns() - w0 < 50000ull) __nanosleep(1000);
   }
 }
 
@@ -475,15 +599,33 @@ static int check_layers(const sv_kv_cache* from, const sv_kv_cache* to, int n_la
   return SV_OK;
 }
 
-// REST 1, 2: the first launch finishes a reserve or a compact too, and there is one even without layers.
-template <int REST>
+// REST: the first launch finishes a reserve (PART) or a compact too, and there is one even without layers.
+template <bool PART, bool REST>
+static cudaError_t launch_copy(const PageCopyParams& p, int grid, cudaStream_t s) {
+  const auto kernel = PART ? kv_part_copy_kernel<REST> : p.stage == 8192 ? kv_page_copy_kernel<8192, REST> : kv_page_copy_kernel<16384, REST>;
+  const int smem = PART ? 0 : PC_SMEM;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(PC_THREADS), smem, s, attr);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+template <bool PART, bool REST>
 static int launch_copies(PageCopyParams& p, const sv_kv_cache* from, const sv_kv_cache* to, int n_layers, cudaStream_t s) {
   const int sms = device_sm_count();
   if (sms <= 0) return fail(SV_ECUDA, "no CUDA device");
-  const long long page = n_layers ? 1ll << p.c.page_shift : 0;
-  const long long pieces = n_layers ? p.c.heads * page * (p.c.dim * p.c.bits / 128) : 0;
-  p.tiles_kv = (int)((pieces + PG_TILE - 1) / PG_TILE);
-  p.tiles = 2 * p.tiles_kv + (n_layers && p.c.bits != 16 ? 4 : 0);
+  const long long kv = n_layers ? (long long)p.c.heads * (p.c.dim * p.c.bits / 8) << p.c.page_shift : 0;   // bytes of an array's page
+  const long long side = n_layers && p.c.bits != 16 ? (long long)p.c.heads * (p.c.dim / GROUP * 2) << p.c.page_shift : 0;
+  auto tiles = [](long long bytes, long long size) { return (int)((bytes + size - 1) / size); };
+  if (PART) {
+    p.tiles_kv = tiles(kv, 16 * PP_TILE);
+    p.tiles = 2 * p.tiles_kv + (side ? 1 : 0);
+  } else {
+    p.stage = kv < 16384 ? 8192 : 16384;
+    p.tiles_kv = tiles(kv, p.stage);
+    p.side_tiles = 4 * side <= p.stage ? 0 : tiles(side, p.stage);
+    p.tiles = 2 * p.tiles_kv + (!side ? 0 : !p.side_tiles ? 1 : 4 * p.side_tiles);
+  }
   for (int l0 = 0; l0 == 0 || l0 < n_layers; l0 += PG_LAYERS) {
     p.n_layers = n_layers - l0 < PG_LAYERS ? n_layers - l0 : PG_LAYERS;
     for (int l = 0; l < p.n_layers; ++l) {
@@ -494,11 +636,12 @@ static int launch_copies(PageCopyParams& p, const sv_kv_cache* from, const sv_kv
       p.to[l] = c.p;
     }
     const bool rest = REST && l0 == 0;
-    const long long most = (long long)p.n * p.n_layers * p.tiles, want = rest && most < p.g.slots ? p.g.slots : most;
+    const int each = PART ? 1 : PC_SMEM / (PC_STAGES * p.stage);
+    long long want = ((long long)p.n * p.n_layers * p.tiles + each - 1) / each;
+    if (rest && want < p.g.slots) want = p.g.slots;
     if (!want) continue;
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)std::min(want, (long long)sms * PG_CTAS)), dim3(PG_COPY_THREADS), 0, s, attr);
-    const cudaError_t e = rest ? cudaLaunchKernelEx(&cfg, kv_page_copy_kernel<REST>, p) : cudaLaunchKernelEx(&cfg, kv_page_copy_kernel<0>, p);
+    const int grid = (int)std::min(want, (long long)sms * (PART ? PP_CTAS : 1));
+    const cudaError_t e = rest ? launch_copy<PART, REST>(p, grid, s) : launch_copy<PART, false>(p, grid, s);
     if (e != cudaSuccess) return cuda_fail(e, "page copy launch");
   }
   return SV_OK;
@@ -567,7 +710,7 @@ int sv_kv_reserve(const sv_kv_pages* pages, const sv_kv_cache* layers, int n_lay
   p.step = 3;
   p.n = r.g.slots;
   p.count = counts + 1;
-  return launch_copies<1>(p, layers, layers, n_layers, s);
+  return launch_copies<true, true>(p, layers, layers, n_layers, s);
 }
 
 int sv_kv_compact(const sv_kv_pages* pages, const sv_kv_cache* layers, int n_layers, int32_t* counts, int32_t* moves, void* stream) {
@@ -592,7 +735,7 @@ int sv_kv_compact(const sv_kv_pages* pages, const sv_kv_cache* layers, int n_lay
   p.step = 2;
   p.n = g.n_pages / 2;                   // a page that moves fills one that is free
   p.count = counts + 1;
-  return launch_copies<2>(p, layers, layers, n_layers, s);
+  return launch_copies<false, true>(p, layers, layers, n_layers, s);
 }
 
 int sv_kv_copy_pages(const sv_kv_cache* from, const sv_kv_cache* to, int n_layers, int n, const int32_t* src, const int32_t* dst, void* stream) {
@@ -607,7 +750,7 @@ int sv_kv_copy_pages(const sv_kv_cache* from, const sv_kv_cache* to, int n_layer
   p.dst = dst;
   p.step = 1;
   p.n = n;
-  return launch_copies<0>(p, from, to, n_layers, static_cast<cudaStream_t>(stream));
+  return launch_copies<false, false>(p, from, to, n_layers, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
