@@ -39,6 +39,23 @@ struct TreeAttnParams {
   int keep;
 };
 
+// A part's maximum and weight of row k: beside those of the other rows, or (where every part is left for the join) in a sector of their
+// own, written whole.  Writes of parts of sectors are slow where other SMs read and write the rest: a join that put 150 thousand of
+// them back to zero took 44 to 130 us, with whole sectors 28.
+constexpr int TA_STAT = 8;                         // floats of a sector
+__device__ __forceinline__ void ta_put_sector(float* at, float most, float weight) {
+  reinterpret_cast<float4*>(at)[0] = make_float4(most, weight, 0.f, 0.f);
+  reinterpret_cast<float4*>(at)[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+__device__ __forceinline__ void ta_put_stats(const TreeAttnParams& p, size_t slot, int k, float most, float weight) {
+  if (p.keep) {
+    ta_put_sector(p.stats + (slot * p.block + k) * TA_STAT, most, weight);
+  } else {
+    p.stats[2 * slot * p.block + k] = most;
+    p.stats[(2 * slot + 1) * p.block + k] = weight;
+  }
+}
+
 // Of request b: the table's entries of its own tokens.
 __device__ __forceinline__ const int32_t* ta_table(const TreeAttnParams& p, int b) { return p.table + (size_t)b * p.table_pages + p.skip[b]; }
 

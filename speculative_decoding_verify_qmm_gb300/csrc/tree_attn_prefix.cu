@@ -35,6 +35,7 @@ struct PxShape {
   static_assert(SMEM <= 220 * 1024, "shared memory");
   static_assert(TEAMS == 0 || OPS % 2 == 0, "a team meets its slots in every turn");
   static constexpr float BIAS = BITS == 16 ? -30.f : 5.f, GROW = BITS == 16 ? -15.f : 15.f;   // as in tree attention
+  static constexpr int AT_ONCE = BITS == 16 ? 64 : 32;    // a row's scores in registers at once
 };
 
 // Order of a run's operand tiles.  Two matrices on the same tiles: K0, V0, K1, V1, ...  On every other tile: K0, K1, V0, K2, V1, ...,
@@ -54,42 +55,29 @@ __device__ __forceinline__ bool px_item(bool pair, int e, int n, int* tile) {
 struct PxRun {
   int g, h, rb, rows;            // group, key head, block and its rows
   int tile0, n;                  // first tile, tiles
-  int slot;                      // place of its sums
+  int slot;                      // number of its first piece: place of its sums
   bool pair;                     // two matrices on the same tiles
-  long long next;
 };
-__device__ __forceinline__ PxRun px_run(const PrefixParams& p, long long u, long long u1) {
+// The CTA's pieces are those from next to end - 1.  By key head, block, tokens.
+__device__ __forceinline__ bool px_next(const PrefixParams& p, int* next, int end, PxRun* r) {
+  if (*next >= end) return false;
+  r->slot = *next;
   int lo = 0, hi = p.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (p.pre[mid] <= u) lo = mid; else hi = mid;
+    if (p.pieces[mid] <= r->slot) lo = mid; else hi = mid;
   }
-  const PxGroup g = px_group(p, p.rows[lo], p.tokens[lo]);
-  const long long local = u - p.pre[lo];
-  PxRun r;
-  r.g = lo;
-  r.h = (int)ta_div(local, g.span);
-  const long long rest = local - r.h * g.span;
-  r.rb = (int)ta_div(rest, g.full);
-  if (r.rb > g.blocks - 1) r.rb = g.blocks - 1;
-  const bool last = r.rb == g.blocks - 1;
-  const long long a0 = p.pre[lo] + r.h * g.span + r.rb * g.full, end = a0 + (last ? g.tail : g.full);
-  r.pair = !last || g.last;
-  const int cost = p.cost[r.pair];
-  r.rows = last ? p.rows[lo] - r.rb * PX_ROWS : PX_ROWS;
-  r.next = end < u1 ? end : u1;
-  r.tile0 = ta_units_before(u, a0, g.nt, cost, p.begin_cost);
-  r.n = ta_units_before(r.next, a0, g.nt, cost, p.begin_cost) - r.tile0;
-  r.slot = p.items[lo] + r.h * g.blocks + r.rb + (int)blockIdx.x;
-  return r;
-}
-__device__ __forceinline__ bool px_next(const PrefixParams& p, long long* u, long long u1, PxRun* r) {
-  while (*u < u1) {
-    *r = px_run(p, *u, u1);
-    *u = r->next;
-    if (r->n > 0) return true;
-  }
-  return false;
+  const int blocks = px_blocks(p.rows[lo]), splits = p.splits[lo], nt = px_tiles(p.tokens[lo]), i = r->slot - p.pieces[lo];
+  const int item = i / splits, part = i - item * splits, parts = min(splits - part, end - r->slot);
+  *next += parts;
+  r->g = lo;
+  r->h = item / blocks;
+  r->rb = item - r->h * blocks;
+  r->pair = px_pair(p.rows[lo], r->rb);
+  r->rows = min(PX_ROWS, p.rows[lo] - r->rb * PX_ROWS);
+  r->tile0 = (int)((long long)part * nt / splits);
+  r->n = (int)((long long)(part + parts) * nt / splits) - r->tile0;
+  return true;
 }
 
 template <int D, int BITS>
@@ -131,7 +119,7 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
-  const long long total = p.pre[p.n], u0 = (long long)blockIdx.x * p.per, u1 = u0 + p.per < total ? u0 + p.per : total;
+  const int all = p.pieces[p.n], first = px_first(all, p.grid, blockIdx.x), end = px_first(all, p.grid, blockIdx.x + 1);
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
@@ -140,12 +128,12 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
   pdl_trigger();               // after the wait: what comes later may then read what came before this kernel
 
   if (warp == Sh::PROD) {
-    long long u = u0;
+    int u = first;
     PxRun s;
     bool ok = true;
     TaRing<RAW16 ? Sh::OPS : TA_PIECES> ring;
     const int shift = p.c.page_shift < 7 ? p.c.page_shift : 7, place_mask = (1 << p.c.page_shift) - 1;
-    while (ok && px_next(p, &u, u1, &s)) {
+    while (ok && px_next(p, &u, end, &s)) {
       const int32_t* const table = p.table + (size_t)p.request[s.g] * p.table_pages;
       const int tokens = p.tokens[s.g];
       constexpr int PER = D / 64;
@@ -256,9 +244,9 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
       tc05_fence_after();
       return got;
     };
-    long long u = u0;
+    int u = first;
     PxRun s;
-    while (ok && px_next(p, &u, u1, &s)) {
+    while (ok && px_next(p, &u, end, &s)) {
       const int n = __shfl_sync(0xffffffffu, s.n, 0);
       uint32_t kb = 0, vb = 0;
       if (s.pair) {
@@ -332,9 +320,9 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
     uint8_t* const qbuf = smem + x * Sh::QB + L * 128;
     uint32_t n_s = 0, n_run = 0;                        // phases of s_full, run_done
     bool ok = true;
-    long long u = u0;
+    int u = first;
     PxRun s;
-    while (ok && px_next(p, &u, u1, &s)) {
+    while (ok && px_next(p, &u, end, &s)) {
       const int rr = s.pair ? 128 * x + L : L;          // row of the block
       const bool real = rr < s.rows;
       const int r = s.rb * PX_ROWS + rr;
@@ -393,16 +381,25 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
         const int j = s.pair ? i : 2 * i + x, left = tokens - (s.tile0 + j) * TA_TILE;
         auto weigh = [&](auto is_masked) {
           constexpr bool MASKED = decltype(is_masked)::value;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(sbuf + 32 * c, v);
-            const int seen = left - 32 * c;
-            const uint32_t m = !MASKED || seen >= 32 ? 0xffffffffu : (seen > 0 ? (1u << seen) - 1 : 0u);
-            float mx = -INFINITY;
+          constexpr int NB = Sh::AT_ONCE;                 // columns at once
 #pragma unroll
-            for (int y = 0; y < 32; y += 2)
-              mx = ta_max3(mx, !MASKED || (m >> y & 1) ? __uint_as_float(v[y]) : -INFINITY, !MASKED || (m >> (y + 1) & 1) ? __uint_as_float(v[y + 1]) : -INFINITY);
+          for (int c0 = 0; c0 < TA_TILE; c0 += NB) {
+            uint32_t v[NB];
+#pragma unroll
+            for (int c = 0; c < NB; c += 32) tmem_ld32_async(sbuf + c0 + c, v + c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < NB; c += 32) tmem_arrived(v + c);
+            if constexpr (MASKED) {
+#pragma unroll
+              for (int y = 0; y < NB; ++y) v[y] = c0 + y < left ? v[y] : 0xff800000u;   // -inf
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int y = 0; y < NB; y += 8)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) m4[z] = ta_max3(m4[z], __uint_as_float(v[y + 2 * z]), __uint_as_float(v[y + 2 * z + 1]));
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const float top = mx == -INFINITY ? mx : mx * f;
             if (__any_sync(0xffffffffu, top + nref > lim)) {   // rare: the reference moves (nothing visible: it does not)
               const bool move = top + nref > lim;
@@ -411,7 +408,6 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
               lim = move ? Sh::GROW : lim;
               nref = now;
               sum *= fix;
-              tmem_st_wait();                           // the tile's weights so far are read back below
               if (i > 0) {
 #pragma unroll 1
                 for (int y = 0; y < D / 16; ++y) {
@@ -423,8 +419,9 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
                   tmem_st16(obuf + 16 * y, w);
                 }
               }
+              if (c0 > 0) tmem_st_wait();               // the tile's weights so far are read back
 #pragma unroll 1
-              for (int y = 0; y < c; ++y) {             // the tile's weights so far
+              for (int y = 0; y < c0 / 32; ++y) {
                 float o[16];
                 uint32_t w[16];
                 tmem_ld16(sbuf + 16 * y, o);
@@ -443,24 +440,26 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
                 }
                 tmem_st16(sbuf + 16 * y, w);
               }
-              tmem_st_wait();
             }
-            uint32_t w[16];
-            float2 acc = make_float2(0.f, 0.f);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 f2 = make_float2(f, f), n2 = make_float2(nref, nref);
 #pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])), f2, n2);
-              float2 e = make_float2(ta_exp2(z.x), ta_exp2(z.y));
-              if constexpr (MASKED) {
-                e.x = m >> (2 * y) & 1 ? e.x : 0.f;
-                e.y = m >> (2 * y + 1) & 1 ? e.y : 0.f;
+            for (int c = 0; c < NB; c += 32) {
+              uint32_t w[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[c + 2 * y]), __uint_as_float(v[c + 2 * y + 1])), f2, n2);
+                float2 e = make_float2(ta_exp2(z.x), ta_exp2(z.y));
+                if constexpr (MASKED) {                   // (a factor of zero makes NaN of -inf)
+                  e.x = c0 + c + 2 * y < left ? e.x : 0.f;
+                  e.y = c0 + c + 2 * y + 1 < left ? e.y : 0.f;
+                }
+                acc[y & 1] = __fadd2_rn(acc[y & 1], e);
+                w[y] = ta_pack(e.x, e.y, RAW16);
               }
-              acc = __fadd2_rn(acc, e);
-              w[y] = ta_pack(e.x, e.y, RAW16);
+              tmem_st16(sbuf + (c0 + c) / 2, w);          // P takes the place of S, behind the reads
             }
-            sum += acc.x + acc.y;
-            tmem_st16(sbuf + 16 * c, w);                // P takes the place of S, column by column behind the reads
+            sum += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
           }
         };
         if (left < TA_TILE) weigh(std::true_type{}); else weigh(std::false_type{});
@@ -477,8 +476,7 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
       }
       const size_t at = (size_t)s.slot * PX_ROWS + 128 * x + L;
       if (real) {
-        p.stats[(size_t)s.slot * (2 * PX_ROWS) + 128 * x + L] = lim == -INFINITY ? -INFINITY : -nref;
-        p.stats[(size_t)s.slot * (2 * PX_ROWS) + PX_ROWS + 128 * x + L] = sum;
+        ta_put_sector(p.stats + at * TA_STAT, lim == -INFINITY ? -INFINITY : -nref, sum);
       }
       if (n) {
         // natural element y of a chunk's columns (codes of 4 bits stand at another position inside each 8 elements)

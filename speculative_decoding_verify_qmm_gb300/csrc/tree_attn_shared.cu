@@ -6,125 +6,150 @@
 // at once (tree_attn_prefix.cu: its K and V are read once per 256 rows instead of once per request), and each request's own tokens
 // by the kernels of tree attention, told to skip the prefix's pages.  Both leave fp32 sums with their maximum and weight; the join
 // brings them together and rounds once.
+#include <algorithm>
+#include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "tree_attn_prefix.cuh"
 
 namespace sv {
 
-constexpr int TJ_WARPS = 8, TJ_AHEAD = 4;      // warps a CTA, parts of a row on their way at once
+// Cached tokens times key heads that requests need not read again, from which on two more launches pay (32 query and 8 key heads, apart and
+// together, us: 16 requests of a row over 1024 tokens 20.3 and 27.2, over 4096 37.3 and 32.5, over 16384 101 and 43; 4 of 8 rows over 8192
+// 31.6 and 42.2, over 16384 48.3 and 50.1, over 32768 81 and 71; 4-bit caches alike.  One key head: 16 of 8 rows over 32768 41 and 58).
+constexpr double PX_WORTH = 500000.0;
+constexpr double PX_BEGIN = 3.0, PX_PART = 0.3, PX_JOIN = 0.3;
+constexpr int TJ_WARPS = 8, TJ_CTAS = 4;       // warps a CTA, CTAs an SM
+constexpr int TJ_AHEAD = 4;                    // parts of a row on their way at once
 
-// One warp per (row, query head).  The parts of a row, in a fixed order: the prefix's, by CTA (two each where both matrices had the
-// same rows), then the own tokens', by CTA.  What is read goes back to zero.
+// One warp per (row, query head).  The parts of a row, in a fixed order: the prefix's, by tokens (two each where both matrices had the
+// same rows), then the own tokens', by CTA.  A lane finds one part's place, maximum and weight, so that all parts' sums are asked for
+// together, TJ_AHEAD at a time; what is read goes back to zero.  (A warp that went from part to part with all of its lanes: 44 us
+// against 28 us for 396 rows of 48 heads in eight parts.)
 template <int D>
-__global__ void __launch_bounds__(32 * TJ_WARPS) tree_attn_shared_join_kernel(const __grid_constant__ TreeAttnParams p,
-                                                                              const __grid_constant__ PrefixParams x) {
+__global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_kernel(const __grid_constant__ TreeAttnParams p,
+                                                                                       const __grid_constant__ PrefixParams x) {
   constexpr int E = D / 32;
+  using Vec = std::conditional_t<E == 4, float4, float2>;
   __shared__ TaPlan plan;
-  const int lane = threadIdx.x & 31;
+  // what is looked up by request and group: indexed reads of the launch parameters take hundreds of cycles each
+  __shared__ int s_offs[MAX_BATCH + 1];
+  __shared__ short s_group[MAX_BATCH];
+  __shared__ int s_rows[MAX_BATCH], s_row0[MAX_BATCH], s_pieces[MAX_BATCH], s_splits[MAX_BATCH];
+  const int lane = threadIdx.x & 31, B = p.map.B;
+  if (threadIdx.x >= 32)
+    for (int i = threadIdx.x - 32; i <= B; i += 32 * (TJ_WARPS - 1)) {
+      s_offs[i] = p.map.offs[i];
+      if (i < B) s_group[i] = x.group[i];
+      if (i < x.n) {
+        s_rows[i] = x.rows[i];
+        s_row0[i] = x.row0[i];
+        s_pieces[i] = x.pieces[i];
+        s_splits[i] = x.splits[i];
+      }
+    }
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 32) ta_plan(p, &plan, true, false);
   __syncthreads();
   const long long all = plan.pre[p.map.B], per = ta_div(all + p.grid - 1, p.grid);
-  const int heads = p.c.heads * p.group;
-  const long long pairs = (long long)p.map.offs[p.map.B] * heads;
-  for (long long id = (long long)blockIdx.x * TJ_WARPS + (threadIdx.x >> 5); id < pairs; id += (long long)gridDim.x * TJ_WARPS) {
-    const int row = (int)ta_div(id, heads), hq = (int)(id - (long long)row * heads), h = hq / p.group;
-    const int b = request_of(p.map, row), i = row - p.map.offs[b], m = p.map.offs[b + 1] - p.map.offs[b];
-    // the own tokens' parts
-    const int r = i * p.group + (hq - h * p.group), rb = r / p.block, k = r - rb * p.block;
-    const int nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT, cost = ta_cost(p, m);
-    const long long span = (long long)nt * cost;
-    const int local = h * ta_blocks(m * p.group, p.block) + rb, item = (b ? plan.items[b] : 0) + local;
-    const long long a0 = plan.pre[b] + (long long)local * (span + plan.begin);
+  const unsigned heads = p.c.heads * p.group, units = p.map.offs[p.map.B] * heads;
+  const int shift = 31 - __clz(p.block), x_all = x.pieces[x.n];   // (the block is a power of two)
+  for (unsigned id = blockIdx.x * TJ_WARPS + (threadIdx.x >> 5); id < units; id += gridDim.x * TJ_WARPS) {
+    const int row = (int)(id / heads), hq = (int)(id - row * heads), h = hq / p.group, hg = hq - h * p.group;
+    int b = 0;
+    for (int hi = B; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (s_offs[mid] <= row) b = mid; else hi = mid;
+    }
+    const int i = row - s_offs[b], m = s_offs[b + 1] - s_offs[b];
+    // own tokens
+    const int nt = (plan.len[b] + m + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT, cost = ta_cost(p, m), r = i * p.group + hg;
+    const int local = h * ta_blocks(m * p.group, p.block) + (r >> shift), k = r & (p.block - 1), item = (b ? plan.items[b] : 0) + local;
+    const long long span = (long long)nt * cost, a0 = plan.pre[b] + (long long)local * (span + plan.begin);
     const int c0 = (int)ta_div(a0 + plan.begin + cost - 1, per), c1 = (int)ta_div(a0 + plan.begin + span - 1, per);
-    // the prefix's
-    const int gi = x.group[b];
-    int xc0 = 0, xn = 0, xk = 0, xitem = 0, xcost = 1, xnt = 0, halves = 1;
-    long long xa0 = 0;
+    // the prefix
+    const int gi = s_group[b];
+    int xn = 0, xk = 0, xslot = 0, halves = 0;
     if (gi >= 0) {
-      const PxGroup g = px_group(x, x.rows[gi], x.tokens[gi]);
-      const int xr = (row - x.row0[gi]) * p.group + (hq - h * p.group), xrb = xr / PX_ROWS;
-      xk = xr - xrb * PX_ROWS;
-      const bool pair = xrb < g.blocks - 1 || g.last;
-      xcost = x.cost[pair];
-      xnt = g.nt;
-      xa0 = x.pre[gi] + h * g.span + xrb * g.full;
-      xitem = x.items[gi] + h * g.blocks + xrb;
-      halves = pair ? 1 : 2;
-      xc0 = (int)ta_div(xa0 + x.begin_cost + xcost - 1, x.per);
-      xn = ((int)ta_div(xa0 + x.begin_cost + (long long)xnt * xcost - 1, x.per) - xc0 + 1) * halves;
+      const int xr = (row - s_row0[gi]) * p.group + hg, xrb = xr / PX_ROWS;
+      xk = xr % PX_ROWS;
+      xslot = s_pieces[gi] + (h * px_blocks(s_rows[gi]) + xrb) * s_splits[gi];
+      halves = !px_pair(s_rows[gi], xrb);              // two parts a piece, as a shift
+      xn = s_splits[gi] << halves;
     }
     const int n = xn + c1 - c0 + 1;
     float acc[E] = {}, weight = 0.f, most = -INFINITY;
-    for (int j0 = 0; j0 < n; j0 += TJ_AHEAD) {
-      float *sums[TJ_AHEAD], *stat[TJ_AHEAD];
-      int step[TJ_AHEAD];
-      float st[TJ_AHEAD], wt[TJ_AHEAD], v[TJ_AHEAD][E];
-#pragma unroll
-      for (int y = 0; y < TJ_AHEAD; ++y) {
-        const int j = j0 + y;
-        sums[y] = nullptr;
-        if (j < xn) {
-          const int c = xc0 + j / halves;
-          const long long lo = (long long)c * x.per;
-          if (ta_units_before(lo + x.per, xa0, xnt, xcost, x.begin_cost) > ta_units_before(lo, xa0, xnt, xcost, x.begin_cost)) {
-            const size_t slot = (size_t)xitem + c;
-            const int kk = xk + (halves == 2 ? (j & 1) * 128 : 0);
-            sums[y] = x.partial + (slot * PX_ROWS + kk) * D;
-            stat[y] = x.stats + slot * (2 * PX_ROWS) + kk;
-            step[y] = PX_ROWS;
-          }
-        } else if (j < n) {
-          const int c = c0 + j - xn;
-          const long long lo = (long long)c * per;
-          if (ta_units_before(lo + per, a0, nt, cost, plan.begin) > ta_units_before(lo, a0, nt, cost, plan.begin)) {
-            const size_t slot = (size_t)item + c;
-            sums[y] = p.partial + (slot * p.block + k) * D;
-            stat[y] = p.stats + 2 * slot * p.block + k;
-            step[y] = p.block;
-          }
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const int j = j0 + lane;
+      unsigned place = 0;                              // row of the sums: in the prefix's, or the own tokens'
+      float st = -INFINITY, wt = 0.f;
+      float* at = nullptr;
+      if (j < xn) {
+        // a piece that another of its item and CTA comes before has no sums of its own
+        const int piece = xslot + (j >> halves);
+        if (piece == xslot || px_cta(x_all, x.grid, piece) != px_cta(x_all, x.grid, piece - 1)) {
+          place = piece * PX_ROWS + xk + (halves ? (j & 1) * 128 : 0);
+          at = x.stats + (size_t)place * TA_STAT;
         }
-        st[y] = -INFINITY;
-        wt[y] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[y][e] = 0.f;
-        if (sums[y]) {
-          st[y] = stat[y][0];
-          wt[y] = stat[y][step[y]];
-          if constexpr (E == 4) {
-            const float4 t = reinterpret_cast<const float4*>(sums[y])[lane];
-            v[y][0] = t.x; v[y][1] = t.y; v[y][2] = t.z; v[y][3] = t.w;
-          } else {
-            const float2 t = reinterpret_cast<const float2*>(sums[y])[lane];
-            v[y][0] = t.x; v[y][1] = t.y;
-          }
+      } else if (j < n) {
+        const int c = c0 + j - xn;
+        const long long lo = (long long)c * per;
+        if (ta_units_before(lo + per, a0, nt, cost, plan.begin) > ta_units_before(lo, a0, nt, cost, plan.begin)) {
+          place = (item + c) * p.block + k;
+          at = p.stats + (size_t)place * TA_STAT;
         }
       }
-      __syncwarp();                      // every lane has the statistics
-      float top = most;
-#pragma unroll
-      for (int y = 0; y < TJ_AHEAD; ++y) {
-        top = fmaxf(top, st[y]);
-        if (!sums[y]) continue;
-        if constexpr (E == 4) reinterpret_cast<float4*>(sums[y])[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-        else reinterpret_cast<float2*>(sums[y])[lane] = make_float2(0.f, 0.f);
-        if (lane < 2) stat[y][lane * step[y]] = 0.f;
+      if (at) {
+        const float2 both = *reinterpret_cast<const float2*>(at);
+        st = both.x;
+        wt = both.y;
       }
-      const float base = top == -INFINITY ? 0.f : top, fix = ta_exp2(most - base);
-      weight *= fix;
+      float top = fmaxf(most, st);
+#pragma unroll
+      for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float base = top == -INFINITY ? 0.f : top, fix = ta_exp2(most - base), w = ta_exp2(st - base);
+      float sum = wt * w;
+#pragma unroll
+      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      weight = weight * fix + sum;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= fix;
-#pragma unroll
-      for (int y = 0; y < TJ_AHEAD; ++y) {
-        const float w = ta_exp2(st[y] - base);
-        weight += wt[y] * w;
-        // a part without weights may not have written its sums
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += st[y] == -INFINITY ? 0.f : v[y][e] * w;
-      }
       most = top;
+      unsigned parts = __ballot_sync(0xffffffffu, at != nullptr);
+      while (parts) {
+        Vec v[TJ_AHEAD];
+        const unsigned now = parts;                    // the next TJ_AHEAD of them
+#pragma unroll
+        for (int y = 0; y < TJ_AHEAD; ++y) {
+          const int src = parts ? __ffs(parts) - 1 : 0;
+          const unsigned row_at = __shfl_sync(0xffffffffu, place, src);
+          v[y] = Vec{};
+          // (a part without weights may not have written its sums)
+          if (parts && __shfl_sync(0xffffffffu, st, src) != -INFINITY)
+            v[y] = reinterpret_cast<const Vec*>((j0 + src < xn ? x.partial : p.partial) + (size_t)row_at * D)[lane];
+          parts &= parts - 1;
+        }
+        unsigned done = now;
+#pragma unroll
+        for (int y = 0; y < TJ_AHEAD; ++y) {
+          const int src = done ? __ffs(done) - 1 : 0;
+          const unsigned row_at = __shfl_sync(0xffffffffu, place, src);
+          const float f = __shfl_sync(0xffffffffu, w, src);
+          if (!done) break;
+          acc[0] += v[y].x * f;
+          acc[1] += v[y].y * f;
+          if constexpr (E == 4) {
+            acc[2] += v[y].z * f;
+            acc[3] += v[y].w * f;
+          }
+          const bool pre = j0 + src < xn;
+          reinterpret_cast<Vec*>((pre ? x.partial : p.partial) + (size_t)row_at * D)[lane] = Vec{};
+          if (lane < 2) reinterpret_cast<float4*>((pre ? x.stats : p.stats) + (size_t)row_at * TA_STAT)[lane] = float4{};   // a whole sector
+          done &= done - 1;
+        }
+      }
     }
     __nv_bfloat16* dst = p.out + (size_t)row * p.ldo + hq * D + lane * E;
 #pragma unroll
@@ -135,8 +160,8 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_attn_shared_join_kernel(co
 }
 
 // ------------------------------------------------------------------ host side
-// What a call shares: the groups whose prefix is worth a pass of its own, and the sizes of the sums.  A group of one request has nothing
-// to share: its prefix stays with the request.
+// What a call shares, and the sizes of the sums.  A group of one request has nothing to share: its prefix stays with the request, and
+// so do all where there is little to save.
 struct SharedSizes {
   size_t partial, stats, px_partial, px_stats, total;
 };
@@ -152,15 +177,16 @@ static int shared_plan(const KvCache& c, const RowMap& map, int G, const int32_t
       return fail(SV_EINVAL, "shared_pages[%d] must be in [0, 2^30 / page_size] (got %d)", g, shared_pages[g]);
   const int sms = ta_sms(), heads_per = n_q_heads / c.heads;
   x->heads_per = heads_per;
-  x->cost[0] = 6;
-  x->cost[1] = 10;
-  x->begin_cost = 40;
   x->n = 0;
-  for (int b = 0; b < map.B; ++b) {
-    skip[b] = 0;
-    x->group[b] = -1;
-  }
-  long long items = 0;
+  double saved = 0.0;
+  auto alone = [&] {                     // every request attends to all of its tokens
+    x->n = 0;
+    for (int b = 0; b < map.B; ++b) {
+      skip[b] = 0;
+      x->group[b] = -1;
+    }
+  };
+  alone();
   for (int g = 0; g < G; ++g) {
     int first = -1, with_rows = 0;
     for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
@@ -169,33 +195,64 @@ static int shared_plan(const KvCache& c, const RowMap& map, int G, const int32_t
         ++with_rows;
       }
     if (with_rows < 2 || !shared_pages[g]) continue;
+    saved += (double)(with_rows - 1) * ((long long)shared_pages[g] << c.page_shift) * c.heads;
     const int i = x->n++;
     x->row0[i] = map.offs[group_offsets[g]];
     x->rows[i] = (map.offs[group_offsets[g + 1]] - x->row0[i]) * heads_per;
     x->tokens[i] = shared_pages[g] << c.page_shift;
     x->request[i] = first;
-    const PxGroup s = px_group(*x, x->rows[i], x->tokens[i]);
-    x->pre[i + 1] = x->pre[i] + c.heads * s.span;
-    items += (long long)c.heads * s.blocks;
-    x->items[i + 1] = (int)items;
     for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b) {
       skip[b] = shared_pages[g];
       x->group[b] = (short)i;
     }
   }
+  if (saved < PX_WORTH) alone();
   memset(z, 0, sizeof(*z));
   z->total = ta_workspace_bytes(c);
   if (!x->n) return SV_OK;
-  x->grid = x->pre[x->n] < sms ? (int)x->pre[x->n] : sms;
-  x->per = (x->pre[x->n] + x->grid - 1) / x->grid;
+  // Pieces: of the numbers that come to up to twelve a CTA, the one that ends first, in tiles' time, where beginning and ending a run takes
+  // as long as PX_BEGIN tiles, and the join of another part of every row PX_PART of them and PX_JOIN a thousand rows and query heads.
+  auto cut = [&](double target) {        // tiles of a piece -> pieces
+    int all = 0;
+    x->pieces[0] = 0;
+    for (int i = 0; i < x->n; ++i) {
+      const int nt = px_tiles(x->tokens[i]), s = (int)(nt / target + 0.5);
+      x->splits[i] = s < 1 ? 1 : (s > nt ? nt : s);
+      all += c.heads * px_blocks(x->rows[i]) * x->splits[i];
+      x->pieces[i + 1] = all;
+    }
+    return all;
+  };
+  double work = 0.0, rows = 0.0, best = 0.0, best_cost = 1e30;
+  for (int i = 0; i < x->n; ++i) {
+    work += (double)c.heads * px_blocks(x->rows[i]) * px_tiles(x->tokens[i]);
+    rows += (double)c.heads * x->rows[i];
+  }
+  for (int each = -4; each <= 12; ++each)    // pieces a CTA, or (below 1) CTAs without one
+    for (int less = 0; less < 2; ++less) {   // a little less than that many, or a little more
+      const double many = each < 1 ? 0.5 / (1 << -each) : each, target = std::max(1.0, work / (many * sms) * (less ? 1.06 : 1.0));
+      const int all = cut(target), most = (all + sms - 1) / sms;
+      double longest = 0.0, parts = 0.0;
+      for (int i = 0; i < x->n; ++i) {
+        longest = std::max(longest, std::ceil((double)px_tiles(x->tokens[i]) / x->splits[i]));
+        parts = std::max(parts, (1.0 + (double)(x->splits[i] - 1) / most) * (px_pair(x->rows[i], px_blocks(x->rows[i]) - 1) ? 1 : 2));
+      }
+      const double cost = most * longest + PX_BEGIN * (1.0 + (most - 1) / (double)x->splits[0]) + (PX_PART + PX_JOIN * 1e-3 * rows) * parts;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = target;
+      }
+    }
+  const int items = cut(best);
+  x->grid = items < sms ? items : sms;
   int block;
   ta_choose_block(map, heads_per, &block);
   size_t own = sms;                              // runs of own tokens: one per item and CTA
   for (int b = 0; b < map.B; ++b) own += (size_t)c.heads * ta_blocks((map.offs[b + 1] - map.offs[b]) * heads_per, block);
   z->partial = align256(own * block * c.dim * sizeof(float));
-  z->stats = align256(own * block * 2 * sizeof(float));
-  z->px_partial = align256((items + sms) * PX_ROWS * c.dim * sizeof(float));
-  z->px_stats = align256((items + sms) * PX_ROWS * 2 * sizeof(float));
+  z->stats = align256(own * block * TA_STAT * sizeof(float));
+  z->px_partial = align256((size_t)items * PX_ROWS * c.dim * sizeof(float));
+  z->px_stats = align256((size_t)items * PX_ROWS * TA_STAT * sizeof(float));
   const size_t need = z->partial + z->stats + z->px_partial + z->px_stats;
   if (need > z->total) z->total = need;
   return SV_OK;
@@ -214,8 +271,6 @@ size_t sv_tree_attention_shared_workspace_bytes(const sv_kv_cache* cache, int G,
   PrefixParams x;
   int skip[MAX_BATCH];
   SharedSizes z;
-  x.pre[0] = 0;
-  x.items[0] = 0;
   if (ta_check_batch(cache, B, row_offsets, n_q_heads, &c, &m) || shared_plan(c, m, G, group_offsets, shared_pages, n_q_heads, &x, skip, &z)) return 0;
   return z.total;
 }
@@ -265,7 +320,7 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
   bool one_unit;
   st = ta_launch(&p, s, &one_unit);
   if (st) return st;
-  const long long pairs = (long long)p.map.offs[B] * n_q_heads, ctas = (pairs + TJ_WARPS - 1) / TJ_WARPS, most = 8ll * ta_sms();
+  const long long units = (long long)p.map.offs[B] * n_q_heads, ctas = (units + TJ_WARPS - 1) / TJ_WARPS, most = (long long)TJ_CTAS * ta_sms();
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(ctas < most ? ctas : most)), dim3(32 * TJ_WARPS), 0, s, attr);
   e = p.c.dim == 128 ? cudaLaunchKernelEx(&cfg, tree_attn_shared_join_kernel<128>, p, x) : cudaLaunchKernelEx(&cfg, tree_attn_shared_join_kernel<64>, p, x);

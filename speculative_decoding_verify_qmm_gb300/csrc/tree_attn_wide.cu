@@ -554,8 +554,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
       const float own = ta_exp2(ref - base);
       const float factor = whole ? (weight == 0.f ? 0.f : own / weight) : own;
       if (!whole && grp == 0 && rr < s.rows) {
-        p.stats[(2 * slot) * p.block + rr] = most;
-        p.stats[(2 * slot + 1) * p.block + rr] = weight;
+        ta_put_stats(p, slot, rr, most, weight);
       }
       // natural element y of a chunk's columns (codes of 4 bits stand at another position inside each 8 elements)
       auto col = [](int d) { return BITS == 4 ? (d & ~7) + 2 * (d & 3) + ((d >> 2) & 1) : d; };
