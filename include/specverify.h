@@ -474,8 +474,9 @@ int sv_kv_commit(const sv_kv_cache* layers, int n_layers, int B, const int32_t* 
  * hold the same (which request's entries are read is not specified).  Every
  * request of the group with rows has kv_len >= shared_pages * page_size: the shared
  * tokens are committed and visible to all its rows.  A smaller kv_len is bad
- * input: that request's output is undefined.  A group of one request, or
- * without shared pages, is the plain case, and no groups are ever mixed.
+ * input: that request's output is undefined.  Where sharing saves little (over all
+ * groups, the requests with rows but one, times shared tokens, times key heads, come to
+ * less than 500,000) the call is sv_tree_attention.
  * The formulas, formats and rules of sv_tree_attention hold; sums run in another
  * order.  Prefix tokens are read once per 256 rows (drafted rows of the whole group
  * times query heads per key head).  A captured call keeps the groups and shared_pages it
@@ -550,8 +551,8 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
  * source may be named many times; a page that is named twice as dst, or as
  * dst and as src of one cache, ends up with either content, or parts of both.
  * An index out of range is bad input: that copy is not made.
- * In all of these no cache may be listed twice, nor one layer's source be another
- * layer's destination. */
+ * In all of these the caches are alike in sizes and bits, no cache may be listed
+ * twice, and no layer's source be another layer's destination. */
 typedef struct {
   int32_t* refs;
   int32_t* block_table;

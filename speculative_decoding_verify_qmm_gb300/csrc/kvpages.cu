@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) kv_reserve_kernel(const __grid_
     s_part[tid] = part;
     s_asks[tid] = s_copy[tid] = -1;
     s_bad[tid] = 0;
+    if (tid < g.slots) p.before[tid] = 0;             // the workspace may hold anything; the next launch looks at every slot
   }
   int entries;
   const int mine = block_scan(look, &entries);
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) kv_reserve_kernel(const __grid_
   }
   if (tid < g.slots && s_first[tid] >= 0 && !s_bad[tid]) {
     g.held[tid] = s_wants[tid];
-    p.before[tid] = s_has[tid] > s_wants[tid] ? s_has[tid] : 0;
+    if (s_has[tid] > s_wants[tid]) p.before[tid] = s_has[tid];
   }
   if (tid == 0) {
     p.counts[0] = 0;
