@@ -603,7 +603,7 @@ class Library:
                 _vector("path", path, i32, dev, 0)]
         ws, size = (None, 0) if workspace is None else self._workspace(workspace, None, logits.device, dev, stream)
         status = self.lib.sv_tree_accept(B, offs, logits.data_ptr(), ldl, *ptrs, None if q is None else q.data_ptr(), ldq,
-                                         bool(distinct), V, float(temperature), up, int(top_k), float(top_p), *outs,
+                                         bool(distinct), V, float(temperature), up, max(-1, min(int(top_k), _INT_MAX)), float(top_p), *outs,
                                          path.shape[1], None if ws is None else ws.data_ptr(), size, handle)
         if status:
             self.check(status)

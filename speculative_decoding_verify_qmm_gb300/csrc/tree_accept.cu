@@ -84,7 +84,8 @@ __device__ __forceinline__ u64 tv_shift(u64 x, int s) {
   return r;
 }
 // exp((z - top) / T) in units of 2^-40, off by about one unit at most; 0 for -inf and NaN.  The exponent y = (z - top) log2(e) / T is held
-// in two floats (the difference and the product exactly), y = N / 128 + r: 2^(N/128) from the table, 2^r - 1 as g + g^2/2 + g^3/6 +
+// in two floats (the difference and the product exactly), y = N / 128 + r as in P. Tang's table-driven exponential (ACM TOMS 15, 1989):
+// 2^(N/128) from the table, 2^r - 1 as g + g^2/2 + g^3/6 +
 // g^4/24 of g = r ln 2, |g| < 2^-8.5, its first term and the result in two floats too.  Without branches: these would keep one element's
 // chain from running beside another's.
 __device__ __forceinline__ u64 tv_weight(float z, float top, float ch, float cl, const float2* table) {
