@@ -1,5 +1,5 @@
 // Attention of the drafted rows over the paged cache: the entry point, and the join of items that spanned CTAs (the kernel
-// itself is tree_attn_narrow.cu up to 32 rows and tree_attn_wide.cu above).
+// itself is tree_attn_narrow.cuh up to 32 rows and tree_attn_wide.cu above).
 #include <cmath>
 #include <cstddef>
 #include <cstring>
@@ -216,8 +216,9 @@ int ta_encode(const KvCache& c, CUtensorMap* tk, CUtensorMap* tv) {
   return st ? st : encode_tiled_3d_sw128(tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.p.v, c.dim, page, slabs, 2, 64, box);
 }
 
-int ta_launch(TreeAttnParams* out, cudaStream_t s, bool* one_unit) {
-  TreeAttnParams& p = *out;
+template <typename P>
+int ta_launch(P* out, cudaStream_t s, bool* one_unit) {
+  P& p = *out;
   const bool narrow = ta_choose_block(p.map, p.group, &p.block);
   // Beginning an item, in the same measure: what gave the least time over several batches and lengths.  (Wide, bf16, 32 rows of
   // 65536 tokens: 60.8 us with 30, 59.0 with 60; 4 x 8 rows in 48 heads 68.0 and 64.2, over codes 54.8 and 56.1.  Narrow, 8-bit,
@@ -230,7 +231,7 @@ int ta_launch(TreeAttnParams* out, cudaStream_t s, bool* one_unit) {
   *one_unit = true;
   for (int b = 0; b < p.map.B; ++b) {
     const int m = p.map.offs[b + 1] - p.map.offs[b];
-    const long long places = (long long)(p.table_pages - p.skip[b]) << p.c.page_shift;
+    const long long places = (long long)(p.table_pages - ta_skip(p, b)) << p.c.page_shift;
     if (m > places) return fail(SV_EINVAL, "request %d has more rows than block_table has places", b);
     const long long units = (places + (1 << TA_UNIT_SHIFT) - 1) >> TA_UNIT_SHIFT;
     most += (long long)p.c.heads * ta_blocks(m * p.group, p.block) * units;
@@ -245,6 +246,8 @@ int ta_launch(TreeAttnParams* out, cudaStream_t s, bool* one_unit) {
   const cudaError_t e = narrow ? launch_tree_attn_narrow(p, s) : launch_tree_attn_wide(p, s);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "tree attention launch");
 }
+template int ta_launch(TreeAttnParams*, cudaStream_t, bool*);
+template int ta_launch(TreeAttnOwnParams*, cudaStream_t, bool*);
 
 template <int D, int WPP, int PAIRS>
 static cudaError_t launch_join_w(const TreeAttnParams& p, long long pairs, long long most, cudaStream_t s) {

@@ -33,10 +33,15 @@ struct TreeAttnParams {
   int block;                 // rows (drafted row x query head of the group) per item
   int cost[2];               // of a unit with up to 16 rows, and with more
   int begin_cost;            // of beginning an item
-  // of a call over shared prefixes: the pages in front of each request's own tokens, which another kernel attends to, and whether
-  // every part is left for the join
+  static constexpr bool KEEP = false;
+};
+
+// Of a call over shared prefixes: the pages in front of each request's own tokens, which another kernel attends to; every part is left for
+// that call's join.  (Kernels of their own: where the plain ones asked which call it is, one request of 8 rows over 16384 tokens took 22.7 us
+// instead of 22.1, and 48 of 1 to 5 rows over up to 12007 tokens 165 instead of 159.)
+struct TreeAttnOwnParams : TreeAttnParams {
   int skip[MAX_BATCH];
-  int keep;
+  static constexpr bool KEEP = true;
 };
 
 // A part's maximum and weight of row k: beside those of the other rows, or (where every part is left for the join) in a sector of their
@@ -47,8 +52,9 @@ __device__ __forceinline__ void ta_put_sector(float* at, float most, float weigh
   reinterpret_cast<float4*>(at)[0] = make_float4(most, weight, 0.f, 0.f);
   reinterpret_cast<float4*>(at)[1] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
-__device__ __forceinline__ void ta_put_stats(const TreeAttnParams& p, size_t slot, int k, float most, float weight) {
-  if (p.keep) {
+template <typename P>
+__device__ __forceinline__ void ta_put_stats(const P& p, size_t slot, int k, float most, float weight) {
+  if constexpr (P::KEEP) {
     ta_put_sector(p.stats + (slot * p.block + k) * TA_STAT, most, weight);
   } else {
     p.stats[2 * slot * p.block + k] = most;
@@ -56,8 +62,14 @@ __device__ __forceinline__ void ta_put_stats(const TreeAttnParams& p, size_t slo
   }
 }
 
-// Of request b: the table's entries of its own tokens.
-__device__ __forceinline__ const int32_t* ta_table(const TreeAttnParams& p, int b) { return p.table + (size_t)b * p.table_pages + p.skip[b]; }
+// Of request b: pages in front of its own tokens, and the table's entries behind them.
+template <typename P>
+__host__ __device__ __forceinline__ int ta_skip(const P& p, int b) {
+  if constexpr (P::KEEP) return p.skip[b];
+  else return 0;
+}
+template <typename P>
+__device__ __forceinline__ const int32_t* ta_table(const P& p, int b) { return p.table + (size_t)b * p.table_pages + ta_skip(p, b); }
 
 // What every CTA derives from the lengths: prefix sums of units.
 struct TaPlan {
@@ -72,7 +84,8 @@ __host__ __device__ __forceinline__ int ta_blocks(int rows, int block) { return 
 __device__ __forceinline__ int ta_cost(const TreeAttnParams& p, int m) { return p.cost[m * p.group > 16]; }
 
 // By one warp; `real` false: with lengths of zero, which reads nothing.
-__device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, bool real, bool report) {
+template <typename P>
+__device__ __forceinline__ void ta_plan(const P& p, TaPlan* plan, bool real, bool report) {
   const int lane = threadIdx.x & 31;
   const RowMap& map = p.map;
   long long run = 0;             // of the units' cost
@@ -83,8 +96,9 @@ __device__ __forceinline__ void ta_plan(const TreeAttnParams& p, TaPlan* plan, b
     int n = 0;
     if (b < map.B) {
       const int m = map.offs[b + 1] - map.offs[b];
-      const long long cap = (long long)(p.table_pages - p.skip[b]) << p.c.page_shift;   // at least the request's rows (checked by the host)
-      long long len = real ? p.kv_len[b] - ((long long)p.skip[b] << p.c.page_shift) : 0;
+      const int skip = ta_skip(p, b);
+      const long long cap = (long long)(p.table_pages - skip) << p.c.page_shift;   // at least the request's rows (checked by the host)
+      long long len = real ? p.kv_len[b] - ((long long)skip << p.c.page_shift) : 0;
       if (m && (len < 0 || len + m > cap)) {
         if (report) raise_error(ERR_BAD_INPUT);
         len = len < 0 ? 0 : cap - m;
@@ -184,7 +198,8 @@ struct TaShare {
 // By the whole CTA, up to and past its wait for the kernels before.  Lengths may be those kernels' results, but the same
 // instructions are run once before the wait, on lengths of zero: they are in the caches when it counts.  (A first run of the
 // planning takes 2.5 us; with the dry run before it one row over 2048 tokens takes 9.4 us against 10.3.)
-__device__ __forceinline__ TaShare ta_begin(const TreeAttnParams& p, TaPlan* plan) {
+template <typename P>
+__device__ __forceinline__ TaShare ta_begin(const P& p, TaPlan* plan) {
   TaShare x;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -246,9 +261,11 @@ __device__ __forceinline__ bool ta_half_bad(uint32_t h) { return (h & 0x7c00u) =
 
 // Whether a run is written to the output at once, and where it leaves its partial sums otherwise.  Where every run leaves them, item plus
 // CTA tells runs apart: neither goes down from run to run, and one of them goes up.
-__device__ __forceinline__ bool ta_whole(const TreeAttnParams& p, const TaSeg& s) { return s.n == s.nt && !p.keep; }
-__device__ __forceinline__ size_t ta_slot(const TreeAttnParams& p, const TaSeg& s) {
-  return p.keep ? (size_t)s.item + blockIdx.x : 2 * (size_t)blockIdx.x + (s.first ? 0 : 1);
+template <typename P>
+__device__ __forceinline__ bool ta_whole(const P&, const TaSeg& s) { return s.n == s.nt && !P::KEEP; }
+template <typename P>
+__device__ __forceinline__ size_t ta_slot(const P&, const TaSeg& s) {
+  return P::KEEP ? (size_t)s.item + blockIdx.x : 2 * (size_t)blockIdx.x + (s.first ? 0 : 1);
 }
 
 // Host side.  Checks of a batch; the same workspace for every batch; the rows per block (16, 32, or 128 of the tensor-memory kernel:
@@ -261,10 +278,13 @@ bool ta_choose_block(const RowMap& map, int group, int* block);
 int ta_check_call(TreeAttnParams* p, const int32_t* kv_len, const int32_t* block_table, int table_pages, const uint16_t* q, int ldq,
                   int n_q_heads, float scale, const uint64_t* tree_mask, uint16_t* to, int ldo);
 int ta_encode(const KvCache& c, CUtensorMap* tk, CUtensorMap* tv);     // tensor maps of a 16-bit cache
-// The kernel for p's rows (partial, stats, skip and keep are set).  one_unit: no item can have more than one unit.
-int ta_launch(TreeAttnParams* p, cudaStream_t s, bool* one_unit);
+// The kernel for p's rows (partial and stats are set, and skip).  one_unit: no item can have more than one unit.
+template <typename P>
+int ta_launch(P* p, cudaStream_t s, bool* one_unit);
 
 cudaError_t launch_tree_attn_wide(const TreeAttnParams& p, cudaStream_t s);     // blocks of 128 rows
+cudaError_t launch_tree_attn_wide(const TreeAttnOwnParams& p, cudaStream_t s);
 cudaError_t launch_tree_attn_narrow(const TreeAttnParams& p, cudaStream_t s);   // of 16 or 32
+cudaError_t launch_tree_attn_narrow(const TreeAttnOwnParams& p, cudaStream_t s);
 
 }  // namespace sv

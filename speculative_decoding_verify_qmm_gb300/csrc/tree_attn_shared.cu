@@ -28,7 +28,7 @@ constexpr int TJ_AHEAD = 4;                    // parts of a row on their way at
 // together, TJ_AHEAD at a time; what is read goes back to zero.  (A warp that went from part to part with all of its lanes: 44 us
 // against 28 us for 396 rows of 48 heads in eight parts.)
 template <int D>
-__global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_kernel(const __grid_constant__ TreeAttnParams p,
+__global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_kernel(const __grid_constant__ TreeAttnOwnParams p,
                                                                                        const __grid_constant__ PrefixParams x) {
   constexpr int E = D / 32;
   using Vec = std::conditional_t<E == 4, float4, float2>;
@@ -279,7 +279,7 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
                              const int32_t* row_offsets, const int32_t* kv_len, const int32_t* block_table, int table_pages,
                              const uint16_t* q, int ldq, int n_q_heads, float scale, const uint64_t* tree_mask, uint16_t* out, int ldo,
                              void* workspace, size_t workspace_bytes, void* stream) {
-  TreeAttnParams p;
+  TreeAttnOwnParams p;
   PrefixParams x;
   SharedSizes z;
   memset(static_cast<void*>(&p), 0, sizeof(p));
@@ -299,7 +299,6 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.partial = reinterpret_cast<float*>(ws);
   p.stats = reinterpret_cast<float*>(ws + z.partial);
-  p.keep = 1;
   x.partial = reinterpret_cast<float*>(ws + z.partial + z.stats);
   x.stats = reinterpret_cast<float*>(ws + z.partial + z.stats + z.px_partial);
   x.c = p.c;

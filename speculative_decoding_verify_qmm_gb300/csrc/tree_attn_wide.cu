@@ -77,8 +77,8 @@ __device__ __forceinline__ bool ta_item(int e, int n, int* tile) {
 // Tiles whose V the transforming warps look through: those with drafted tokens or past the end.
 __device__ __forceinline__ bool ta_fixed(const TaSeg& s, int j) { return (s.tile0 + j + 1) * TA_TILE > s.len; }
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_kernel(const __grid_constant__ TreeAttnParams p) {
+template <int D, int BITS, typename P>
+__global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_kernel(const __grid_constant__ P p) {
   using Sh = TaShape<D, BITS>;
   constexpr bool RAW16 = BITS == 16;
   extern __shared__ uint8_t smem_raw[];
@@ -653,20 +653,24 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
   }
 }
 
-template <int D, int BITS>
-static cudaError_t launch_wide(const TreeAttnParams& p, cudaStream_t s) {
+template <int D, int BITS, typename P>
+static cudaError_t launch_wide(const P& p, cudaStream_t s) {
   using Sh = TaShape<D, BITS>;
-  const cudaError_t e = cudaFuncSetAttribute(tree_attn_wide_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(tree_attn_wide_kernel<D, BITS, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pdl_config(dim3(p.grid), dim3(Sh::THREADS), Sh::SMEM, s, attr);
-  return cudaLaunchKernelEx(&cfg, tree_attn_wide_kernel<D, BITS>, p);
+  return cudaLaunchKernelEx(&cfg, tree_attn_wide_kernel<D, BITS, P>, p);
 }
 
-cudaError_t launch_tree_attn_wide(const TreeAttnParams& p, cudaStream_t s) {
+template <typename P>
+static cudaError_t launch_wide_any(const P& p, cudaStream_t s) {
   if (p.c.dim == 128)
     return p.c.bits == 16 ? launch_wide<128, 16>(p, s) : (p.c.bits == 8 ? launch_wide<128, 8>(p, s) : launch_wide<128, 4>(p, s));
   return p.c.bits == 16 ? launch_wide<64, 16>(p, s) : (p.c.bits == 8 ? launch_wide<64, 8>(p, s) : launch_wide<64, 4>(p, s));
 }
+
+cudaError_t launch_tree_attn_wide(const TreeAttnParams& p, cudaStream_t s) { return launch_wide_any(p, s); }
+cudaError_t launch_tree_attn_wide(const TreeAttnOwnParams& p, cudaStream_t s) { return launch_wide_any(p, s); }
 
 }  // namespace sv
