@@ -672,6 +672,7 @@ __global__ void __launch_bounds__(TnShape<D, BITS, MT>::THREADS, 1) tree_attn_na
       __syncthreads();
     }
   }
+  ta_end(p);
 }
 
 template <int D, int BITS, int MT, typename P>

@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
     tc05_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  ta_end(p);
 }
 
 template <int D, int BITS, typename P>
