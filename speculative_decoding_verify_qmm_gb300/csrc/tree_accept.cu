@@ -13,6 +13,10 @@
 // with its slice of the vocabulary (E kept in shared memory), all of them take the same decisions from the same numbers, and
 // meet only where a sum is needed.  What the tests need of every node is asked for at once before the walk begins.
 //
+// Measured (vocabulary 151936, in a graph): one tree of 32 nodes with the head's statistics 24 us; 24 trees of up to 64 nodes from raw logits
+// 95 to 118 (alone, the longest walks among them take 57 to 61: a node some 8 us, a rejection 4, of which an exchange between CTAs is 1.5); 8
+// trees of 24 nodes, truncated to 64 tokens, 42 to 55; 4 greedy trees of 16 nodes 9.8.  How long a walk is lies in the uniforms.
+//
 // Weights are 64-bit integers in units of 2^-40: their sums do not depend on any order, a draw compares integers, and the
 // cumulative sums are exact to some 2^-40 of the largest weight, where sums of fp32 terms (2^-24) would choose another token than
 // the formula for one draw in some hundreds over a flat distribution.

@@ -11,6 +11,13 @@
 // exponentials a warpgroup.  A block of up to 128 rows puts the same rows into both matrices and gives each every other tile: two
 // independent sums over half of the tokens.
 //
+// Bound by the softmax warps where rows fill the matrices: a tile of 128 tokens takes a pair of matrices some 3500 cycles over a 16-bit cache
+// (two exponentials of 32 a cycle and SM would be 1024, the products alone 2048), 1390 TFLOP/s or 0.74 of the measured rate; over codes, where
+// transforming warps share the issue slots, 5600 cycles, 870 TFLOP/s.  (32 query and 8 key heads of 128: 512 rows a key head behind 16384
+// tokens of an 8-bit cache 50 us.)  Few rows are bound by memory and latency: 256 rows a key head behind 8016 tokens of a 4-bit cache 30 us.
+// No gain: two softmax warps a row (S is read twice as often for a maximum), an issuing warp for each matrix, scores asked for a step
+// ahead, 128 scores of a row at once, five operand tiles.  Waits that spin without a time limit in the instruction cost 25 %.
+//
 // S, S, O and O fill the tensor memory (512 columns at 128 elements); Q is therefore read from shared memory.  The references and the
 // formats of the weights are those of tree attention's tensor-core kernel.  16-bit caches come by TMA (the tail of a last tile reads as
 // zeros: its page lies outside the tensor), codes through two teams of transforming warps.
