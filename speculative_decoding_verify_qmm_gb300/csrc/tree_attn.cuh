@@ -48,9 +48,14 @@ struct TreeAttnOwnParams : TreeAttnParams {
 // own, written whole.  Writes of parts of sectors are slow where other SMs read and write the rest: a join that put 150 thousand of
 // them back to zero took 44 to 130 us, with whole sectors 28.
 constexpr int TA_STAT = 8;                         // floats of a sector
+__device__ __forceinline__ void ta_store8(float* at, const uint32_t* v) {   // 32 bytes, a sector
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void ta_put_sector(float* at, float most, float weight) {
-  reinterpret_cast<float4*>(at)[0] = make_float4(most, weight, 0.f, 0.f);
-  reinterpret_cast<float4*>(at)[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const uint32_t v[8] = {__float_as_uint(most), __float_as_uint(weight)};
+  ta_store8(at, v);
 }
 template <typename P>
 __device__ __forceinline__ void ta_put_stats(const P& p, size_t slot, int k, float most, float weight) {

@@ -494,8 +494,12 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
           tmem_ld32(obuf + 32 * c, o);
           if (!real) continue;
 #pragma unroll
-          for (int y = 0; y < 32; y += 4)
-            *reinterpret_cast<uint4*>(p.partial + at * D + 32 * c + y) = make_uint4(o[col(y)], o[col(y + 1)], o[col(y + 2)], o[col(y + 3)]);
+          for (int y = 0; y < 32; y += 8) {              // a lane has a row: whole sectors
+            uint32_t v[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) v[z] = o[col(y + z)];
+            ta_store8(p.partial + at * D + 32 * c + y, v);
+          }
         }
       }
     }
