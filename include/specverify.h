@@ -247,7 +247,7 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
  * logits, parent, token, q and u; its row 0 is the anchor, row i > 0 is a
  * draft token[i] whose parent is row parent[i] < i of the same request (parent
  * and token of the anchor are not read).  The children of a node are its rows in
- * ascending order.  From the anchor on, at node v:
+ * ascending order.  From the anchor on, at node v (T = temperature, 0 .. 2^120):
  * T == 0: t = argmax(logits[v]); the first child with token t is next.
  * T > 0, q given: p = softmax(logits[v] / T) and the draft's distribution q[v]
  *   (fp32 [rows, V], stride ldq; rows of nodes without children are not read).

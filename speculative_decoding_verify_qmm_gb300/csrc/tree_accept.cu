@@ -325,7 +325,10 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
           entered = true;
           break;
         }
-        const float Mf = (float)M, Af = (float)A, leftf = (float)left;
+        // A child after a rejected one needs the sum that is left; the sum before is not smaller, and a child that is accepted by that
+        // needs no other.
+        bool bound = false;
+        const float Mf = (float)M;
         while (rest && !fresh && what < 0) {
           const int i = __ffsll((long long)rest) - 1, x = s_token[i];
           rest &= rest - 1;
@@ -335,15 +338,19 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
           bool fits = false;
           if (!TRUNC || tv_place(s_z[i], x) >= cut) {
             // u q < W / M * left in fp32 (an exponent of up to 150 is off by 2^-16), in fp64 (slow here) where that does not tell
-            const float qx = s_q[i], taken = Af * qx, want = s_u[i] * qx * Mf, got = fmaxf(0.f, s_e[i] - taken) * leftf;
-            fits = want < got;
-            if (!(fabsf(want - got) > 3e-5f * (want + (s_e[i] + taken) * leftf))) {
+            const float leftf = (float)left, qx = s_q[i], taken = (float)A * qx, want = s_u[i] * qx * Mf, got = fmaxf(0.f, s_e[i] - taken) * leftf;
+            const bool sure = fabsf(want - got) > 3e-5f * (want + (s_e[i] + taken) * leftf);
+            fits = want < got && (sure || !bound);
+            if (!sure && !bound) {
               const double e = exp(((double)s_z[i] - (double)(stats ? s_top[v] : top)) / (double)p.temperature);
               fits = (double)s_u[i] * (double)qx * M < fmax(0.0, e - A * (double)qx) * left;
             }
           }
           if (fits) {
             follow(i);
+          } else if (bound) {
+            rest |= 1ull << i;                              // to be tried with the sum
+            what = TV_SUM;
           } else {
             if (p.distinct) {
               A += left == 1.0 ? M : M / left;
@@ -353,10 +360,10 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
             } else {
               A += M;
             }
-            what = TV_SUM;
+            bound = true;
           }
         }
-        if (what < 0 && !fresh) what = TV_DRAW;
+        if (what < 0 && !fresh) what = bound ? TV_SUM : TV_DRAW;
       }
       s_v = v;
       s_len = len;
@@ -787,7 +794,8 @@ int sv_tree_accept(int B, const int32_t* row_offsets, const float* logits, int l
   for (int b = 0; b < B; ++b)
     if (map.offs[b + 1] == map.offs[b]) return fail(SV_EINVAL, "request %d has no rows (the anchor is one)", b);
   if (V < 2 || V > TV_MAX_V) return fail(SV_EINVAL, "V must be in [2, 2^22] (got %d)", V);
-  if (!(temperature >= 0.f && temperature <= 3.4028235e38f)) return fail(SV_EINVAL, "temperature must be finite and >= 0");
+  // (a difference of two logits that is beyond a float then has no weight)
+  if (!(temperature >= 0.f && temperature <= 0x1p120f)) return fail(SV_EINVAL, "temperature must be in [0, 2^120]");
   if (!logits || !parent || !token || !out_len || !out_tokens || !path) return fail(SV_EINVAL, "null pointer argument");
   for (const void* a : {(const void*)logits, (const void*)parent, (const void*)token, (const void*)q, (const void*)u, (const void*)row_max,
                         (const void*)row_sumexp, (const void*)row_argmax, (const void*)out_len, (const void*)out_tokens, (const void*)path})

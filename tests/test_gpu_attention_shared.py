@@ -121,6 +121,8 @@ SHAPES = [
     ([[(16, 0)] * 16], [33], 16, 16, 128, 64),                    # 256 rows: a full block; no own tokens but the drafts
     ([[(1, 0)] * 256], [123], 4, 1, 64, 16),                      # the most requests; a prefix that ends inside a tile
     ([[(1, 9)] * 2, [(2, 9)] * 2], [4097, 3001], 9, 9, 64, 16),
+    ([[(2, 40)] * 8], [1], 4, 2, 64, 65536),                      # one page, the largest
+    ([[(1, 3)] * 2] * 128, [40] * 128, 8, 8, 64, 16),             # 128 groups
 ]
 
 
@@ -190,6 +192,19 @@ def test_values_that_are_not_finite_stay_with_those_that_see_them(lib, bits):
     b.check(got, requests=[0, 2, 4, 15])
     assert got[12:16].isnan().any() and not got[:12].isnan().any() and not got[16:64].isnan().any()
     assert got[64:, :64].isnan().all() and not got[64:, 64:].isnan().any()
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_rows_of_q_that_are_not_finite_stay_alone(lib, bits):
+    b = Batch(lib, 69, bits, [[(4, 10)] * 24], [100], 8, 8, 64, 32)
+    assert b.shares()
+    want = b.call()
+    b.q_d[5, 64:128], b.q_d[30, 3] = float("nan"), float("inf")
+    got = b.call()
+    assert got[5, 64:128].isnan().all()
+    keep = torch.ones_like(got, dtype=torch.bool)
+    keep[5, 64:128], keep[30, :64] = False, False
+    assert torch.equal(got[keep], want[keep])
 
 
 def test_in_place_and_strided_rows(lib):

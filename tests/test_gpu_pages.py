@@ -232,6 +232,20 @@ def test_copy_pages(lib, bits, heads, dim, page):
     lib.kv_copy_pages(a, i32([]), i32([]))
 
 
+def test_largest_pages(lib):
+    """Pages of 65536 tokens: copied whole, moved, and in part."""
+    w = World(lib, 19, 4, 65536, 3, 2, [(2, 64, 4)] * 2)
+    w.reserve([0] * 3, [40001, 65537, -1])
+    w.fork([0], [2], [40001])
+    w.reserve([0, 0, 40001], [-1, 0, 50000])                        # (slot 0 is left alone: its page stays shared until then)
+    w.check()
+    w.reserve([0, 0, 0], [0, -1, -1])
+    w.compact()
+    w.check()
+    lib.kv_copy_pages(w.caches, i32([0]), i32([3]))
+    assert all(torch.equal(t[3].view(torch.int16), t[0].view(torch.int16)) for c in w.caches for t in c.tensors) and lib.device_error() == 0
+
+
 def test_offsets_past_32_bits(lib):
     """A cache of more than 2^32 bytes a tensor: its last page."""
     n, heads, page, dim = 9000, 32, 64, 128

@@ -58,7 +58,8 @@ class Case:
     def stats(self):
         top = self.z.max(1)
         T = np.float64(np.float32(self.T)) if self.T else 1.0
-        return top, np.exp((self.z - top[:, None]).astype(np.float64) / T).sum(1).astype(np.float32), self.z.argmax(1).astype(np.int32)
+        with np.errstate(over="ignore"):
+            return top, np.exp((self.z - top[:, None]).astype(np.float64) / T).sum(1).astype(np.float32), self.z.argmax(1).astype(np.int32)
 
     def call(self, lib, stats=False, **kw):
         st = tuple(dev(x) for x in self.stats()) if stats else None
@@ -324,6 +325,35 @@ def test_emitted_tokens_have_the_target_distribution(lib):
         n = B * rounds
         chi = ((seen - n * p) ** 2 / (n * p)).sum()
         assert chi < 50.0                                        # 15 degrees of freedom: 1 - 1e-5 lies at 49.3
+
+
+@pytest.mark.parametrize("mode", ["independent", "distinct", "target"])
+@pytest.mark.parametrize("T", [1e-44, 1e-20, 1e5, 2.0 ** 120])
+def test_extreme_temperatures_and_logits(lib, mode, T):
+    c = Case(40, [7, 12], 600, 1.0, mode)
+    c.T = T
+    c.z[3, ::3], c.z[4, 5], c.z[4, 6] = -3e38, 3e38, -3e38
+    for stats in (False, True):
+        for kw in ({}, dict(top_k=9), dict(top_p=0.5)):
+            c.check(c.call(lib, stats, **kw), stats, **kw)
+    assert lib.device_error() == 0
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_a_chain_of_64_nodes_that_fits(lib, mode):
+    """The deepest path: every draft is the target's certain token."""
+    c = Case(41, [64, 64], 200, 0.0 if mode == "greedy" else 1.0, mode, kids=1)
+    for b in range(2):
+        for i in range(1, 64):
+            v = c.offs[b] + i - 1
+            c.parent[v + 1], c.token[v + 1] = i - 1, (7 * i) % 200
+            c.z[v, (7 * i) % 200] = 90.0
+            if c.q is not None:
+                c.q[v] = 0.0
+                c.q[v, (7 * i) % 200] = 1.0
+    length, tokens, path = c.call(lib)
+    assert length.tolist() == [64, 64] and path[1].tolist() == list(range(64)) and tokens[64:127].tolist() == [(7 * i) % 200 for i in range(1, 64)]
+    c.check((length, tokens, path))
 
 
 def test_refusals_of_tensors(lib):

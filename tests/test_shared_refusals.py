@@ -25,7 +25,7 @@ def _accept(raw, B=1, offs=None, logits=16, ldl=100, top=None, total=None, arg=N
     (dict(B=0), SV_EINVAL), (dict(B=257), SV_EINVAL), (dict(offs=_offs(1, 3)), SV_EINVAL), (dict(offs=_offs(0, 0)), SV_EINVAL),
     (dict(B=2, offs=_offs(0, 3, 3)), SV_EINVAL), (dict(B=2, offs=_offs(0, 3, 2)), SV_EINVAL), (dict(offs=_offs(0, 65)), SV_EUNSUPPORTED),
     (dict(V=1), SV_EINVAL), (dict(V=(1 << 22) + 1, ldl=1 << 23, ldq=1 << 23), SV_EINVAL), (dict(ldl=99), SV_EINVAL), (dict(ldq=99), SV_EINVAL),
-    (dict(T=-0.1), SV_EINVAL), (dict(T=float("inf")), SV_EINVAL), (dict(T=float("nan")), SV_EINVAL), (dict(u=None), SV_EINVAL),
+    (dict(T=-0.1), SV_EINVAL), (dict(T=2.0 ** 121), SV_EINVAL), (dict(T=float("inf")), SV_EINVAL), (dict(T=float("nan")), SV_EINVAL), (dict(u=None), SV_EINVAL),
     (dict(logits=None), SV_EINVAL), (dict(parent=None), SV_EINVAL), (dict(token=None), SV_EINVAL), (dict(n=None), SV_EINVAL),
     (dict(tokens=None), SV_EINVAL), (dict(path=None), SV_EINVAL), (dict(logits=18), SV_EINVAL), (dict(q=17), SV_EINVAL), (dict(u=18), SV_EINVAL),
     (dict(path=18), SV_EINVAL), (dict(top=16), SV_EINVAL), (dict(top=16, arg=16), SV_EINVAL), (dict(total=16, arg=16), SV_EINVAL),
