@@ -31,7 +31,10 @@
 namespace sv {
 
 constexpr int TV_THREADS = 512;
-constexpr int TV_BATCH = 10;             // vocabulary elements per thread whose loads are in flight together
+// Vocabulary elements per thread whose loads are in flight together: where sums are made, and where a row is only read.  (24 trees of 64 nodes,
+// one tree, four greedy ones, us: 7 and 20 105, 23.7, 9.4; 10 and 10 112, 24.1, 9.8; 13 and 20 106, 24.9, 9.4; 20 and 20 113, 24.7, 9.4.)
+constexpr int TV_BATCH = 7;
+constexpr int TV_READ = 20;
 constexpr int TV_UNIT = 40;              // weights count in 2^-40 of the largest
 constexpr int TV_MAX_V = 1 << 22;        // sums stay below 2^62
 constexpr int TV_MAX_CLUSTER = 16;
@@ -390,28 +393,28 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
         constexpr bool OLD = decltype(is_old)::value, SUB = decltype(has_a)::value;
         auto batch = [&](int k, auto whole) {
           constexpr bool ALL = decltype(whole)::value;
-          float x[TV_BATCH], y[TV_BATCH];
+          float x[OLD ? 1 : TV_BATCH], y[SUB ? TV_BATCH : 1];
 #pragma unroll
           for (int i = 0; i < TV_BATCH; ++i) {
             const int kk = k + i * T;
             const bool in = ALL || kk < k1;
-            x[i] = y[i] = 0.f;
-            if (!OLD && in) x[i] = near ? *reinterpret_cast<const float*>(s_weight + (kk - k0)) : z[kk];
-            if (SUB && in) y[i] = qr[kk];
+            if constexpr (!OLD) x[i] = !in ? 0.f : near ? *reinterpret_cast<const float*>(s_weight + (kk - k0)) : z[kk];
+            if constexpr (SUB) y[i] = in ? qr[kk] : 0.f;
           }
 #pragma unroll
           for (int i = 0; i < TV_BATCH; ++i) {
             const int kk = k + i * T;
-            if (!ALL && kk >= k1) continue;
+            if (!OLD && !ALL && kk >= k1) continue;
             u64 w;
             if (OLD) {
-              w = s_weight[kk - k0];
+              w = ALL || kk < k1 ? s_weight[kk - k0] : 0;   // (without branches)
             } else {
               w = weight(kk, x[i]);
               each(x[i]);
               if (CACHED) s_weight[kk - k0] = w;
             }
-            sum += SUB ? tv_left(w, tv_product(a, y[i])) : w;
+            if constexpr (SUB) w = tv_left(w, tv_product(a, y[i]));
+            sum += w;
           }
         };
         int k = k0 + tid;
@@ -451,12 +454,12 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
         // its largest logit, lowest index first (its values stay in the weights' places)
         float best = -INFINITY;
         int at = k0 + tid < k1 ? k0 + tid : -1;
-        for (int k = k0 + tid; k < k1; k += TV_BATCH * T) {
-          float x[TV_BATCH];
+        for (int k = k0 + tid; k < k1; k += TV_READ * T) {
+          float x[TV_READ];
 #pragma unroll
-          for (int i = 0; i < TV_BATCH; ++i) x[i] = k + i * T < k1 ? z[k + i * T] : -INFINITY;
+          for (int i = 0; i < TV_READ; ++i) x[i] = k + i * T < k1 ? z[k + i * T] : -INFINITY;
 #pragma unroll
-          for (int i = 0; i < TV_BATCH; ++i) {
+          for (int i = 0; i < TV_READ; ++i) {
             const int kk = k + i * T;
             if (x[i] > best) {
               best = x[i];
