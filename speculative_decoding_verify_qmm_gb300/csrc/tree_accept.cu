@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
         // the candidates: all tokens up to that bin's far edge, and a little more
         const u64 least = (u64)(tv_bin_weight((float)(s_last + 1)) * 0.998f);
         auto candidates = [&](auto take) {
+#pragma unroll 4
           for (int k = k0 + tid; k < k1; k += T) {
             u64 w = CACHED ? s_weight[k - k0] : 0;
             if (CACHED && w < least) continue;
@@ -548,8 +549,11 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
               sorted = s_list + T;
               const u64 mine = tid < listed ? s_list[tid] : 0;
               int before = 0;
-              for (int i = 0; i < listed; ++i) before += s_list[i] > mine;
-              if (tid < listed) sorted[before] = mine;
+              if (tid < listed) {
+#pragma unroll 8
+                for (int i = 0; i < listed; ++i) before += s_list[i] > mine;
+                sorted[before] = mine;
+              }
             } else {
               int size = T;
               while (size < listed) size <<= 1;
@@ -620,9 +624,11 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
           cut = lowest;
         }
         // what is cut off has no weight
-        if (CACHED)
+        if (CACHED) {
+#pragma unroll 4
           for (int k = k0 + tid; k < k1; k += T)
             if (s_weight[k - k0] < least || tv_place(z[k], k) < cut) s_weight[k - k0] = 0;
+        }
         summed = false;
       }
     }
