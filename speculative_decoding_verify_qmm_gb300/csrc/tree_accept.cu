@@ -14,8 +14,10 @@
 // meet only where a sum is needed.  What the tests need of every node is asked for at once before the walk begins.
 //
 // Measured (vocabulary 151936, in a graph): one tree of 32 nodes with the head's statistics 24 us; 24 trees of up to 64 nodes from raw logits
-// 95 to 118 (alone, the longest walks among them take 57 to 61: a node some 8 us, a rejection 4, of which an exchange between CTAs is 1.5); 8
-// trees of 24 nodes, truncated to 64 tokens, 42 to 55; 4 greedy trees of 16 nodes 9.8.  How long a walk is lies in the uniforms.
+// 88 to 112 by their uniforms, which say how far a walk goes (alone, the longest among them take 58: a node some 8 us, a rejection 4, of which
+// an exchange between CTAs is 1 to 1.5); 8 trees of 24 nodes, truncated to 64 tokens, 45 to 52 (25 a node: E and bins 5, the bins' sum 3,
+// candidates and their order 7, exchanges and the draw the rest); 4 greedy trees of 16 nodes 9.6.  Issue slots are a quarter full at most, and
+// neither prefetching likely rows to the L2 cache nor more loads in flight helps: chains of 64-bit arithmetic, barriers and exchanges.
 //
 // Weights are 64-bit integers in units of 2^-40: their sums do not depend on any order, a draw compares integers, and the
 // cumulative sums are exact to some 2^-40 of the largest weight, where sums of fp32 terms (2^-24) would choose another token than

@@ -8,9 +8,9 @@
 // brings them together and rounds once.
 //
 // Measured (us, in a graph; 32 query and 8 key heads of 128, against tree attention of the same batch): 16 requests of 8 rows behind 16384
-// tokens with up to 700 of their own, 8-bit, 82 to 87 against 169 (prefix 50, own tokens 25, join 8, less what overlaps); 64 of a row
-// behind 8016 with up to 2011, 4-bit, 105 against 240 (30 to 40, 59, 14); 24 trees of up to 32 nodes in 48 heads behind 30000 and 25000, bf16, 276
-// against 477 (210, 56, 24).
+// tokens with up to 700 of their own, 8-bit, 81 to 86 against 169 (prefix 50, own tokens 25, join 8, less what overlaps); 64 of a row
+// behind 8016 with up to 2011, 4-bit, 104 to 105 against 240 (30 to 40, 59, 14); 24 trees of up to 32 nodes in 48 heads behind 30000 and 25000,
+// bf16, 273 to 279 against 478 (210, 56, 24).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
