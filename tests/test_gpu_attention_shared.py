@@ -123,6 +123,8 @@ SHAPES = [
     ([[(1, 9)] * 2, [(2, 9)] * 2], [4097, 3001], 9, 9, 64, 16),
     ([[(2, 40)] * 8], [1], 4, 2, 64, 65536),                      # one page, the largest
     ([[(1, 3)] * 2] * 128, [40] * 128, 8, 8, 64, 16),             # 128 groups
+    ([[(5, 20)] * 9], [245], 64, 1, 64, 256),                     # 64 query heads to a key head: twelve blocks
+    ([[(2, 3)] * 3], [256], 4, 1, 64, 4096),                      # a million tokens
 ]
 
 
