@@ -481,8 +481,10 @@ int sv_kv_commit(const sv_kv_cache* layers, int n_layers, int B, const int32_t* 
  * order.  Prefix tokens are read once per 256 rows (drafted rows of the whole group
  * times query heads per key head).  A captured call keeps the groups and shared_pages it
  * was given; lengths, tables and pages are read when it runs.
- * Workspace: sv_tree_attention_shared_workspace_bytes (0 for a bad argument; it
- * grows with the rows), same rules as sv_tree_attention's. */
+ * Workspace: sv_tree_attention_shared_workspace_bytes (0 for a bad argument), same
+ * rules as sv_tree_attention's.  It follows from the requests' rows and from the groups,
+ * not from shared_pages or lengths; fewer rows in some requests (or none), or
+ * groups and requests left out, never need more: that of the largest batch does for all. */
 size_t sv_tree_attention_shared_workspace_bytes(const sv_kv_cache* cache, int G, const int32_t* group_offsets,
                                                 const int32_t* shared_pages, int B, const int32_t* row_offsets,
                                                 int n_q_heads);

@@ -62,21 +62,22 @@ __device__ __forceinline__ bool px_item(bool pair, int e, int n, int* tile) {
 struct PxRun {
   int g, h, rb, rows;            // group, key head, block and its rows
   int tile0, n;                  // first tile, tiles
-  int slot;                      // number of its first piece: place of its sums
+  int slot;                      // place of its sums
   bool pair;                     // two matrices on the same tiles
 };
 // The CTA's pieces are those from next to end - 1.  By key head, block, tokens.
 __device__ __forceinline__ bool px_next(const PrefixParams& p, int* next, int end, PxRun* r) {
   if (*next >= end) return false;
-  r->slot = *next;
+  const int piece = *next;
   int lo = 0, hi = p.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (p.pieces[mid] <= r->slot) lo = mid; else hi = mid;
+    if (p.pieces[mid] <= piece) lo = mid; else hi = mid;
   }
-  const int blocks = px_blocks(p.rows[lo]), splits = p.splits[lo], nt = px_tiles(p.tokens[lo]), i = r->slot - p.pieces[lo];
-  const int item = i / splits, part = i - item * splits, parts = min(splits - part, end - r->slot);
+  const int blocks = px_blocks(p.rows[lo]), splits = p.splits[lo], nt = px_tiles(p.tokens[lo]), i = piece - p.pieces[lo];
+  const int item = i / splits, part = i - item * splits, parts = min(splits - part, end - piece);
   *next += parts;
+  r->slot = p.items[lo] + item + blockIdx.x;
   r->g = lo;
   r->h = item / blocks;
   r->rb = item - r->h * blocks;

@@ -2,7 +2,8 @@
 //
 // Every (group, key head, block of up to 256 rows) is an item of tiles of 128 tokens, cut into equal pieces; a CTA takes some
 // consecutive pieces whole, and those of one item among them as one run.  All of it is known on the host.  A run leaves fp32 sums (with
-// their maximum and weight) in the workspace, at the number of its first piece.
+// their maximum and weight) in the workspace, at item plus CTA: neither goes down from run to run, and one of them goes up.  (So their
+// number follows from the rows, whatever the pieces: a workspace for the largest batch does for all.)
 #pragma once
 
 #include "tree_attn.cuh"
@@ -19,10 +20,11 @@ struct PrefixParams {
   const __nv_bfloat16* q; int ldq;
   int heads_per;                      // query heads per key head
   float scale;
-  float* partial;                     // [pieces][256][dim]
-  float* stats;                       // [pieces][256][8]: maximum (as an exponent of 2) and weight of a row, in a sector of its own
+  float* partial;                     // [items + CTAs][256][dim]
+  float* stats;                       // [items + CTAs][256][8]: maximum (as an exponent of 2) and weight of a row, in a sector of its own
   int grid, n;                        // CTAs; groups with a prefix
   int pieces[MAX_BATCH + 1];          // of the groups before
+  int items[MAX_BATCH];               // likewise
   int splits[MAX_BATCH];              // pieces of an item
   int row0[MAX_BATCH], rows[MAX_BATCH];       // first row; rows times heads_per
   int tokens[MAX_BATCH], request[MAX_BATCH];  // of the prefix; the request whose pages are read

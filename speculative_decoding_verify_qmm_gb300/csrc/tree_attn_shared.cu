@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
   // what is looked up by request and group: indexed reads of the launch parameters take hundreds of cycles each
   __shared__ int s_offs[MAX_BATCH + 1];
   __shared__ short s_group[MAX_BATCH];
-  __shared__ int s_rows[MAX_BATCH], s_row0[MAX_BATCH], s_pieces[MAX_BATCH], s_splits[MAX_BATCH];
+  __shared__ int s_rows[MAX_BATCH], s_row0[MAX_BATCH], s_pieces[MAX_BATCH], s_splits[MAX_BATCH], s_items[MAX_BATCH];
   const int lane = threadIdx.x & 31, B = p.map.B;
   if (threadIdx.x >= 32)
     for (int i = threadIdx.x - 32; i <= B; i += 32 * (TJ_WARPS - 1)) {
@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
         s_row0[i] = x.row0[i];
         s_pieces[i] = x.pieces[i];
         s_splits[i] = x.splits[i];
+        s_items[i] = x.items[i];
       }
     }
   pdl_wait();
@@ -76,11 +77,13 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
     const int c0 = (int)ta_div(a0 + plan.begin + cost - 1, per), c1 = (int)ta_div(a0 + plan.begin + span - 1, per);
     // the prefix
     const int gi = s_group[b];
-    int xn = 0, xk = 0, xslot = 0, halves = 0;
+    int xn = 0, xk = 0, xitem = 0, xslot = 0, halves = 0;
     if (gi >= 0) {
       const int xr = (row - s_row0[gi]) * p.group + hg, xrb = xr / PX_ROWS;
       xk = xr % PX_ROWS;
-      xslot = s_pieces[gi] + (h * px_blocks(s_rows[gi]) + xrb) * s_splits[gi];
+      xitem = h * px_blocks(s_rows[gi]) + xrb;
+      xslot = s_pieces[gi] + xitem * s_splits[gi];     // its first piece
+      xitem += s_items[gi];
       halves = !px_pair(s_rows[gi], xrb);              // two parts a piece, as a shift
       xn = s_splits[gi] << halves;
     }
@@ -93,9 +96,9 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
       float* at = nullptr;
       if (j < xn) {
         // a piece that another of its item and CTA comes before has no sums of its own
-        const int piece = xslot + (j >> halves);
-        if (piece == xslot || px_cta(x_all, x.grid, piece) != px_cta(x_all, x.grid, piece - 1)) {
-          place = piece * PX_ROWS + xk + (halves ? (j & 1) * 128 : 0);
+        const int piece = xslot + (j >> halves), cta = px_cta(x_all, x.grid, piece);
+        if (piece == xslot || cta != px_cta(x_all, x.grid, piece - 1)) {
+          place = (xitem + cta) * PX_ROWS + xk + (halves ? (j & 1) * 128 : 0);
           at = x.stats + (size_t)place * TA_STAT;
         }
       } else if (j < n) {
@@ -165,13 +168,37 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
 }
 
 // ------------------------------------------------------------------ host side
-// What a call shares, and the sizes of the sums.  A group of one request has nothing to share: its prefix stays with the request, and
-// so do all where there is little to save.
+// Sizes of the sums, from the rows and the groups alone and never more for less of them, so that a workspace for the largest batch does
+// for all: own tokens' as if blocks were the largest that the kernel of these rows takes, the prefixes' as if every group shared one.
 struct SharedSizes {
   size_t partial, stats, px_partial, px_stats, total;
 };
+static int with_rows(const RowMap& map, const int32_t* group_offsets, int g) {
+  int n = 0;
+  for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b) n += map.offs[b + 1] > map.offs[b];
+  return n;
+}
+static SharedSizes shared_sizes(const KvCache& c, const RowMap& map, int G, const int32_t* group_offsets, int heads_per) {
+  int block;
+  const int widest = ta_choose_block(map, heads_per, &block) ? 32 : 128;
+  size_t own = ta_sms(), prefix = ta_sms();      // runs: one per item and CTA
+  for (int b = 0; b < map.B; ++b) own += (size_t)c.heads * ta_blocks((map.offs[b + 1] - map.offs[b]) * heads_per, widest);
+  for (int g = 0; g < G; ++g)
+    if (with_rows(map, group_offsets, g) > 1)
+      prefix += (size_t)c.heads * px_blocks((map.offs[group_offsets[g + 1]] - map.offs[group_offsets[g]]) * heads_per);
+  SharedSizes z;
+  z.partial = align256(own * widest * c.dim * sizeof(float));
+  z.stats = align256(own * widest * TA_STAT * sizeof(float));
+  z.px_partial = align256(prefix * PX_ROWS * c.dim * sizeof(float));
+  z.px_stats = align256(prefix * PX_ROWS * TA_STAT * sizeof(float));
+  z.total = std::max(ta_workspace_bytes(c), z.partial + z.stats + z.px_partial + z.px_stats);
+  return z;
+}
+
+// What a call shares.  A group of one request has nothing to share: its prefix stays with the request, and so do all where there is
+// little to save.
 static int shared_plan(const KvCache& c, const RowMap& map, int G, const int32_t* group_offsets, const int32_t* shared_pages, int n_q_heads,
-                       PrefixParams* x, int* skip, SharedSizes* z) {
+                       PrefixParams* x, int* skip) {
   if (G < 1 || G > MAX_BATCH) return fail(SV_EINVAL, "G must be in [1, 256] (got %d)", G);
   if (!group_offsets || !shared_pages) return fail(SV_EINVAL, "group_offsets and shared_pages must be non-null");
   if (group_offsets[0] != 0 || group_offsets[G] != map.B) return fail(SV_EINVAL, "group_offsets must go from 0 to B");
@@ -193,14 +220,11 @@ static int shared_plan(const KvCache& c, const RowMap& map, int G, const int32_t
   };
   alone();
   for (int g = 0; g < G; ++g) {
-    int first = -1, with_rows = 0;
-    for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
-      if (map.offs[b + 1] > map.offs[b]) {
-        if (first < 0) first = b;
-        ++with_rows;
-      }
-    if (with_rows < 2 || !shared_pages[g]) continue;
-    saved += (double)(with_rows - 1) * ((long long)shared_pages[g] << c.page_shift) * c.heads;
+    const int requests = with_rows(map, group_offsets, g);
+    if (requests < 2 || !shared_pages[g]) continue;
+    int first = group_offsets[g];
+    while (map.offs[first + 1] == map.offs[first]) ++first;
+    saved += (double)(requests - 1) * ((long long)shared_pages[g] << c.page_shift) * c.heads;
     const int i = x->n++;
     x->row0[i] = map.offs[group_offsets[g]];
     x->rows[i] = (map.offs[group_offsets[g + 1]] - x->row0[i]) * heads_per;
@@ -212,8 +236,6 @@ static int shared_plan(const KvCache& c, const RowMap& map, int G, const int32_t
     }
   }
   if (saved < PX_WORTH) alone();
-  memset(z, 0, sizeof(*z));
-  z->total = ta_workspace_bytes(c);
   if (!x->n) return SV_OK;
   // Pieces: of the numbers that come to up to twelve a CTA, the one that ends first, in tiles' time, where beginning and ending a run takes
   // as long as PX_BEGIN tiles, and the join of another part of every row PX_PART of them and PX_JOIN a thousand rows and query heads.
@@ -248,18 +270,12 @@ static int shared_plan(const KvCache& c, const RowMap& map, int G, const int32_t
         best = target;
       }
     }
-  const int items = cut(best);
-  x->grid = items < sms ? items : sms;
-  int block;
-  ta_choose_block(map, heads_per, &block);
-  size_t own = sms;                              // runs of own tokens: one per item and CTA
-  for (int b = 0; b < map.B; ++b) own += (size_t)c.heads * ta_blocks((map.offs[b + 1] - map.offs[b]) * heads_per, block);
-  z->partial = align256(own * block * c.dim * sizeof(float));
-  z->stats = align256(own * block * TA_STAT * sizeof(float));
-  z->px_partial = align256((size_t)items * PX_ROWS * c.dim * sizeof(float));
-  z->px_stats = align256((size_t)items * PX_ROWS * TA_STAT * sizeof(float));
-  const size_t need = z->partial + z->stats + z->px_partial + z->px_stats;
-  if (need > z->total) z->total = need;
+  const int pieces = cut(best);
+  x->grid = pieces < sms ? pieces : sms;
+  for (int i = 0, items = 0; i < x->n; ++i) {
+    x->items[i] = items;
+    items += c.heads * px_blocks(x->rows[i]);
+  }
   return SV_OK;
 }
 
@@ -275,9 +291,8 @@ size_t sv_tree_attention_shared_workspace_bytes(const sv_kv_cache* cache, int G,
   RowMap m;
   PrefixParams x;
   int skip[MAX_BATCH];
-  SharedSizes z;
-  if (ta_check_batch(cache, B, row_offsets, n_q_heads, &c, &m) || shared_plan(c, m, G, group_offsets, shared_pages, n_q_heads, &x, skip, &z)) return 0;
-  return z.total;
+  if (ta_check_batch(cache, B, row_offsets, n_q_heads, &c, &m) || shared_plan(c, m, G, group_offsets, shared_pages, n_q_heads, &x, skip)) return 0;
+  return shared_sizes(c, m, G, group_offsets, n_q_heads / c.heads).total;
 }
 
 int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* group_offsets, const int32_t* shared_pages, int B,
@@ -286,17 +301,18 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
                              void* workspace, size_t workspace_bytes, void* stream) {
   TreeAttnOwnParams p;
   PrefixParams x;
-  SharedSizes z;
   memset(static_cast<void*>(&p), 0, sizeof(p));
   memset(static_cast<void*>(&x), 0, sizeof(x));
   int st = ta_check_batch(cache, B, row_offsets, n_q_heads, &p.c, &p.map);
   if (!st) st = ta_check_call(&p, kv_len, block_table, table_pages, q, ldq, n_q_heads, scale, tree_mask, out, ldo);
-  if (!st) st = shared_plan(p.c, p.map, G, group_offsets, shared_pages, n_q_heads, &x, p.skip, &z);
+  if (!st) st = shared_plan(p.c, p.map, G, group_offsets, shared_pages, n_q_heads, &x, p.skip);
   if (st) return st;
   for (int g = 0; g < G; ++g)
     if (shared_pages[g] > table_pages) return fail(SV_EINVAL, "shared_pages[%d] is more than table_pages", g);
   if (!workspace || !aligned(workspace, 256)) return fail(SV_EINVAL, "workspace must be non-null and 256-byte aligned");
-  if (workspace_bytes < z.total) return fail(SV_EINVAL, "workspace too small: %zu < %zu", workspace_bytes, z.total);
+  const SharedSizes z = shared_sizes(p.c, p.map, G, group_offsets, x.heads_per);
+  const size_t bytes = x.n ? z.total : ta_workspace_bytes(p.c);
+  if (workspace_bytes < bytes) return fail(SV_EINVAL, "workspace too small: %zu < %zu", workspace_bytes, bytes);
   if (!x.n)                               // nothing is shared
     return sv_tree_attention(cache, B, row_offsets, kv_len, block_table, table_pages, q, ldq, n_q_heads, scale, tree_mask, out, ldo, workspace,
                              workspace_bytes, stream);
