@@ -492,14 +492,16 @@ __global__ void __launch_bounds__(PxShape<D, BITS>::THREADS, 1) tree_attn_prefix
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
+          __syncwarp();                                  // the whole warp loads; what is above and below is for lanes with a row alone
           tmem_ld32(obuf + 32 * c, o);
-          if (!real) continue;
+          if (real) {
 #pragma unroll
-          for (int y = 0; y < 32; y += 8) {              // a lane has a row: whole sectors
-            uint32_t v[8];
+            for (int y = 0; y < 32; y += 8) {            // a lane has a row: whole sectors
+              uint32_t v[8];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) v[z] = o[col(y + z)];
-            ta_store8(p.partial + at * D + 32 * c + y, v);
+              for (int z = 0; z < 8; ++z) v[z] = o[col(y + z)];
+              ta_store8(p.partial + at * D + 32 * c + y, v);
+            }
           }
         }
       }

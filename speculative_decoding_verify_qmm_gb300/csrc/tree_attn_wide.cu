@@ -565,21 +565,24 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
+            __syncwarp();                                // the whole warp loads; what is above and below is for lanes with a row alone
             tmem_ld32(tmem + TA_O + lanes + 32 * c, o);
             float e[32];
 #pragma unroll
             for (int x = 0; x < 32; ++x) e[x] = __uint_as_float(o[col(x)]) * factor;
-            if (!real) continue;
-            if constexpr (decltype(is_whole)::value) {
+            if (real) {
+              if constexpr (decltype(is_whole)::value) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 8) {
-                const uint4 w = make_uint4(ta_pack(e[x], e[x + 1], true), ta_pack(e[x + 2], e[x + 3], true),
-                                           ta_pack(e[x + 4], e[x + 5], true), ta_pack(e[x + 6], e[x + 7], true));
-                *reinterpret_cast<uint4*>(p.out + at + 32 * c + x) = w;
+                for (int x = 0; x < 32; x += 8) {
+                  const uint4 w = make_uint4(ta_pack(e[x], e[x + 1], true), ta_pack(e[x + 2], e[x + 3], true),
+                                             ta_pack(e[x + 4], e[x + 5], true), ta_pack(e[x + 6], e[x + 7], true));
+                  *reinterpret_cast<uint4*>(p.out + at + 32 * c + x) = w;
+                }
+              } else {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                  *reinterpret_cast<float4*>(p.partial + at + 32 * c + x) = make_float4(e[x], e[x + 1], e[x + 2], e[x + 3]);
               }
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(p.partial + at + 32 * c + x) = make_float4(e[x], e[x + 1], e[x + 2], e[x + 3]);
             }
           }
         };
@@ -589,6 +592,7 @@ __global__ void __launch_bounds__(TaShape<D, BITS>::THREADS, 1) tree_attn_wide_k
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
+          __syncwarp();
           tmem_ld32(tmem + TA_O + lanes + 32 * c, o);
           float* dst = scratch + L * TA_PAD;
 #pragma unroll
