@@ -536,7 +536,8 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
  * [slots, 3], DEVICE: the first counts[1] rows are (from, to, places), in slot
  * order; later rows are untouched.  Bad input (the slot is left alone): keep
  * outside [0, min(need, held * page_size)], need beyond the table, a page
- * outside [0, n_pages).
+ * outside [0, n_pages) among the slot's entries from keep / page_size on (what
+ * it keeps before them is not looked at).
  * Workspace: sv_kv_reserve_workspace_bytes(pages) (0 for a bad argument),
  * 256-byte aligned; it need not be zero, and what the call wrote is zero again after it.
  *
