@@ -545,8 +545,9 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
  * to the free ones below, both in ascending order, in all of n_layers caches
  * (0 .. 1024) with their refs, and the slots' entries are renumbered.  counts
  * int32 [2], DEVICE: live, pages moved.  moves int32 [n_pages, 2], DEVICE: the
- * first counts[1] rows are (from, to).  An entry that names no page in use is
- * bad input and left as it is.
+ * first counts[1] rows are (from, to).  An entry that names no page in use
+ * (outside the cache, or free: refs == 0) is bad input and left as it is; where its
+ * page was free below live, that page may now hold another request's tokens.
  *
  * sv_kv_copy_pages: page src[i] of cache from[l] to page dst[i] of to[l], codes,
  * scales and biases as they are, for i < n <= 2^24 and each of n_layers

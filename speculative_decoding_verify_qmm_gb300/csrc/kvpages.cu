@@ -376,7 +376,8 @@ __device__ __forceinline__ void finish_reserve(const PageCopyParams& p) {
   }
 }
 
-// The rest of a compact: tables.  src of the moves ascends.
+// The rest of a compact: tables.  src and dst of the moves ascend; a page from live on is in use if it is a src, one below if it is no
+// dst (then it was free, and holds another's tokens now).
 __device__ __forceinline__ void finish_compact(const PageCopyParams& p) {
   const int live = *p.live, n = *p.count;
   for (int s = blockIdx.x; s < p.g.slots; s += gridDim.x) {
@@ -388,14 +389,16 @@ __device__ __forceinline__ void finish_compact(const PageCopyParams& p) {
     for (int e = threadIdx.x; e < has; e += PC_THREADS) {
       int32_t* at = p.g.table + (size_t)s * p.g.table_pages + e;
       const int id = *at;
-      if ((unsigned)id < (unsigned)live) continue;
+      const bool stays = (unsigned)id < (unsigned)live;
+      const int32_t* col = stays ? p.dst : p.src;
       int lo = 0, hi = n;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.src[2 * mid] <= id) lo = mid; else hi = mid;
+        if (col[2 * mid] <= id) lo = mid; else hi = mid;
       }
-      if (lo < n && p.src[2 * lo] == id) *at = p.dst[2 * lo];
-      else raise_error(ERR_BAD_INPUT);
+      const bool found = n && col[2 * lo] == id;
+      if (found == stays) raise_error(ERR_BAD_INPUT);
+      else if (found) *at = p.dst[2 * lo];
     }
   }
 }

@@ -57,3 +57,39 @@ def test_bad_entries_among_many_slots(lib):
     w.model.reserve([0] * 100, [-1 if s % 3 == 0 else 0 for s in range(100)])
     w.check()
     assert torch.equal(w.pages.block_table, good)
+
+
+def test_compact_reports_entries_that_name_no_page_in_use(lib):
+    """A stale entry of each kind: a hole that is filled, a page behind the last in use, one outside the cache."""
+    def world():
+        w = World(lib, 23, 20, 16, 5, 6)
+        w.reserve([0] * 5, [40, 30, 60, 20, 33])
+        w.reserve([0] * 5, [-1, 0, -1, 0, -1])                   # pages 3, 4 and 9, 10 are free now
+        return w
+    w = world()
+    assert [i for i, r in enumerate(w.model.refs) if not r] == [3, 4, 9, 10] + list(range(14, 20))
+    for slot, entry, stale in ((0, 1, 3), (0, 0, 4), (2, 3, 9), (4, 2, 10), (4, 0, 14), (2, 1, 19), (0, 2, 20), (2, 0, -1), (4, 1, 2 ** 31 - 1)):
+        w = world()
+        live, moves = w.model.compact()
+        assert live == 10 and moves == [(11, 3), (12, 4), (13, 9)]
+        w.pages.block_table[slot, entry] = stale
+        counts, out = lib.kv_compact(w.pages, w.caches)
+        low = stale in (3, 4, 9)
+        assert lib.device_error() == 4, (slot, entry, stale)
+        assert counts.tolist() == [live, 3] and out[:3].tolist() == [list(m) for m in moves] and low == (stale in [d for _, d in moves])
+        assert w.pages.block_table[slot, entry].item() == stale
+        w.pages.block_table[slot, entry] = w.model.table[slot][entry]
+        w.check()
+
+
+def test_compact_of_what_is_dense_already(lib):
+    """Nothing moves: every entry in use stands, the others are reported."""
+    w = World(lib, 24, 9, 16, 3, 4)
+    w.reserve([0] * 3, [40, 30, -1])
+    w.fork([0], [2], [40])
+    w.compact()
+    w.check()
+    for stale in (5, 8, 9, -1):
+        w.pages.block_table[1, 1] = stale
+        counts, _ = lib.kv_compact(w.pages, w.caches)
+        assert lib.device_error() == 4 and counts.tolist() == [5, 0] and w.pages.block_table[1, 1].item() == stale
