@@ -505,6 +505,8 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
  *   block_table int32 [slots, table_pages]: as the attention calls take it, a
  *               slot being a request of the batch
  *   held        int32 [slots]: a slot has the entries 0 .. held - 1 of its row
+ * 1 <= slots <= 256, 1 <= n_pages <= 2^30, table_pages * page_size <= 2^30 and
+ * slots * table_pages <= 2^30 (SV_EUNSUPPORTED above the last two).
  * Entries of block_table from held on are neither read nor written, but for
  * those a call adds.  A fresh state is all zeros.  Results follow from the
  * inputs alone, whatever the order in which threads run.

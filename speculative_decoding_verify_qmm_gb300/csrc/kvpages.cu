@@ -601,6 +601,7 @@ static int check_pool(const sv_kv_pages* pages, PagePool* g) {
   if (pages->table_pages < 1) return fail(SV_EINVAL, "table_pages must be >= 1 (got %d)", pages->table_pages);
   if (((long long)pages->table_pages << g->page_shift) > (1ll << 30))
     return fail(SV_EUNSUPPORTED, "table_pages * page_size must be <= 2^30");
+  if ((long long)pages->slots * pages->table_pages > (1ll << 30)) return fail(SV_EUNSUPPORTED, "slots * table_pages must be <= 2^30");
   return SV_OK;
 }
 
