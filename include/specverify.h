@@ -275,6 +275,7 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
  *   row_max, row_sumexp, row_argmax: the lm_head row outputs, all given or all
  *     NULL (then the call finds what it needs of the rows it visits).
  *   u fp32 [rows] in [0, 1), may be NULL when T == 0.  2 <= V <= 2^22.
+ * The outputs overlap neither each other nor what is read (SV_EINVAL otherwise).
  * Tests are taken in fp64.  Residuals and draws count a weight exp((z - max) / T) in
  * integer units of 2^-40 (a token below half of that is never drawn): sums are exact and
  * the result does not depend on timing.  Logits of -inf have probability 0.

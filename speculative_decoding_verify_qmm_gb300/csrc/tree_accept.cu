@@ -823,6 +823,18 @@ int sv_tree_accept(int B, const int32_t* row_offsets, const float* logits, int l
   if (top_k < 0) return fail(SV_EINVAL, "top_k must be >= 0 (0 = no limit)");
   if (!(top_p > 0.f && top_p <= 1.f)) return fail(SV_EINVAL, "top_p must be in (0, 1]");
   if (max_path < 1 || max_path > KV_MAX_DRAFT) return fail(SV_EINVAL, "max_path must be in [1, 64] (got %d)", max_path);
+  // The CTAs of a request take the same steps because they read the same numbers; one of them writes while others may still read.
+  const size_t rows = (size_t)map.offs[B];
+  const struct { const void* at; size_t n; } arrays[] = {
+      {out_len, (size_t)B}, {out_tokens, rows}, {path, (size_t)B * max_path},                     // what is written
+      {parent, rows}, {token, rows}, {logits, (rows - 1) * ldl + V}, {row_max, rows}, {row_sumexp, rows}, {row_argmax, rows},
+      {sampled ? u : nullptr, rows}, {sampled ? q : nullptr, (rows - 1) * ldq + V}};
+  for (int i = 0; i < 3; ++i)
+    for (const auto& x : arrays) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[i].at), c = reinterpret_cast<uintptr_t>(x.at);
+      if (&x != &arrays[i] && x.at && a < c + 4 * x.n && c < a + 4 * arrays[i].n)
+        return fail(SV_EINVAL, "out_len, out_tokens and path may not overlap each other or an input");
+    }
   for (int b = 0; b <= B; ++b) p.offs[b] = map.offs[b];
   p.logits = logits;
   p.ldl = ldl;
