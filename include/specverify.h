@@ -260,7 +260,8 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
  *   If no child is accepted the last token is the first k whose cumulative r
  *   (index order) exceeds u[anchor] times its sum (a residual of zero mass
  *   falls back to p).  A chain gets sv_spec_accept's rule, draft i's uniform
- *   being u[i] here and u[i-1] there, the draw's u[0] here and u[m] there.
+ *   being u[i] here and u[i-1] there, the draw's u[0] here and u[m] there, but for
+ *   a draft with q(x) = 0 and r(x) = 0: rejected here, accepted there.
  * T > 0, q NULL: t is drawn from p in the same way with u[v]; the first child
  *   with token t is next (drafts without a distribution: the output is an exact
  *   sample all the same).
@@ -274,7 +275,8 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
  *     behind these are untouched.  1 <= max_path <= 64.
  *   row_max, row_sumexp, row_argmax: the lm_head row outputs, all given or all
  *     NULL (then the call finds what it needs of the rows it visits).
- *   u fp32 [rows] in [0, 1), may be NULL when T == 0.  2 <= V <= 2^22.
+ *   u fp32 [rows] in [0, 1), may be NULL when T == 0.  2 <= V <= 2^22 (a quarter of
+ *     sv_spec_accept's: sums are counted exactly in 64 bits).
  * The outputs overlap neither each other nor what is read (SV_EINVAL otherwise).
  * Tests are taken in fp64.  Residuals and draws count a weight exp((z - max) / T) in
  * integer units of 2^-40 (a token below half of that is never drawn): sums are exact and
@@ -517,8 +519,8 @@ int sv_tree_attention_shared(const sv_kv_cache* cache, int G, const int32_t* gro
  * cache is touched.  parent, child, tokens int32 [n], DEVICE, n <= 256; a
  * parent may be named many times.  Bad input (reported by sv_device_error(),
  * nothing is done for that f): a slot outside [0, slots), a child that is not
- * empty, that an earlier f names too, or that is a parent of this call, more
- * tokens than the parent's pages hold, a page outside [0, n_pages).
+ * empty or that an earlier f names too, a parent that any f names as its child,
+ * more tokens than the parent's pages hold, a page outside [0, n_pages).
  *
  * sv_kv_reserve: slot s keeps its first keep[s] tokens and gets room for
  * need[s]: afterwards held[s] = ceil(need[s] / page_size), and what lies from
