@@ -193,7 +193,7 @@ int sv_lm_head_run(const uint32_t* wq, const uint16_t* scales, const uint16_t* b
  * none); out_tokens = draft[0..a-1] followed by argmax(logits[a]); out_len = a+1.
  * Sampled (temperature > 0; releases page, v0.0.2 "Highlights"): with
  * p_i = softmax(logits[i] / T), draft i is accepted iff u[i] < p_i[d]/q_i[d]
- * (q_i[d] == 0 accepts).  At the first rejection i the committed token is the
+ * (q_i[d] == 0 accepts, unless p_i[d] == 0 too).  At the first rejection i the committed token is the
  * smallest k whose cumulative residual max(0, p_i - q_i) (index order) exceeds
  * u[m] times its total (a zero residual falls back to p_i); if all m drafts
  * are accepted the bonus token is drawn the same way from p_m.
@@ -260,8 +260,7 @@ int sv_spec_accept_truncated(int B, const int32_t* row_offsets, const float* log
  *   If no child is accepted the last token is the first k whose cumulative r
  *   (index order) exceeds u[anchor] times its sum (a residual of zero mass
  *   falls back to p).  A chain gets sv_spec_accept's rule, draft i's uniform
- *   being u[i] here and u[i-1] there, the draw's u[0] here and u[m] there, but for
- *   a draft with q(x) = 0 and r(x) = 0: rejected here, accepted there.
+ *   being u[i] here and u[i-1] there, the draw's u[0] here and u[m] there.
  * T > 0, q NULL: t is drawn from p in the same way with u[v]; the first child
  *   with token t is next (drafts without a distribution: the output is an exact
  *   sample all the same).

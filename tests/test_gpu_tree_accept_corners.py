@@ -1,4 +1,4 @@
-"""Where the rule of a draft tree and that of a chain part, and what the tree's call does not read."""
+"""Drafts that neither distribution holds, and what the call does not read."""
 
 import numpy as np
 import pytest
@@ -11,18 +11,19 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("stats", [False, True])
-def test_a_draft_that_neither_distribution_holds(lib, stats):
-    """q(x) = p(x) = 0: 0 < 0 rejects it in a tree; the chain's ratio is infinite and accepts it."""
+@pytest.mark.parametrize("z,accepted", [(-np.inf, False), (-30.0, True), (0.0, True), (-300.0, True)])
+def test_a_draft_that_came_with_probability_0(lib, stats, z, accepted):
+    """q(x) = 0: taken where p(x) > 0, however small, and not where p(x) = 0; a chain and a tree of one child alike."""
     c = Case(70, [2], 50, 0.9, "independent")
     c.token[1] = 7
-    c.z[0, 7], c.q[0, 7] = -np.inf, 0.0
+    c.z[0, 7], c.q[0, 7] = z, 0.0
     c.u[:] = [0.3, 0.5]
     length, tokens, _ = c.call(lib, stats)
-    assert length.item() == 1 and tokens[0].item() != 7
-    want = ot.accept(c.z, c.parent.tolist(), c.token.tolist(), c.T, c.q, c.u)   # (its margin is 0: it says which side is the rule's)
-    assert want[0] == [0] and tokens[0].item() == want[1][0]
+    assert length.item() == 1 + accepted and (tokens[0].item() == 7) == accepted
+    want = ot.accept(c.z, c.parent.tolist(), c.token.tolist(), c.T, c.q, c.u)[1]   # (its margin is 0 here: it says which side is the rule's)
+    assert tokens[0].item() == want[0]
     n, chain = lib.spec_accept_batched(c.offs, dev(c.z), dev(c.token[1:]), c.T, q=dev(c.q[:1]), u=dev(c.u[::-1].copy()))
-    assert n.item() == 2 and chain[0].item() == 7
+    assert n.item() == length.item() and chain[0].item() == tokens[0].item()
 
 
 @pytest.mark.parametrize("mode", ["independent", "distinct"])
