@@ -77,13 +77,11 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
     const int c0 = (int)ta_div(a0 + plan.begin + cost - 1, per), c1 = (int)ta_div(a0 + plan.begin + span - 1, per);
     // the prefix
     const int gi = s_group[b];
-    int xn = 0, xk = 0, xitem = 0, xslot = 0, halves = 0;
+    int xn = 0, xrow = 0, xpiece = 0, halves = 0;
     if (gi >= 0) {
-      const int xr = (row - s_row0[gi]) * p.group + hg, xrb = xr / PX_ROWS;
-      xk = xr % PX_ROWS;
-      xitem = h * px_blocks(s_rows[gi]) + xrb;
-      xslot = s_pieces[gi] + xitem * s_splits[gi];     // its first piece
-      xitem += s_items[gi];
+      const int xr = (row - s_row0[gi]) * p.group + hg, xrb = xr / PX_ROWS, xitem = h * px_blocks(s_rows[gi]) + xrb;
+      xpiece = s_pieces[gi] + xitem * s_splits[gi];    // its first
+      xrow = (s_items[gi] + xitem - xrb) * PX_ROWS + xr;
       halves = !px_pair(s_rows[gi], xrb);              // two parts a piece, as a shift
       xn = s_splits[gi] << halves;
     }
@@ -96,9 +94,9 @@ __global__ void __launch_bounds__(32 * TJ_WARPS, TJ_CTAS) tree_attn_shared_join_
       float* at = nullptr;
       if (j < xn) {
         // a piece that another of its item and CTA comes before has no sums of its own
-        const int piece = xslot + (j >> halves), cta = px_cta(x_all, x.grid, piece);
-        if (piece == xslot || cta != px_cta(x_all, x.grid, piece - 1)) {
-          place = (xitem + cta) * PX_ROWS + xk + (halves ? (j & 1) * 128 : 0);
+        const int piece = xpiece + (j >> halves), cta = px_cta(x_all, x.grid, piece);
+        if (piece == xpiece || cta != px_cta(x_all, x.grid, piece - 1)) {
+          place = xrow + cta * PX_ROWS + (halves ? (j & 1) * 128 : 0);
           at = x.stats + (size_t)place * TA_STAT;
         }
       } else if (j < n) {
