@@ -221,32 +221,21 @@ __global__ void __launch_bounds__(PG_THREADS, 1) kv_reserve_kernel(const __grid_
   auto fresh = [&](const PageEntry& y) {
     return !s_bad[y.slot] && (y.e >= s_has[y.slot] || (y.shared && (!y.part || s_copy[y.slot] >= 0)));
   };
-  // Entries that go back are judged before anything is changed, too: a warp has 128 of each of four slots on their way at once.
-  // (96 samples forked, reserved and freed: 73.7 us, 71.6 without the look.)
-  for (int s0 = tid >> 5; s0 < g.slots; s0 += 4 * PG_WARPS) {
-    int at[4], end[4], most = 0;
+  // Entries that go back are judged before anything is changed, too: a warp has a slot's next 128 on their way at once.  (96 samples
+  // forked, reserved and freed: 74.0 us, 71.9 without the look; four slots a warp at once no faster.)
+#pragma unroll 1
+  for (int s = tid >> 5; s < g.slots; s += PG_WARPS) {
+    const int has = s_first[s] < 0 ? 0 : s_has[s];
+    const int32_t* row = g.table + (size_t)s * g.table_pages;
+#pragma unroll 1
+    for (int e = s_wants[s] + (tid & 31); e < has; e += 128) {
+      int id[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = s0 + i * PG_WARPS;
-      const bool looks = s < g.slots && s_first[s] >= 0;
-      at[i] = looks ? s_wants[s] : 0;
-      end[i] = looks ? s_has[s] : 0;
-      most = max(most, end[i] - at[i]);
-    }
-    for (int e0 = tid & 31; e0 < most; e0 += 128) {
-      int id[4][4];
+      for (int y = 0; y < 4; ++y) id[y] = e + 32 * y < has ? row[e + 32 * y] : 0;
+      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int e = at[i] + e0 + 32 * y;
-          id[i][y] = e < end[i] ? g.table[(size_t)(s0 + i * PG_WARPS) * g.table_pages + e] : 0;
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if ((unsigned)id[i][y] >= (unsigned)g.n_pages) s_bad[s0 + i * PG_WARPS] = 1;
+      for (int y = 0; y < 4; ++y) bad |= (unsigned)id[y] >= (unsigned)g.n_pages;
+      if (bad) s_bad[s] = 1;
     }
   }
   // half-filled pages that others name too
@@ -406,7 +395,9 @@ __device__ __forceinline__ void finish_compact(const PageCopyParams& p) {
 // ---- beginnings of pages (copies of a reserve): pieces of 16 bytes by threads.  Strided pieces of a few KB are
 // nothing for bulk copies (93 copies of 7 places in 64 layers: 61 us by threads, 77 by bulk copies of each head's).
 constexpr int PP_AHEAD = 8, PP_TILE = PC_THREADS * PP_AHEAD;   // pieces a thread has in flight; of a tile
-constexpr int PP_CTAS = 3;   // per SM (93 copies of 7 places in 64 layers, with the calls around them: 68.9 us, 4 86.5, 2 67.4)
+// CTAs an SM: three are the better for few copies, two for many, so it is the middle one.  (7 copies of 8 places in 36 layers, with the calls
+// around them: 2 22.1 us, 3 21.5; 93 copies of 7 places in 64 layers 2 70.9, 3 74.1, 4 90.9.)
+constexpr int PP_CTAS = 3;
 template <bool REST>
 __global__ void __launch_bounds__(PC_THREADS, PP_CTAS) kv_part_copy_kernel(const __grid_constant__ PageCopyParams p) {
   pdl_trigger();
