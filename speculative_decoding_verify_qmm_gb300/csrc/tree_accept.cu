@@ -605,7 +605,10 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_accept_kernel(const __grid
           cluster_sync();
           cut = s_tell[0];
         } else {
-          // Too many: the place is found bit by bit, by tokens, then by mass.  (A flat row: a pass per bit.)
+          // Too many: the place is found bit by bit, by tokens, then by mass, with a pass over the row and an exchange for each of 64 bits.  Right
+          // for any row, but slow.  (8 trees of 24 nodes, vocabulary 151936, logits of spread 2.5 at T = 0.75: top_p 0.8, which keeps some 1100,
+          // 84 us in all; 0.9, where some rows have more than 4096 candidates, 491; 0.95 644, with a draft's distribution 1000 to 2300; top_k 20000 and
+          // 0.95 959.)
           u64 lowest = 1;
           for (int by_mass = by_count ? 0 : 1; by_mass < (p.top_p < 1.f ? 2 : 1); ++by_mass) {
             const u64 floor_place = lowest;
@@ -773,8 +776,9 @@ static int tv_max_cluster() {
 }
 
 // CTAs a request: 16, for the shortest passes, while all requests are resident at once (two CTAs an SM), and 12 from there on, where fewer
-// meetings count for more.  (A row of 151936, 16 and 12: 1 request 24.8 us and 28.2, 9 requests 32.6 and 37.2, 16 from raw logits 102 and
-// 114; 24 134 and 122, 64 131 and 113.  8: 35, 40, 124, 167 and 144.)
+// meetings count for more.  (A row of 151936; 16, 12, 8 and 4: 1 request 23.8 us, 26.7, 34.9 and 90; 9 requests 35, 44, 47 and 127; 16 from
+// raw logits 90, 97, 106 and 193; 24 of 64 nodes 125, 127, 162 and 211, 64 of 16 nodes 225, 198, 257 and 267.)  The rule is made for large
+// vocabularies.  (Of 32000: 1 request 16.5, 17.0, 19.8 and 26.8, 64 130, 97, 85 and 79; of 1000: 14.4, 13.9, 13.9 and 13.9, 64 106, 73, 52 and 36.)
 static cudaError_t launch_tree_accept(const TreeAcceptParams& p, int B, cudaStream_t s) {
   const int most = tv_max_cluster(), C = B * 16 <= 2 * device_sm_count() || most < 12 ? most : 12;
   if (!(p.temperature > 0.f)) return launch_tree_accept_as<TV_GREEDY, false>(p, B, C, 0, s);

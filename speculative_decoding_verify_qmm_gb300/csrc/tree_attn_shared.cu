@@ -20,10 +20,16 @@
 
 namespace sv {
 
-// Cached tokens times key heads that requests need not read again, from which on two more launches pay (32 query and 8 key heads, apart and
-// together, us: 16 requests of a row over 1024 tokens 20.3 and 27.2, over 4096 37.3 and 32.5, over 16384 101 and 43; 4 of 8 rows over 8192
-// 31.6 and 42.2, over 16384 48.3 and 50.1, over 32768 81 and 71; 4-bit caches alike.  One key head: 16 of 8 rows over 32768 41 and 58).
+// Cached tokens times key heads that requests need not read again, from which on two more launches pay.  (8-bit, 32 query and 8 key heads,
+// apart and together, us: 16 requests of a row over 1024 tokens 25.0 and 31.2, over 2048 31.2 and 34.5, over 4096 (491,520) 45.2 and 37.3, over
+// 16384 119 and 47.5; 4 of 8 rows over 8192 35.3 and 41.4, over 16384 (393,216) 53.7 and 49.6, over 32768 94.6 and 76.2; other caches alike.
+// One key head: 16 of 8 rows over 32768 (491,520) 53.6 and 59.8.  So two launches pay from 250 to 400 thousand on with eight key heads, and not
+// yet at 490 thousand with one: the border is on the safe side, and leaves up to 8 us below it.)
 constexpr double PX_WORTH = 500000.0;
+// Of the plan's model, fitted to the times of such cases.  (PX_BEGIN 0 or 6: within 0.3 us in all of eight.  PX_PART 0: 16 x 1 row over 16384
+// tokens 54.5 us instead of 48.3, 48 x 2 over 5000 57.6 instead of 59.6; 1: 64 x 1 over 8016 117 instead of 106, 4 x 8 over 32768 71 instead of
+// 74.  PX_JOIN 0: 92.4 instead of 89.4 for 16 x 8 over 16384, 112 instead of 106 for 64 x 1; 1: 105 and 117, and 377 instead of 356 for 32 x 64
+// over 2048.)
 constexpr double PX_BEGIN = 3.0, PX_PART = 0.3, PX_JOIN = 0.3;
 constexpr int TJ_WARPS = 8, TJ_CTAS = 4;       // warps a CTA, CTAs an SM
 constexpr int TJ_AHEAD = 4;                    // parts of a row on their way at once
