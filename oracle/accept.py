@@ -18,7 +18,7 @@ rejection; the output is then an exact sample of the target at temperature T
   as probabilities already at the draft's temperature and is never rescaled.
 * Draft i (token d) is accepted iff u[i] < p_i[d] / q_i[d] (strict; u in
   [0, 1) makes the min(1, .) implicit).  q_i[d] == 0 gives an infinite ratio
-  and the draft is accepted.
+  and the draft is accepted, unless p_i[d] == 0 too: the target never emits it.
 * Exactly m + 1 uniforms per round: u[0..m-1] are the accept tests, u[m]
   drives the single final draw.
 * Final draw: the smallest k whose cumulative weight C_k (index order) exceeds
@@ -91,7 +91,7 @@ def sampled_accept_detail(logits, q, draft, temperature, u):
         p_i = target_probs(z[i], temperature)
         q_i = qf[i].astype(np.float64)
         d = draft[i]
-        r = np.inf if q_i[d] == 0.0 else p_i[d] / q_i[d]
+        r = 0.0 if p_i[d] == 0.0 else (np.inf if q_i[d] == 0.0 else p_i[d] / q_i[d])
         ratios.append(r)
         if float(u[i]) < r:
             tokens.append(d)
